@@ -432,6 +432,145 @@ pa_status pa_scatter_blocks(const void *staging_k, const void *staging_v, void *
                             void *v_cache, const int32_t *block_ids, int num_ids, int num_blocks,
                             size_t block_bytes, void *stream);
 
+/* ------------------------------------------------------------------------- *
+ * The 8-bit cache.  The pages have no counterpart: the same paged cache, half *
+ * the bytes of a 16-bit one, so half the bytes a decode has to read.          *
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Layout of kv_cache (K and V in one buffer, num_blocks blocks of pa_q8_block_bytes):
+ *     codes   e4m3 (8 bits: sign, 4 exponent bits, 3 mantissa bits; largest 448)
+ *             [num_kv_heads][K, V][block_size][head_dim]
+ *     scales  fp32 [num_kv_heads, rounded up to even][K, V] at pa_q8_scales_offset
+ *             bytes into the block, padded to 128 bytes
+ * A code stands for code * scale.  The scales travel with their block: pa_q8_copy_blocks
+ * (copy-on-write) and pa_q8_swap_blocks (preemption) move whole blocks.  The cache needs
+ * no initialisation: a block's scale is set when its first row is written.
+ * pa_q8_block_bytes / pa_q8_scales_offset: (size_t)-1 for sizes that are not built
+ * (head_dim 64 or 128, block_size 16 or 32).
+ */
+size_t pa_q8_block_bytes(int num_kv_heads, int head_dim, int block_size);
+size_t pa_q8_scales_offset(int num_kv_heads, int head_dim, int block_size);
+
+/*
+ * pa_q8_append -- write new tokens' K and V rows into the 8-bit cache.
+ *
+ * Sequence s appends n_s = query_start[s + 1] - query_start[s] rows, rows query_start[s]
+ * .. of k and v; they are its last n_s tokens: row i goes to position p =
+ * context_lens[s] - n_s + i (context_lens count them already, as for pa_decode), block
+ * block_tables[s][p / B], row p % B.  query_start NULL: one row per sequence, row s its
+ * newest token (num_tokens = num_seqs).  For every block that gets rows, and each of K
+ * and V of each kv head:
+ *     need  = the smallest power of two (2^-126 at least) with max |x| <= 448 * need over
+ *             the block's new rows (infinities and NaN left out)
+ *     scale = need if the block's row 0 is among them (the block starts anew: what its
+ *             other rows held no longer means anything), else max(scale, need)
+ *     code  = x / scale rounded to e4m3, to nearest even; NaN for infinities and NaN
+ * Where scale grew, the block's other rows become (code * old scale / scale), rounded
+ * again: exact but for values that fall below e4m3's normal range.  So a block filled
+ * row by row holds what it would hold if it had been written at once, to within that
+ * second rounding.  Rows that are not written and blocks whose scale stays are left as
+ * they were.
+ *
+ * No block may be written for two sequences in one call (apply the step's copy-on-write
+ * pairs first, pa_q8_copy_blocks).  Rows at negative positions, past the table's
+ * max_blocks_per_seq * block_size, of blocks outside [0, num_blocks), and rows of k and
+ * v from query_start[num_seqs] on (padding) are skipped; nothing is accessed outside the
+ * arguments.  Results do not depend on the order in which tokens arrive within a call.
+ *
+ *   k, v          device [num_tokens][num_kv_heads][head_dim], dtype `dtype`
+ *   kv_cache      device, 16-byte aligned, written
+ *   block_tables  device int32 [num_seqs][max_blocks_per_seq]
+ *   context_lens  device int32 [num_seqs];  query_start device int32 [num_seqs + 1],
+ *                 non-decreasing from 0, or NULL
+ * Errors: PA_ERR_INVALID (null or misaligned pointer, bad size, query_start NULL with
+ *   num_tokens != num_seqs), PA_ERR_UNSUPPORTED (head_dim, block_size or dtype not
+ *   built), PA_ERR_CUDA.  num_tokens = 0 or num_seqs = 0 is a no-op.
+ */
+pa_status pa_q8_append(const void *k, const void *v, void *kv_cache, const int32_t *block_tables,
+                       int max_blocks_per_seq, const int32_t *context_lens, const int32_t *query_start,
+                       int num_seqs, int num_tokens, int num_blocks, int num_kv_heads, int head_dim,
+                       int block_size, pa_dtype dtype, void *stream);
+
+/*
+ * pa_q8_decode -- pa_decode over the 8-bit cache.
+ *
+ * As pa_decode with partition_size 0, with K_t and V_t = code * scale of their block and
+ * kv head.  q and out are `dtype`; scores, softmax statistics and sums are fp32.  The
+ * codes enter the products exactly; queries and probabilities enter them in fp16 (fp32
+ * queries and outputs: two fp16 terms, about 22 bits).  Scales may be any finite,
+ * non-negative values, powers of two or not.  T = 0 yields a zero row; rows past T are
+ * never counted, whatever they hold; a table entry outside [0, num_blocks) reads zeros; a
+ * NaN among a sequence's codes makes the outputs that it enters NaN.  num_q_heads /
+ * num_kv_heads may be any size (16 query heads at a time share a read of the cache).
+ * Workspace: pa_q8_decode_workspace_size bytes, used as pa_decode's: calls that may
+ * overlap need one each, replays of a captured graph start clean.  Waits are bounded and
+ * reported as pa_decode's are (pa_device_errors).  Errors as pa_decode.
+ */
+pa_status pa_q8_decode(void *out, const void *q, const void *kv_cache, const int32_t *block_tables,
+                       int max_blocks_per_seq, const int32_t *context_lens, int num_seqs, int num_blocks,
+                       float scale, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                       pa_dtype dtype, void *workspace, size_t workspace_bytes, void *stream);
+size_t pa_q8_decode_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                   int block_size, int max_blocks_per_seq);
+
+/*
+ * pa_q8_copy_blocks / pa_q8_swap_blocks -- pa_copy_blocks and pa_swap_blocks for the
+ * 8-bit cache's single buffer: codes and scales of a block move together.  block_bytes =
+ * pa_q8_block_bytes.  Same rules and errors.
+ */
+pa_status pa_q8_copy_blocks(void *kv_cache, const int32_t *src_dst_pairs, int num_pairs, int num_blocks,
+                            size_t block_bytes, void *stream);
+pa_status pa_q8_swap_blocks(const void *src_cache, void *dst_cache, const int32_t *src_dst_pairs,
+                            int num_pairs, int src_num_blocks, int dst_num_blocks, size_t block_bytes,
+                            void *stream);
+
+/*
+ * pa_build_tables -- one allocator step of a batch on the GPU: block tables, lengths and
+ * slot map from request lengths, with no host round trip.
+ *
+ * The device counterpart of pa_alloc_free_seq and pa_alloc_append_n ([T] §2.2, §3.1) for
+ * batches whose blocks are not shared (no reference counts, no copy-on-write).  The pool
+ * is free_list[0 .. *num_free), popped from the end, as the host allocator's.  For
+ * request s with T = context_lens[s] tokens in ceil(T / B) blocks:
+ *   new_tokens[s] < 0   released: its blocks, in table order, go to the end of the free
+ *                       list; its length becomes 0.  All releases come before the
+ *                       first grant, in request order.
+ *   new_tokens[s] >= 0  granted when its row of the table can hold T + n tokens and,
+ *                       where it needs blocks, they and those wanted by the requests
+ *                       before it fit the pool, and its rows and those wanted before it
+ *                       fit num_slots: it takes the next blocks from the end of the free
+ *                       list, its length grows by n.  Otherwise refused: nothing of it
+ *                       changes.  (A request whose table row is too short counts
+ *                       nothing toward the ones after it; one refused for want of
+ *                       blocks or slots does: later requests are not served in its
+ *                       place, unless they need no block.)
+ * Outputs:
+ *   block_tables      entries of the granted requests' new blocks written; others left
+ *   context_lens_out  lengths after the step; may be context_lens
+ *   free_list         released blocks appended; *num_free_out its length after the
+ *                     step; may be num_free.  Entries past it are left as they were.
+ *   granted           n if granted, -1 if refused, 0 if released
+ *   query_start       int32 [num_seqs + 1]: first slot of each request's granted tokens
+ *                     (pa_q8_append's query_start)
+ *   slot_mapping      int64 [num_slots]: block * B + offset of each granted token, in
+ *                     request and position order (pa_reshape_and_cache's slots); -1
+ *                     behind the last (padding: those rows are skipped)
+ * Deterministic.  Lengths below 0 count as 0, *num_free is clamped to [0, num_blocks]; a
+ * free-list entry outside [0, num_blocks) is handed out as it is and gets slots -1 where
+ * it is negative; pushes past num_blocks are dropped.  Nothing is accessed outside the
+ * arguments.
+ *   free_list         device int32 [num_blocks]
+ * Errors: PA_ERR_INVALID (null or misaligned pointer, non-positive num_blocks,
+ *   block_size or max_blocks_per_seq, num_blocks or max_blocks_per_seq * block_size >=
+ *   2^31), PA_ERR_CUDA.  num_seqs = 0 still pads the slot map.
+ */
+pa_status pa_build_tables(int32_t *block_tables, int max_blocks_per_seq, int32_t *context_lens_out,
+                          const int32_t *context_lens, const int32_t *new_tokens, int num_seqs,
+                          int32_t *free_list, int num_blocks, int32_t *num_free_out,
+                          const int32_t *num_free, int block_size, int32_t *granted,
+                          int32_t *query_start, int64_t *slot_mapping, int num_slots, void *stream);
+
 /*
  * Host predicate of [K] "KV recompute threshold": fetching another engine's KV for
  * a prefix pays off only from threshold_tokens reusable tokens up (the article's

@@ -15,6 +15,9 @@ calls on tensors that are not CUDA tensors raise.
     pa_swap_blocks          block moves between the device pool and pinned host memory
     pa_gather_blocks /      pack blocks into a contiguous staging buffer and back
       pa_scatter_blocks       (the local halves of a KV transfer)
+    pa_q8_append /          the same cache in 8 bits (e4m3 codes, a scale per block and
+      pa_q8_decode            kv head): quantising append, and decode attention over it
+    pa_build_tables         block tables, lengths and slot maps grown and released on the GPU
     BlockAllocator          host ref-counted block allocator (pa_alloc_*)
 """
 from __future__ import annotations
@@ -659,6 +662,199 @@ def pa_scatter_blocks(staging_k, staging_v, k_cache, v_cache, block_ids, stream=
     _check(st, "pa_scatter_blocks")
 
 
+# ----------------------------------------------------------------------------
+# the 8-bit cache, and tables built on the GPU
+# ----------------------------------------------------------------------------
+def _device_of(*named):
+    """A context in which the tensors' device is the current one; the tensors must be
+    contiguous CUDA tensors of one device."""
+    import contextlib
+    import torch
+    dev = None
+    for name, t in named:
+        _cuda(t, name)
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the others on {dev}")
+    if dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
+def _want(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def pa_q8_block_bytes(num_kv_heads: int, head_dim: int, block_size: int) -> int:
+    """Bytes of one block of the 8-bit cache: codes of K and V, then the scales."""
+    n = _load().pa_q8_block_bytes(num_kv_heads, head_dim, block_size)
+    if n == ctypes.c_size_t(-1).value:
+        raise PagedKVError(PA_ERR_UNSUPPORTED, "pa_q8_block_bytes")
+    return n
+
+
+def alloc_q8_cache(num_blocks: int, num_kv_heads: int, head_dim: int, block_size: int, device="cuda",
+                   pin_memory: bool = False):
+    """A zeroed 8-bit cache, uint8 [num_blocks, block bytes] (device="cpu" with
+    pin_memory=True: a pool to swap to)."""
+    import torch
+    return torch.zeros(num_blocks, pa_q8_block_bytes(num_kv_heads, head_dim, block_size), dtype=torch.uint8,
+                       device=device, pin_memory=pin_memory)
+
+
+def q8_views(kv_cache, num_kv_heads: int, head_dim: int, block_size: int):
+    """(codes, scales) of an 8-bit cache as views of its memory: float8_e4m3fn
+    [num_blocks, Hkv, 2, B, d] and float32 [num_blocks, Hkv, 2], index 0 of the pair K
+    and 1 V; a code stands for code * scale."""
+    import torch
+    n = _load().pa_q8_scales_offset(num_kv_heads, head_dim, block_size)
+    _want(kv_cache.shape[1] == pa_q8_block_bytes(num_kv_heads, head_dim, block_size),
+          "kv_cache has another block size in bytes")
+    codes = kv_cache[:, :n].view(torch.float8_e4m3fn).unflatten(1, (num_kv_heads, 2, block_size, head_dim))
+    scales = kv_cache[:, n:n + num_kv_heads * 8].view(torch.float32).unflatten(1, (num_kv_heads, 2))
+    return codes, scales
+
+
+def _check_batch(kv_cache, block_tables, context_lens, num_kv_heads, head_dim, block_size):
+    import torch
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise TypeError("block_tables and context_lens must be int32")
+    if kv_cache.dtype != torch.uint8:
+        raise TypeError("kv_cache must be uint8")
+    _want(block_tables.dim() == 2 and context_lens.shape == block_tables.shape[:1],
+          "block_tables must be [S, W] and context_lens [S]")
+    _want(kv_cache.dim() == 2 and kv_cache.shape[1] == pa_q8_block_bytes(num_kv_heads, head_dim, block_size),
+          "kv_cache must be [num_blocks, pa_q8_block_bytes(...)]")
+
+
+def pa_q8_append(k, v, kv_cache, block_tables, context_lens, block_size: int, query_start=None, stream=None):
+    """Write new K and V rows ([N, Hkv, d]) into the 8-bit cache at the ends of their
+    sequences, raising a block's scale where a row needs it (see pa_q8_append in
+    include/pagedkv.h).  query_start int32 [S + 1]: first row of each sequence; None:
+    one row per sequence."""
+    import torch
+    _want(k.dim() == 3 and k.shape == v.shape, "k and v must be [N, Hkv, d] and alike")
+    if k.dtype != v.dtype:
+        raise TypeError("k and v must have one dtype")
+    n, hkv, d = k.shape
+    S, W = block_tables.shape
+    _check_batch(kv_cache, block_tables, context_lens, hkv, d, block_size)
+    named = [("k", k), ("v", v), ("kv_cache", kv_cache), ("block_tables", block_tables),
+             ("context_lens", context_lens)]
+    if query_start is not None:
+        if query_start.dtype != torch.int32:
+            raise TypeError("query_start must be int32")
+        _want(query_start.shape == (S + 1,), "query_start must be [S + 1]")
+        named.append(("query_start", query_start))
+    with _device_of(*named):
+        st = _load().pa_q8_append(k.data_ptr(), v.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(), W,
+                                  context_lens.data_ptr(),
+                                  query_start.data_ptr() if query_start is not None else None, S, n,
+                                  kv_cache.shape[0], hkv, d, block_size, _dtype_code(k), _stream(stream))
+    _check(st, "pa_q8_append")
+
+
+def pa_q8_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                                max_blocks_per_seq) -> int:
+    n = _load().pa_q8_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                                            max_blocks_per_seq)
+    if n == ctypes.c_size_t(-1).value:
+        raise PagedKVError(PA_ERR_INVALID, "pa_q8_decode_workspace_size")
+    return n
+
+
+def pa_q8_decode(out, q, kv_cache, block_tables, context_lens, scale: float, num_q_heads: int,
+                 num_kv_heads: int, head_dim: int, block_size: int, workspace=None, stream=None):
+    """out[S, Hq, d] <- decode attention over the 8-bit cache (see pa_q8_decode in
+    include/pagedkv.h); workspace: uint8 CUDA tensor or None (allocated here)."""
+    S, W = block_tables.shape
+    _check_batch(kv_cache, block_tables, context_lens, num_kv_heads, head_dim, block_size)
+    _want(q.shape == (S, num_q_heads, head_dim) and out.shape == q.shape, "q and out must be [S, Hq, d]")
+    if out.dtype != q.dtype:
+        raise TypeError("q and out must have one dtype")
+    named = [("out", out), ("q", q), ("kv_cache", kv_cache), ("block_tables", block_tables),
+             ("context_lens", context_lens)]
+    if workspace is not None:
+        named.append(("workspace", workspace))
+    with _device_of(*named):
+        if workspace is None:
+            workspace = _launch_scratch(pa_q8_decode_workspace_size(S, num_q_heads, num_kv_heads, head_dim,
+                                                                    block_size, W), q.device, stream)
+        st = _load().pa_q8_decode(out.data_ptr(), q.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(), W,
+                                  context_lens.data_ptr(), S, kv_cache.shape[0], float(scale), num_q_heads,
+                                  num_kv_heads, head_dim, block_size, _dtype_code(q), workspace.data_ptr(),
+                                  workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, "pa_q8_decode")
+    return out
+
+
+def pa_q8_copy_blocks(kv_cache, src_dst_pairs, stream=None):
+    """Block dst becomes a copy of block src, codes and scales, for every (src, dst) row of
+    the int32 [n, 2] pairs."""
+    import torch
+    if src_dst_pairs.dtype != torch.int32:
+        raise TypeError("src_dst_pairs must be int32")
+    n = src_dst_pairs.shape[0]
+    if n == 0:
+        return
+    with _device_of(("kv_cache", kv_cache), ("src_dst_pairs", src_dst_pairs)):
+        st = _load().pa_q8_copy_blocks(kv_cache.data_ptr(), src_dst_pairs.data_ptr(), n, kv_cache.shape[0],
+                                       _block_bytes(kv_cache), _stream(stream))
+    _check(st, "pa_q8_copy_blocks")
+
+
+def pa_q8_swap_blocks(src_cache, dst_cache, src_dst_pairs, stream=None):
+    """dst pool blocks <- src pool blocks, codes and scales, for each (src, dst) pair; pools
+    are 8-bit caches on the device or in pinned host memory (pairs likewise)."""
+    import torch
+    if src_dst_pairs.dtype != torch.int32:
+        raise TypeError("src_dst_pairs must be int32")
+    _want(_block_bytes(src_cache) == _block_bytes(dst_cache), "the pools have blocks of different sizes")
+    if src_dst_pairs.shape[0] == 0:
+        return
+    st = _load().pa_q8_swap_blocks(_dev_ptr(src_cache, "src_cache"), _dev_ptr(dst_cache, "dst_cache"),
+                                   _dev_ptr(src_dst_pairs, "src_dst_pairs"), int(src_dst_pairs.shape[0]),
+                                   int(src_cache.shape[0]), int(dst_cache.shape[0]), _block_bytes(src_cache),
+                                   _stream(stream))
+    _check(st, "pa_q8_swap_blocks")
+
+
+def pa_build_tables(block_tables, context_lens, new_tokens, free_list, num_free, block_size: int, slot_mapping,
+                    query_start, granted, context_lens_out=None, num_free_out=None, stream=None):
+    """One allocator step on the GPU (see pa_build_tables in include/pagedkv.h): releases
+    the requests with new_tokens < 0, grows the others; all int32 CUDA tensors but
+    slot_mapping (int64).  context_lens_out and num_free_out default to context_lens and
+    num_free, updated in place."""
+    import torch
+    if context_lens_out is None:
+        context_lens_out = context_lens
+    if num_free_out is None:
+        num_free_out = num_free
+    named = [("block_tables", block_tables), ("context_lens", context_lens), ("new_tokens", new_tokens),
+             ("free_list", free_list), ("num_free", num_free), ("query_start", query_start),
+             ("granted", granted), ("context_lens_out", context_lens_out), ("num_free_out", num_free_out)]
+    for name, t in named:
+        if t.dtype != torch.int32:
+            raise TypeError(f"{name} must be int32")
+    if slot_mapping.dtype != torch.int64:
+        raise TypeError("slot_mapping must be int64")
+    S, W = block_tables.shape
+    _want(context_lens.shape == (S,) and new_tokens.shape == (S,) and granted.shape == (S,) and
+          context_lens_out.shape == (S,), "context_lens, new_tokens, granted and context_lens_out must be [S]")
+    _want(query_start.shape == (S + 1,), "query_start must be [S + 1]")
+    _want(num_free.numel() == 1 and num_free_out.numel() == 1, "num_free and num_free_out hold one number")
+    _want(free_list.dim() == 1 and slot_mapping.dim() == 1, "free_list and slot_mapping must have one dimension")
+    with _device_of(*named, ("slot_mapping", slot_mapping)):
+        st = _load().pa_build_tables(block_tables.data_ptr(), W, context_lens_out.data_ptr(),
+                                     context_lens.data_ptr(), new_tokens.data_ptr(), S, free_list.data_ptr(),
+                                     free_list.shape[0], num_free_out.data_ptr(), num_free.data_ptr(), block_size,
+                                     granted.data_ptr(), query_start.data_ptr(), slot_mapping.data_ptr(),
+                                     slot_mapping.shape[0], _stream(stream))
+    _check(st, "pa_build_tables")
+
+
 def pa_kv_transfer_worthwhile(reusable_tokens: int, threshold_tokens: int = 64) -> bool:
     """Fetch another engine's KV for a prefix (True) or recompute it (False)."""
     return bool(_load().pa_kv_transfer_worthwhile(int(reusable_tokens), int(threshold_tokens)))
@@ -671,6 +867,8 @@ __all__ = ["pa_decode", "pa_decode_append", "pa_decode_plan_bytes", "pa_decode_p
            "share_groups", "share_saving", "share_pays", "SHARE_MIN_SAVING", "SHARE_MIN_BYTES",
            "pa_decode_noalloc", "pa_decode_workspace_size", "pa_decode_partition_size", "alloc_workspace",
            "pa_reshape_and_cache", "pa_copy_blocks", "pa_swap_blocks", "pa_gather_blocks",
-           "pa_scatter_blocks", "pa_kv_transfer_worthwhile", "pa_device_errors", "pa_set_wait_limit_ns",
+           "pa_scatter_blocks", "pa_q8_block_bytes", "alloc_q8_cache", "q8_views", "pa_q8_append", "pa_q8_decode",
+           "pa_q8_decode_workspace_size", "pa_q8_copy_blocks", "pa_q8_swap_blocks", "pa_build_tables",
+           "pa_kv_transfer_worthwhile", "pa_device_errors", "pa_set_wait_limit_ns",
            "PA_DEVERR_TIMEOUT_FULL", "PA_DEVERR_TIMEOUT_EMPTY", "PA_DEVERR_SHARE", "PA_WAIT_LIMIT_DEFAULT_NS", "pa_status_string",
            "BlockAllocator", "PagedKVError", "OutOfBlocks", "library_path"]

@@ -79,6 +79,17 @@ SIGNATURES = {
                                  c_void_p]),
     "pa_scatter_blocks": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_size_t,
                                   c_void_p]),
+    "pa_q8_block_bytes": (c_size_t, [c_int] * 3),
+    "pa_q8_scales_offset": (c_size_t, [c_int] * 3),
+    "pa_q8_append": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_int, c_int,
+                             c_int, c_int, c_int, c_int, c_int, c_void_p]),
+    "pa_q8_decode": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_int, c_int, c_float,
+                             c_int, c_int, c_int, c_int, c_int, c_void_p, c_size_t, c_void_p]),
+    "pa_q8_decode_workspace_size": (c_size_t, [c_int] * 6),
+    "pa_q8_copy_blocks": (c_int, [c_void_p, c_void_p, c_int, c_int, c_size_t, c_void_p]),
+    "pa_q8_swap_blocks": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_size_t, c_void_p]),
+    "pa_build_tables": (c_int, [c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_int, c_void_p,
+                                c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_int, c_void_p]),
     "pa_kv_transfer_worthwhile": (c_int, [ctypes.c_longlong, ctypes.c_longlong]),
 }
 

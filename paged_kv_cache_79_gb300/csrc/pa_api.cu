@@ -48,42 +48,7 @@ std::map<std::tuple<void *, int, size_t>, int> g_occupancy;
 std::map<std::pair<void *, int>, size_t> g_smem_limit;
 std::map<int, unsigned int *> g_err_ptr;
 
-unsigned int *device_error_word(int dev, cudaError_t *err)
-{
-    std::lock_guard<std::mutex> lk(g_mu);
-    auto it = g_err_ptr.find(dev);
-    if (it != g_err_ptr.end())
-        return it->second;
-    void *ptr = nullptr;
-    *err = cudaGetSymbolAddress(&ptr, g_device_errors);
-    if (*err != cudaSuccess)
-        return nullptr;
-    g_err_ptr[dev] = static_cast<unsigned int *>(ptr);
-    return static_cast<unsigned int *>(ptr);
-}
-
 // ---- tensor maps ---------------------------------------------------------------
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn()
-{
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-        cudaGetLastError();
-    });
-    return fn;
-}
-
 // Cache [num_blocks][B][Hkv][d] seen as 4-D: (element within a 128-byte row of d,
 // token slot, 128-byte row of d, kv head).  One box = one kv head of one block:
 // its B token rows, each d / (128 bytes) rows of 128 bytes, landing chunk-major
@@ -149,11 +114,7 @@ int resolve_partition(int B, int max_blocks, int part)
     return part >= max_ctx ? (int)(((max_ctx + B - 1) / B) * B) : part;
 }
 
-// Balanced split workspace: one merge counter per CTA, then partial rows for
-// 2 slots x 16 query heads per CTA.
 size_t balanced_ctas(int sms) { return (size_t)kMaxCtasPerSm * (size_t)sms; }
-size_t balanced_rows(int sms) { return 2 * balanced_ctas(sms) * kHeadsPerItem; }
-size_t counter_bytes(int sms) { return (balanced_ctas(sms) * 8 + 255) & ~size_t(255); }
 
 // Tags of the merge counters: a process starts from a random value, so that a
 // value a workspace kept from another process is unlikely to match.
@@ -161,14 +122,6 @@ std::atomic<unsigned int> g_epoch{std::random_device{}()};
 
 // Limit of the device-side waits of decode launches (pa_set_wait_limit_ns).
 std::atomic<unsigned long long> g_wait_limit_ns{kWaitTimeoutNs};
-
-unsigned int next_epoch()
-{
-    unsigned int e = ++g_epoch;
-    if (e == 0)  // a zeroed counter must never match
-        e = ++g_epoch;
-    return e;
-}
 
 int current_sms()
 {
@@ -181,6 +134,49 @@ int current_sms()
 }
 
 }  // namespace
+
+unsigned int *device_error_word(int dev, cudaError_t *err)
+{
+    std::lock_guard<std::mutex> lk(g_mu);
+    auto it = g_err_ptr.find(dev);
+    if (it != g_err_ptr.end())
+        return it->second;
+    void *ptr = nullptr;
+    *err = cudaGetSymbolAddress(&ptr, g_device_errors);
+    if (*err != cudaSuccess)
+        return nullptr;
+    g_err_ptr[dev] = static_cast<unsigned int *>(ptr);
+    return static_cast<unsigned int *>(ptr);
+}
+
+EncodeTiledFn encode_fn()
+{
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                             &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+        cudaGetLastError();
+    });
+    return fn;
+}
+
+// Balanced split workspace: one merge counter per CTA, then partial rows for
+// 2 slots x 16 query heads per CTA.
+size_t balanced_rows(int sms) { return 2 * balanced_ctas(sms) * kHeadsPerItem; }
+size_t counter_bytes(int sms) { return (balanced_ctas(sms) * 8 + 255) & ~size_t(255); }
+
+unsigned int next_epoch()
+{
+    unsigned int e = ++g_epoch;
+    if (e == 0)  // a zeroed counter must never match
+        e = ++g_epoch;
+    return e;
+}
 
 void note_cuda_error(cudaError_t e) { cuda_fail(e); }
 
@@ -966,7 +962,9 @@ pa_status pa_copy_blocks(void *k_cache, void *v_cache, const int32_t *src_dst_pa
     return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
 
-namespace {
+}  // extern "C"
+
+namespace pagedkv {
 // A pointer the kernels may dereference: device memory, managed memory, or pinned
 // host memory whose device address is the host address (unified addressing).
 bool device_accessible(const void *ptr)
@@ -980,7 +978,9 @@ bool device_accessible(const void *ptr)
         return true;
     return at.type == cudaMemoryTypeHost && at.devicePointer == ptr;
 }
+}  // namespace pagedkv
 
+namespace {
 bool all_accessible(std::initializer_list<const void *> ptrs)
 {
     for (const void *p : ptrs)
@@ -989,6 +989,8 @@ bool all_accessible(std::initializer_list<const void *> ptrs)
     return true;
 }
 }  // namespace
+
+extern "C" {
 
 pa_status pa_swap_blocks(const void *src_k, const void *src_v, void *dst_k, void *dst_v,
                          const int32_t *src_dst_pairs, int num_pairs, int src_num_blocks,

@@ -120,7 +120,7 @@ cudaError_t launch_move_blocks(const void *src_k, const void *src_v, void *dst_k
     attr[0].val.programmaticStreamSerializationAllowed = 1;
 #endif
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)num, 2, z);
+    cfg.gridDim = dim3((unsigned)num, src_v ? 2 : 1, z);
     cfg.blockDim = dim3(kCopyThreads);
     cfg.stream = stream;
     cfg.attrs = attr;

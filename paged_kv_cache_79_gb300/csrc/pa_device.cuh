@@ -182,6 +182,35 @@ __device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t &r0, uint3
                  : "r"(addr));
 }
 
+// Two 16 x 16 matrices of 8-bit elements, transposed: lanes 0..15 give the 16-byte rows
+// of the first, lanes 16..31 of the second.  Lane l gets, of each matrix, elements
+// (rows 4 (l % 4) .. + 3) of column l / 4 (first register) and of column l / 4 + 8.
+__device__ __forceinline__ void ldsm_b8_x2_trans(uint32_t addr, uint32_t &r0, uint32_t &r1,
+                                                 uint32_t &r2, uint32_t &r3)
+{
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+                 : "r"(addr)
+                 : "memory");
+}
+
+// Two e4m3 codes (the low 16 bits of x) as two fp16 values: exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x)
+{
+    uint32_t d;
+    const unsigned short h = (unsigned short)x;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(h));
+    return d;
+}
+
+// Two fp32 values as two e4m3 codes (lo in the low byte), to nearest even.
+__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi)
+{
+    unsigned short d;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
 // 16-byte asynchronous copy global -> shared (per thread), its group commit, and
 // the wait for all of this thread's outstanding groups.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src)

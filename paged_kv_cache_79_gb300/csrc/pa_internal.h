@@ -147,6 +147,69 @@ struct DecodeLaunch {
     int sm_count;
 };
 
+// ---- the 8-bit cache -----------------------------------------------------------
+// One block of the cache: the e4m3 codes [Hkv][K, V][B][d], then the scales, fp32
+// [Hkv, rounded up to even][K, V], padded to 128 bytes.  A kv head's K and V codes of a
+// block are adjacent, so one copy brings both as one contiguous run (a 16-bit block's
+// [B][Hkv][d] order would cut the 8-bit tile into pieces of d bytes); two heads' scales
+// are the 16 bytes a bulk copy moves at least.
+struct Q8Layout {
+    size_t scales;  // byte offset of the scales in a block
+    size_t bytes;   // bytes per block
+};
+inline Q8Layout q8_layout(int block_size, int num_kv_heads, int head_dim)
+{
+    Q8Layout l;
+    l.scales = (size_t)num_kv_heads * 2 * block_size * head_dim;
+    l.bytes = l.scales + (((size_t)((num_kv_heads + 1) & ~1) * 8 + 127) & ~size_t(127));
+    return l;
+}
+
+struct Q8Params {
+    const uint8_t *scales;  // the first block's scales
+    size_t block_bytes;
+};
+
+struct Q8Launch {
+    DecodeParams p;
+    Q8Params q8;
+    CUtensorMap map;
+    int head_dim;
+    int block_size;
+    int sm_count;
+};
+
+cudaError_t launch_q8_decode_f32(const Q8Launch &L, cudaStream_t stream);
+cudaError_t launch_q8_decode_f16(const Q8Launch &L, cudaStream_t stream);
+cudaError_t launch_q8_decode_bf16(const Q8Launch &L, cudaStream_t stream);
+
+struct Q8AppendParams {
+    const void *k, *v;            // [num_tokens][Hkv][d]
+    uint8_t *cache;
+    const int32_t *block_tables;
+    const int32_t *context_lens;
+    const int32_t *query_start;   // null: token s is sequence s's newest
+    size_t block_bytes, scales;   // Q8Layout
+    int max_blocks, num_seqs, num_tokens, num_blocks, num_kv_heads, block_size;
+};
+cudaError_t launch_q8_append(const Q8AppendParams &p, int head_dim, pa_dtype dtype,
+                             cudaStream_t stream);
+
+struct TablesParams {
+    int32_t *block_tables;
+    int32_t *context_lens_out;
+    const int32_t *context_lens;
+    const int32_t *new_tokens;
+    int32_t *free_list;
+    int32_t *num_free_out;
+    const int32_t *num_free;
+    int32_t *granted;
+    int32_t *query_start;
+    int64_t *slots;
+    int max_blocks, num_seqs, num_blocks, block_size, num_slots;
+};
+cudaError_t launch_build_tables(const TablesParams &p, cudaStream_t stream);
+
 // Persistent grid (CTAs) of a balanced-split launch of the plain decode with a
 // plan; 0 if the configuration cannot launch.
 int plan_grid_f32(const DecodeLaunch &L);
@@ -172,6 +235,27 @@ int cached_occupancy(void *kernel, int device, size_t smem, size_t max_smem);
 // Number of SMs of `device` (cached).
 int sm_count(int device);
 
+// The device error word of `device` (null and *err set on failure).
+unsigned int *device_error_word(int device, cudaError_t *err);
+
+// A new tag for the merge counters of a balanced-split launch.
+unsigned int next_epoch();
+
+// Balanced-split workspace on a device of `sms` SMs: partial rows, counter bytes.
+size_t balanced_rows(int sms);
+size_t counter_bytes(int sms);
+
+// cuTensorMapEncodeTiled, or null when the driver does not have it.
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn();
+
+// Whether the kernels may dereference `ptr`: device or managed memory, or pinned host
+// memory whose device address is the host address.
+bool device_accessible(const void *ptr);
+
 // Record `e` as this thread's last CUDA error (read by pa_last_cuda_error) and
 // clear the runtime's sticky launch error.
 void note_cuda_error(cudaError_t e);
@@ -179,6 +263,7 @@ void note_cuda_error(cudaError_t e);
 cudaError_t launch_reshape_and_cache(const void *k, const void *v, void *k_cache, void *v_cache,
                                      const int64_t *slots, int num_tokens, size_t row_bytes,
                                      long long num_slots, cudaStream_t stream);
+// src_v null: one pool each side (a null dst_v with it).
 cudaError_t launch_move_blocks(const void *src_k, const void *src_v, void *dst_k, void *dst_v,
                                const int32_t *src_ids, int src_stride, const int32_t *dst_ids,
                                int dst_stride, int num, int src_blocks, int dst_blocks,

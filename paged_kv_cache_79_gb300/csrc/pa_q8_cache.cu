@@ -1,0 +1,306 @@
+// Append to the 8-bit paged cache: new K and V rows become e4m3 codes under the scale
+// of their (block, kv head).
+//
+// For every block that gets new rows, and each of K and V of each kv head:
+//     need = the smallest power of two with max |x| <= 448 need over the new rows
+//     s    = need when the block's first row is among them (the block starts anew),
+//            else max(old s, need)
+//     code = e4m3(x / s); where s grew, the block's other rows become
+//            e4m3(code * old / s)
+// 448 is e4m3's largest value.  With powers of two, x / s is exact, so a code is its
+// value rounded once, and rounding again loses nothing but what falls below e4m3's
+// smallest normal number: e4m3 keeps its 4 significant bits over 2^-6 .. 448 wherever
+// the maximum lies, so a scale that fits the maximum exactly would gain nothing.
+//
+// One warp has one (block, kv head, K or V): its rows' maximum, the old scale, the codes
+// and, where the scale grew, the rest of the tile are read and written by that warp
+// alone, so nothing is exchanged.  Bound by the bytes of the rows and codes for prompts,
+// by two dependent reads (lengths and table, then rows and scale) for single tokens.
+#include "pa_device.cuh"
+#include "pa_internal.h"
+
+namespace pagedkv {
+
+namespace {
+
+constexpr int kAppendWarps = 8;
+constexpr int kChunk = 32;  // tokens a CTA looks through for the first rows of blocks
+
+// A run of new rows in one block.
+struct Run {
+    int token;  // first row of k and v
+    int rows;
+    int block;
+    int off;    // first row in the block
+};
+
+// The run that starts at token t, or rows = 0 when none does.
+__device__ __forceinline__ Run run_at(const Q8AppendParams &p, int t, int s, int start, int n)
+{
+    Run r = {t, 0, 0, 0};
+    const long long pos = (long long)p.context_lens[s] - n + (t - start);
+    if (pos < 0 || pos >= (long long)p.max_blocks * p.block_size)
+        return r;
+    r.off = (int)(pos % p.block_size);
+    if (r.off != 0 && t != start)
+        return r;  // a row behind the first of its block's
+    r.block = p.block_tables[(size_t)s * p.max_blocks + pos / p.block_size];
+    if (r.block < 0 || r.block >= p.num_blocks)
+        return r;
+    r.rows = min(min(p.block_size - r.off, n - (t - start)), p.num_tokens - t);
+    return r;
+}
+
+// The sequence of each lane's token t0 + lane: the last s with query_start[s] <= t
+// (num_seqs: a row past the last sequence; -1: before the first).  A warp looks through
+// 32 entries at a time, so 1024 sequences take two dependent reads.
+__device__ __forceinline__ int find_sequence(const int32_t *qs, int num_seqs, int t0, int lane)
+{
+    int lo = -1, hi = num_seqs;  // the answer for t0 lies in lo .. hi
+    while (lo < hi) {
+        const int step = (hi - lo + 31) / 32;
+        const int i = lo + (lane + 1) * step;
+        const bool le = i <= hi && qs[i] <= t0;
+        const int c = __popc(__ballot_sync(0xffffffffu, le));
+        lo += c * step;
+        hi = min(hi, lo + step - 1);
+    }
+    int s = lo;
+    for (int base = lo + 1; base <= num_seqs; base += 32) {
+        const int e = base + lane <= num_seqs ? qs[base + lane] : 0x7fffffff;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            s += __shfl_sync(0xffffffffu, e, i) <= t0 + lane ? 1 : 0;
+        if (__shfl_sync(0xffffffffu, e, 31) > t0 + 31)
+            break;
+    }
+    return s;
+}
+
+__device__ __forceinline__ void widen(float (&x)[8], const uint4 &w, const __half *)
+{
+    const __half2 *h = reinterpret_cast<const __half2 *>(&w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(h[i]);
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
+__device__ __forceinline__ void widen(float (&x)[8], const uint4 &w, const __nv_bfloat16 *)
+{
+    const uint32_t *u = reinterpret_cast<const uint32_t *>(&w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(u[i] << 16);
+        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void widen(float (&x)[4], const uint4 &w, const float *)
+{
+    x[0] = __uint_as_float(w.x);
+    x[1] = __uint_as_float(w.y);
+    x[2] = __uint_as_float(w.z);
+    x[3] = __uint_as_float(w.w);
+}
+
+// |x| for the maximum: infinities and NaN do not count (their codes are NaN).
+__device__ __forceinline__ float finite_abs(float x)
+{
+    const float a = fabsf(x);
+    return a <= 3.402823466e38f ? a : 0.f;
+}
+
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d)
+{
+    const float nan = __uint_as_float(0x7fffffffu);
+    a = fabsf(a) < INFINITY ? a : nan;
+    b = fabsf(b) < INFINITY ? b : nan;
+    c = fabsf(c) < INFINITY ? c : nan;
+    d = fabsf(d) < INFINITY ? d : nan;
+    return dev::f32x2_to_e4m3x2(a, b) | (dev::f32x2_to_e4m3x2(c, d) << 16);
+}
+
+// x / s: a product with the exact inverse for the powers of two that this kernel
+// writes, a division for other scales that a caller put into the cache.
+struct Divide {
+    float s, inv;
+    bool pow2;
+    __device__ explicit Divide(float s_)
+    {
+        s = s_;
+        inv = 1.f / s_;
+        pow2 = (__float_as_uint(s_) & 0x7fffffu) == 0;
+    }
+    __device__ float operator()(float x) const { return pow2 ? x * inv : x / s; }
+};
+
+// Four codes times `ratio`, rounded again.
+__device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio)
+{
+    const uint32_t h0 = dev::e4m3x2_to_f16x2(w & 0xffffu), h1 = dev::e4m3x2_to_f16x2(w >> 16);
+    const float2 f0 = __half22float2(*reinterpret_cast<const __half2 *>(&h0));
+    const float2 f1 = __half22float2(*reinterpret_cast<const __half2 *>(&h1));
+    return encode4(f0.x * ratio, f0.y * ratio, f1.x * ratio, f1.y * ratio);
+}
+
+template <typename T, int D, int BS>
+__global__ void __launch_bounds__(32 * kAppendWarps)
+    q8_append_kernel(const __grid_constant__ Q8AppendParams p)
+{
+    constexpr int E = 16 / (int)sizeof(T);    // elements of a 16-byte load
+    constexpr int LR = D / E;                 // lanes on one row
+    constexpr int RP = 32 / LR;               // rows a warp loads at once
+    constexpr int kPasses = BS / RP;
+    constexpr int kHold = kPasses < 16 ? kPasses : 16;  // loads kept in registers
+    __shared__ Run runs[kChunk];
+    __shared__ int num_runs;
+    dev::grid_dependency_wait();  // lengths, tables, rows and cache may come from the previous kernel
+    dev::grid_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == 0) {
+        const int t0 = blockIdx.x * kChunk, t = t0 + lane;
+        Run r = {t, 0, 0, 0};
+        if (p.query_start) {
+            const int s = find_sequence(p.query_start, p.num_seqs, t0, lane);
+            if (t < p.num_tokens && s >= 0 && s < p.num_seqs) {
+                const int start = p.query_start[s];
+                r = run_at(p, t, s, start, p.query_start[s + 1] - start);
+            }
+        } else if (t < p.num_tokens && t < p.num_seqs) {
+            r = run_at(p, t, t, t, 1);
+        }
+        const unsigned has = __ballot_sync(0xffffffffu, r.rows > 0);
+        if (r.rows > 0)
+            runs[__popc(has & ((1u << lane) - 1u))] = r;
+        if (lane == 0)
+            num_runs = __popc(has);
+    }
+    __syncthreads();
+    const int tiles = 2 * p.num_kv_heads;  // (kv head, K or V)
+    const int tasks = num_runs * tiles;
+    for (int task = blockIdx.y * kAppendWarps + warp; task < tasks; task += gridDim.y * kAppendWarps) {
+        const Run r = runs[task / tiles];
+        const int tile = task % tiles;
+        const int h = tile >> 1;
+        const T *src = reinterpret_cast<const T *>((tile & 1) ? p.v : p.k) +
+                       ((size_t)r.token * p.num_kv_heads + h) * D + (lane % LR) * E;
+        const size_t row_stride = (size_t)p.num_kv_heads * D;
+        uint8_t *const block = p.cache + (size_t)r.block * p.block_bytes;
+        uint8_t *const codes = block + (size_t)tile * (BS * D);
+        float *const scale = reinterpret_cast<float *>(block + p.scales) + tile;
+        const float old = r.off == 0 ? 0.f : *scale;
+
+        uint4 w[kHold];
+        float top = 0.f;
+        float x[E];
+#pragma unroll
+        for (int i = 0; i < kHold; ++i) {
+            const int row = i * RP + lane / LR;
+            w[i] = row < r.rows ? __ldg(reinterpret_cast<const uint4 *>(src + row * row_stride))
+                                : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kHold; ++i) {
+            widen(x, w[i], src);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                top = fmaxf(top, finite_abs(x[e]));
+        }
+        // (rows past what the registers hold are read twice: fp32, 128 dims, 32-row blocks)
+        for (int i = kHold; i < kPasses && i * RP < r.rows; ++i) {
+            const int row = i * RP + lane / LR;
+            if (row < r.rows) {
+                widen(x, __ldg(reinterpret_cast<const uint4 *>(src + row * row_stride)), src);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    top = fmaxf(top, finite_abs(x[e]));
+            }
+        }
+        top = dev::warp_max(top);
+        // 448 = 1.75 * 2^8: the exponent of top / 448, one more where top's mantissa
+        // passes 1.75's; at least the smallest normal scale
+        const int e2 = max((int)((__float_as_uint(top) + 0x1fffffu) >> 23) - 8, 1);
+        const float need = __uint_as_float((uint32_t)e2 << 23);
+        const float s = fmaxf(old, need);
+        const Divide div(s);
+        auto put = [&](int i, const uint4 &v) {
+            const int row = i * RP + lane / LR;
+            if (row >= r.rows)
+                return;
+            widen(x, v, src);
+            uint8_t *dst = codes + (size_t)(r.off + row) * D + (lane % LR) * E;
+            const uint32_t c0 = encode4(div(x[0]), div(x[1]), div(x[2]), div(x[3]));
+            if constexpr (E == 8) {
+                const uint32_t c1 = encode4(div(x[4]), div(x[5]), div(x[6]), div(x[7]));
+                *reinterpret_cast<uint2 *>(dst) = make_uint2(c0, c1);
+            } else {
+                *reinterpret_cast<uint32_t *>(dst) = c0;
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < kHold; ++i)
+            put(i, w[i]);
+        for (int i = kHold; i < kPasses && i * RP < r.rows; ++i) {
+            const int row = i * RP + lane / LR;
+            put(i, row < r.rows ? __ldg(reinterpret_cast<const uint4 *>(src + row * row_stride))
+                                : make_uint4(0, 0, 0, 0));
+        }
+        if (r.off != 0 && s > old) {
+            const float ratio = old / s;
+            for (int v = lane; v < BS * D / 16; v += 32) {
+                const int row = v * 16 / D;
+                if (row >= r.off && row < r.off + r.rows)
+                    continue;
+                uint4 q = reinterpret_cast<const uint4 *>(codes)[v];
+                q.x = rescale4(q.x, ratio);
+                q.y = rescale4(q.y, ratio);
+                q.z = rescale4(q.z, ratio);
+                q.w = rescale4(q.w, ratio);
+                reinterpret_cast<uint4 *>(codes)[v] = q;
+            }
+        }
+        if (lane == 0 && (r.off == 0 || s > old))
+            *scale = s;
+    }
+}
+
+template <typename T, int D, int BS>
+cudaError_t launch(const Q8AppendParams &p, cudaStream_t stream)
+{
+    // CTAs over the chunks, then over a chunk's tiles: one tile per warp for the number
+    // of blocks a chunk can be expected to touch
+    const long long chunks = (p.num_tokens + kChunk - 1) / kChunk;
+    const long long runs = p.query_start ? (p.num_tokens + BS - 1) / BS + p.num_seqs : p.num_tokens;
+    const long long per_chunk = ((runs < p.num_tokens ? runs : p.num_tokens) + chunks - 1) / chunks;
+    const long long y = (per_chunk * 2 * p.num_kv_heads + kAppendWarps - 1) / kAppendWarps;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)chunks, (unsigned)(y < 65535 ? y : 65535));
+    cfg.blockDim = dim3(32 * kAppendWarps);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, q8_append_kernel<T, D, BS>, p);
+}
+
+template <typename T>
+cudaError_t dispatch(const Q8AppendParams &p, int head_dim, cudaStream_t stream)
+{
+    if (head_dim == 128)
+        return p.block_size == 16 ? launch<T, 128, 16>(p, stream) : launch<T, 128, 32>(p, stream);
+    return p.block_size == 16 ? launch<T, 64, 16>(p, stream) : launch<T, 64, 32>(p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_q8_append(const Q8AppendParams &p, int head_dim, pa_dtype dtype, cudaStream_t stream)
+{
+    return dtype == PA_F32   ? dispatch<float>(p, head_dim, stream)
+           : dtype == PA_F16 ? dispatch<__half>(p, head_dim, stream)
+                             : dispatch<__nv_bfloat16>(p, head_dim, stream);
+}
+
+}  // namespace pagedkv

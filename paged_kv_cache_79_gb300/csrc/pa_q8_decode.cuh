@@ -1,0 +1,674 @@
+// Decode attention over the 8-bit paged cache (sm_103a).
+//
+// The cache holds e4m3 codes and one fp32 scale per (block, kv head) for K and one
+// for V (layout: pa_internal.h, q8_layout).  With ks, vs the scales of token t's
+// block, the kernel computes
+//     s_t = scale * ks * dot(q, K8_t),   out = sum_t exp(s_t - m) vs V8_t / sum_t exp(s_t - m)
+// The schedule is pa_decode's balanced split, and the walk over the stream of
+// (sequence, kv head, head group) units, the work items, the merge of the four
+// consumer warps and of split units are its code (pa_decode.cuh); the producer and the
+// consumers are this file's.
+//
+// What bounds it: the bytes of the codes, half of a 16-bit cache's; at G = 8 heads per
+// kv head that is 8 multiply-adds per byte, far below the tensor pipes' rate.
+//
+// Conversions.  Every e4m3 value is an fp16 value, so K8 and V8 are widened to fp16
+// exactly (cvt.f16x2.e4m3x2, two codes at a time) and both products run on
+// mma.sync.m16n8k16 with fp16 operands and fp32 accumulators.  What is rounded:
+//   q    each row is multiplied by a power of two that brings its largest element into
+//        [2^10, 2^11), then rounded to fp16.  fp16 queries lose nothing (elements more
+//        than 2^24 below the largest aside), bf16 ones neither (8 significant bits);
+//        fp32 ones are split into two fp16 terms, 22 significant bits.
+//   p    exp2(s - ref), at most 2 (ref follows the maximum), enters as 2^14 p: the fp16
+//        rounding is at most 2^-11 of the value down to p = 2^-28.  fp32 outputs take p
+//        as two fp16 terms.  The sum of p is kept in fp32 from the unrounded values.
+// Scores, sums, running maxima and outputs are fp32; fp32 outputs also add each
+// stage's products to the running output with an fp32 add, since the tensor pipe's own
+// accumulation truncates.
+//
+// Scales.  ks multiplies the fp32 scores.  vs multiplies p before its rounding, divided
+// by the largest vs the warp has met in the item (vref), so that 2^14 p vs / vref stays in
+// fp16's range whatever the scales; a larger vs rescales the accumulator once.
+//
+// Layout of the products (16 tokens at a time).  S^T[token x row] = K Q^T: row r of the
+// A tile is token 4 (r / 2) + r % 2 for r < 8 and that plus 2 for r >= 8, and the k order
+// gives lane t of a row's four lanes the row's bytes [t D / 4, (t + 1) D / 4): a lane's
+// share of a K row is one or two 16-byte shared loads, each word four consecutive k.
+// O^T[dim x row] += V^T P^T: ldmatrix's 8-bit transposing form returns, per lane, four
+// consecutive tokens of one dim; the token order above makes its low and high halves
+// the A fragment's k columns that the score fragment's rows stand for, so P^T needs only
+// a movmatrix transpose per 8 x 8 half, as in the 16-bit kernel.
+#pragma once
+
+#include "pa_decode.cuh"
+
+namespace pagedkv {
+
+#ifndef PA_Q8_STAGE_TOKENS
+#define PA_Q8_STAGE_TOKENS 64  // tokens per ring stage
+#endif
+#ifndef PA_Q8_RING_BYTES
+#define PA_Q8_RING_BYTES 65536  // shared memory of the stage ring
+#endif
+
+template <int D, int BS>
+struct Cfg8 {
+    static constexpr int kTile = BS * D;          // K (or V) codes of one (block, kv head)
+    static constexpr int kRecord = 2 * kTile;     // K tile, then V tile
+    static constexpr int kStageTokens = PA_Q8_STAGE_TOKENS;
+    static constexpr int kBPS = kStageTokens / BS;
+    static constexpr int kStageBytes = kBPS * kRecord;
+    static constexpr int kStagesRaw = (PA_Q8_RING_BYTES / kStageBytes) / kConsumerWarps * kConsumerWarps;
+    static constexpr int kStages = kStagesRaw < kConsumerWarps ? kConsumerWarps : kStagesRaw;
+    static_assert(kStageTokens % BS == 0 && 32 % kBPS == 0, "a stage is a whole number of blocks");
+    static_assert(kTile % 1024 == 0, "tiles start on the swizzle's 1024-byte period");
+};
+
+// Byte offset, in a tile as the 128-byte-swizzled copy leaves it, of 16-byte unit u of
+// token `tok`'s D codes: 128-byte row tok * D / 128, units swizzled by the row's number.
+template <int D>
+__device__ __forceinline__ uint32_t tile_unit(int tok, int u)
+{
+    const int row = D == 128 ? tok : tok >> 1;
+    const int unit = D == 128 ? u : ((tok & 1) * 4 + u);
+    return (uint32_t)(row * 128 + ((unit ^ (row & 7)) << 4));
+}
+
+// Shared memory: as make_layout, with 16 bytes of scales per block of a stage in the
+// place of the fused append's rows.
+__host__ __device__ inline SmemLayout make_layout8(int stages, int stage_bytes, int bps, int rows, int D,
+                                                   int elem_bytes)
+{
+    SmemLayout L;
+    uint32_t o = (uint32_t)stages * (uint32_t)stage_bytes;
+    L.acc = o;
+    o += (uint32_t)(kConsumerWarps * rows * (D + kAccPad) * 4);
+    L.ml = o;
+    o += kConsumerWarps * kHeadsPerItem * 2 * 4;
+    o = (o + 127u) & ~127u;
+    L.pfx = o;
+    L.items = o;
+    o += kItemSlots * 64u;
+    L.q = o;
+    o += (uint32_t)(kItemSlots * (rows <= kNarrowRows ? kNarrowRows : kHeadsPerItem) * D * elem_bytes);
+    L.newrow = o;  // the scales
+    o += (uint32_t)(stages * bps * 16);
+    L.newinfo = o;
+    o = (o + 15u) & ~15u;
+    L.bars = o;
+    o += (2u * (uint32_t)stages + 2u * kItemSlots + 1u) * 8u;
+    o = (o + 15u) & ~15u;
+    L.flag = o;
+    o += 16u + 4u * kConsumerWarps;
+    o = (o + 15u) & ~15u;
+    L.blk = o;
+    o += 32u * 4u;
+    L.total = o + 1024u;
+    return L;
+}
+
+// ---------------------------------------------------------------------------
+// Producer warp: as pa_decode's, with one tiled copy per block (K and V tiles of a kv
+// head are adjacent) and one 16-byte copy of its scales.
+// ---------------------------------------------------------------------------
+template <typename T, int D, int BS, int NT>
+struct Producer8 {
+    using C = Cfg8<D, BS>;
+    const DecodeParams &p;
+    const Q8Params &q8;
+    const CUtensorMap *map;
+    const CtaState &c;
+    int lane;
+    uint32_t g;  // stages issued
+    uint32_t n;  // items published
+    bool failed;
+
+    __device__ Producer8(const DecodeParams &p_, const Q8Params &q8_, const CUtensorMap *map_,
+                         const CtaState &c_, int lane_)
+        : p(p_), q8(q8_), map(map_), c(c_), lane(lane_), g(0), n(0), failed(false)
+    {
+        if (lane == 0)
+            dev::tma_prefetch_desc(map);
+    }
+
+    __device__ bool wait_slot(uint64_t *bar, uint32_t parity)
+    {
+        const int r = dev::mbar_wait_abortable(dev::smem_addr(bar), parity, p.wait_ns, c.abort);
+        if (r == 0)
+            raise_error(p, c.abort, PA_DEVERR_TIMEOUT_EMPTY);
+        return r == 1;
+    }
+
+    __device__ bool emit(const Item &it)
+    {
+        constexpr uint32_t kQSlotBytes = NT * 8 * D * sizeof(T);
+        const uint32_t slot = n % kItemSlots;
+        int ok = 1;
+        if (lane == 0) {
+            ok = wait_slot(&c.item_empty[slot], ((n / kItemSlots) & 1u) ^ 1u);
+            if (ok) {
+                c.items[slot] = it;
+                const uint32_t bytes = (uint32_t)it.rows * D * sizeof(T);
+                const uint32_t fb = dev::smem_addr(&c.item_full[slot]);
+                dev::mbar_arrive_expect_tx(fb, bytes);
+                dev::bulk_load(dev::smem_addr(c.qslots + slot * kQSlotBytes),
+                               reinterpret_cast<const T *>(p.q) +
+                                   ((size_t)it.seq * p.num_q_heads + it.qrow0) * D,
+                               bytes, fb);
+            }
+        }
+        if (!__shfl_sync(0xffffffffu, ok, 0)) {
+            failed = true;
+            return false;
+        }
+        ++n;
+        const int32_t *row = p.block_tables + (size_t)it.tseq * p.max_blocks;
+        for (int jb = it.j0; jb < it.j1; jb += 32) {
+            const int j = jb + lane;
+            c.blk[lane] = (j < it.j1) ? row[j] : -1;  // one coalesced read per 32 blocks
+            __syncwarp();
+            uint32_t issued = 0;
+            ok = 1;
+            if (lane == 0)
+                ok = fill_window(it, min(32, it.j1 - jb), issued);
+            g += __shfl_sync(0xffffffffu, issued, 0);
+            if (!__shfl_sync(0xffffffffu, ok, 0)) {
+                failed = true;
+                return false;
+            }
+        }
+        return true;
+    }
+
+    // Lane 0: the stages of one window of cnt blocks (ids in c.blk).
+    __device__ int fill_window(const Item &it, int cnt, uint32_t &issued)
+    {
+        uint32_t gg = g;
+        for (int i = 0; i < cnt; i += C::kBPS, ++gg) {
+            const int nbs = min(C::kBPS, cnt - i);  // blocks in this stage
+            const uint32_t st = gg % C::kStages;
+            if (!wait_slot(&c.empty[st], ((gg / C::kStages) & 1u) ^ 1u)) {
+                issued = gg - g;
+                return 0;
+            }
+            const uint32_t fb = dev::smem_addr(&c.full[st]);
+            uint8_t *const sc = c.newrow + (size_t)st * C::kBPS * 16;
+            uint32_t bytes = (uint32_t)nbs * C::kRecord;
+#pragma unroll
+            for (int b = 0; b < C::kBPS; ++b) {
+                if (b < nbs) {
+                    const int id = c.blk[i + b];
+                    if (id >= 0 && id < p.num_blocks)
+                        bytes += 16;
+                    else  // an entry outside the pool reads zeros, scales too
+                        *reinterpret_cast<uint4 *>(sc + b * 16) = make_uint4(0, 0, 0, 0);
+                }
+            }
+            dev::mbar_arrive_expect_tx(fb, bytes);
+            const uint32_t dst = dev::smem_addr(c.ring + (size_t)st * C::kStageBytes);
+#pragma unroll
+            for (int b = 0; b < C::kBPS; ++b) {
+                if (b < nbs) {
+                    const int id = c.blk[i + b];
+                    const bool in = id >= 0 && id < p.num_blocks;
+                    dev::tma_load_4d(dst + (uint32_t)b * C::kRecord, map, 0, 0, it.kvh, in ? id : -1, fb);
+                    if (in)
+                        dev::bulk_load(dev::smem_addr(sc + b * 16),
+                                       q8.scales + (size_t)id * q8.block_bytes + (size_t)(it.kvh >> 1) * 16,
+                                       16, fb);
+                }
+            }
+        }
+        issued = gg - g;
+        return 1;
+    }
+
+    // End of the walk: as Producer::finish (every copy in flight lands before the warp
+    // exits, each wait with the full bound).
+    __device__ void finish()
+    {
+        if (lane != 0)
+            return;
+        for (uint32_t k = n > kItemSlots ? n - kItemSlots : 0; k < n; ++k)
+            dev::mbar_wait(dev::smem_addr(&c.item_full[k % kItemSlots]), (k / kItemSlots) & 1u,
+                           kWaitTimeoutNs);
+        if (!failed) {
+            const uint32_t slot = n % kItemSlots;
+            if (wait_slot(&c.item_empty[slot], ((n / kItemSlots) & 1u) ^ 1u)) {
+                c.items[slot].seq = -1;
+                dev::mbar_arrive(dev::smem_addr(&c.item_full[slot]));
+            } else {
+                failed = true;
+            }
+        }
+        for (uint32_t q = g > C::kStages ? g - C::kStages : 0; q < g; ++q)
+            dev::mbar_wait(dev::smem_addr(&c.full[q % C::kStages]), (q / C::kStages) & 1u, kWaitTimeoutNs);
+    }
+};
+
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// N consecutive elements, 16 bytes at a time, as fp32.
+template <typename T, int N>
+__device__ __forceinline__ void load_row(float (&x)[N], const T *src)
+{
+    constexpr int E = 16 / (int)sizeof(T);
+#pragma unroll
+    for (int i = 0; i < N / E; ++i) {
+        const uint4 w = reinterpret_cast<const uint4 *>(src)[i];
+        const T *e = reinterpret_cast<const T *>(&w);
+#pragma unroll
+        for (int k = 0; k < E; ++k)
+            x[i * E + k] = to_float(e[k]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// One item on one consumer warp (its share of the item's stages).  NT: 8-row groups of
+// query rows.  Ends with the warp's partial rows in its merge area.
+// ---------------------------------------------------------------------------
+template <typename T, int D, int BS, int NT>
+__device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaState &c, const Item &it,
+                                              uint32_t slot, uint32_t &g, int warp, int lane, int rows_cap)
+{
+    using C = Cfg8<D, BS>;
+    constexpr bool kSplit = sizeof(T) == 4;  // two fp16 terms for q and p
+    constexpr int QT = kSplit ? 2 : 1;
+    constexpr int TS = C::kStageTokens;
+    constexpr int MT = TS / 16;   // 16-token tiles of a stage
+    constexpr int KS = D / 16;    // k-steps of K Q^T = words of a lane's share of a K row
+    constexpr int DM = D / 16;    // 16-dim tiles of O^T
+    constexpr int SA = D + kAccPad;
+    constexpr uint32_t kQSlotBytes = NT * 8 * D * sizeof(T);
+    constexpr float kUp = 16384.f;  // 2^14: p's factor in the products
+    const int q4 = lane & 3;       // fragment columns: query rows 8 nt + 2 q4, + 1
+    const int r8 = lane >> 2;      // fragment row
+    const int tok0 = 4 * (r8 >> 1) + (r8 & 1);  // this lane's tokens of a tile: tok0, tok0 + 2
+
+    // Q^T as the B operand, and the factor each row's scores take
+    uint32_t qb[NT][QT][KS][2];
+    float fa[NT], fb[NT];
+    {
+        uint32_t all = (uint32_t)(it.seq ^ it.kvh ^ it.hg ^ it.len ^ it.j0 ^ it.j1 ^ it.qrow0 ^ it.rows ^
+                                  it.partial ^ it.prow0 ^ it.tseq ^ it.packed ^ it.c_first ^ it.nparts) ^
+                       it.total_lo ^ it.total_hi;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float x[D / 4];
+            const T *src = reinterpret_cast<const T *>(c.qslots + slot * kQSlotBytes) +
+                           (size_t)(nt * 8 + r8) * D + q4 * (D / 4);
+            load_row<T, D / 4>(x, src);
+            const bool live = nt * 8 + r8 < it.rows;
+            float top = 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 4; ++i) {
+                x[i] = live ? x[i] : 0.f;
+                top = fmaxf(top, fabsf(x[i]));
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // 2^(10 - floor(log2 top)) and its inverse, by exponent bits
+            const int e = min(max((int)(__float_as_uint(top) >> 23), 11), 254);
+            const float up = __uint_as_float((uint32_t)(264 - e) << 23);
+            const float down = top == 0.f ? 1.f : __uint_as_float((uint32_t)(e - 10) << 23);
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float y0 = x[4 * ks + 2 * h] * up, y1 = x[4 * ks + 2 * h + 1] * up;
+                    const uint32_t hi = dev::Mma<__half>::pack(y0, y1);
+                    qb[nt][0][ks][h] = hi;
+                    all ^= hi;
+                    if constexpr (kSplit) {
+                        const __half2 hh = *reinterpret_cast<const __half2 *>(&hi);
+                        qb[nt][1][ks][h] =
+                            dev::Mma<__half>::pack(y0 - __low2float(hh), y1 - __high2float(hh));
+                    }
+                }
+            }
+            fa[nt] = __shfl_sync(0xffffffffu, down, 8 * q4) * p.scale_log2;
+            fb[nt] = __shfl_sync(0xffffffffu, down, 8 * q4 + 4) * p.scale_log2;
+        }
+        // every read of the slot has completed before it is handed back
+        all = __reduce_xor_sync(0xffffffffu, all);
+        if (lane == 0)
+            dev::settle_loads(&c.sink[warp], all);
+        __syncwarp();
+        if (lane == 0)
+            dev::mbar_arrive(dev::smem_addr(&c.item_empty[slot]));
+    }
+
+    float o[NT][DM][4];
+    float ma[NT], mb[NT], la[NT], lb[NT];  // reference and sum of rows 2 q4, 2 q4 + 1
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        ma[nt] = mb[nt] = -INFINITY;
+        la[nt] = lb[nt] = 0.f;
+#pragma unroll
+        for (int i = 0; i < DM; ++i)
+            o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
+    }
+    float vref = FLT_MIN;  // largest vs so far (its inverse is finite, also for scales of 0)
+    const int rot = it.rot();
+    for (int j = it.j0; j < it.j1; j += C::kBPS, ++g) {
+        if (((j - it.j0) / C::kBPS + rot) % kConsumerWarps != warp)
+            continue;
+        const uint32_t st = g % C::kStages;
+        if (!warp_wait(p, c, &c.full[st], (g / C::kStages) & 1u))
+            return false;
+        const int nbs = min(C::kBPS, it.j1 - j);  // blocks in this stage
+        const int valid = min(nbs * BS, it.len - j * BS);
+        const uint8_t *stage = c.ring + (size_t)st * C::kStageBytes;
+        float kscale[C::kBPS], vscale[C::kBPS];
+        float vmax = vref;
+#pragma unroll
+        for (int b = 0; b < C::kBPS; ++b) {
+            const float2 s2 = reinterpret_cast<const float2 *>(c.newrow)[(st * C::kBPS + b) * 2 + (it.kvh & 1)];
+            kscale[b] = s2.x;
+            vscale[b] = b < nbs ? s2.y : 0.f;
+            vmax = fmaxf(vmax, vscale[b]);
+        }
+
+        // S^T = K Q^T
+        float s[MT][NT][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const uint8_t *kt = stage + (mt * 16 / BS) * C::kRecord;
+            const int tk = mt * 16 % BS + tok0;
+            uint32_t w0[KS], w1[KS];
+#pragma unroll
+            for (int u = 0; u < D / 64; ++u) {
+                const int unit = q4 * (D / 64) + u;
+                *reinterpret_cast<uint4 *>(&w0[4 * u]) =
+                    *reinterpret_cast<const uint4 *>(kt + tile_unit<D>(tk, unit));
+                *reinterpret_cast<uint4 *>(&w1[4 * u]) =
+                    *reinterpret_cast<const uint4 *>(kt + tile_unit<D>(tk + 2, unit));
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                const uint32_t a[4] = {dev::e4m3x2_to_f16x2(w0[ks] & 0xffffu), dev::e4m3x2_to_f16x2(w1[ks] & 0xffffu),
+                                       dev::e4m3x2_to_f16x2(w0[ks] >> 16), dev::e4m3x2_to_f16x2(w1[ks] >> 16)};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int t = 0; t < QT; ++t)
+                        dev::Mma<__half>::run(s[mt][nt], a, qb[nt][t][ks][0], qb[nt][t][ks][1]);
+            }
+        }
+
+        // scale, mask, maximum; a new reference where a score passes the old by more
+        // than 1
+        bool raise = vmax > vref;
+        float xa[NT], xb[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float mxa = -INFINITY, mxb = -INFINITY;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                const float ksc = kscale[mt * 16 / BS];
+                const float ga = fa[nt] * ksc, gb = fb[nt] * ksc;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const bool ok = mt * 16 + tok0 + 2 * h < valid;
+                    s[mt][nt][2 * h] = ok ? s[mt][nt][2 * h] * ga : -INFINITY;
+                    s[mt][nt][2 * h + 1] = ok ? s[mt][nt][2 * h + 1] * gb : -INFINITY;
+                    mxa = fmaxf(mxa, s[mt][nt][2 * h]);
+                    mxb = fmaxf(mxb, s[mt][nt][2 * h + 1]);
+                }
+            }
+#pragma unroll
+            for (int o_ = 4; o_ < 32; o_ <<= 1) {
+                mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, o_));
+                mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, o_));
+            }
+            xa[nt] = mxa;
+            xb[nt] = mxb;
+            raise |= mxa > ma[nt] + 1.f || mxb > mb[nt] + 1.f;
+        }
+        if (__any_sync(0xffffffffu, raise)) {
+            const float cv = vref / vmax;
+            vref = vmax;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float na = fmaxf(ma[nt], xa[nt]), nb = fmaxf(mb[nt], xb[nt]);
+                // (no finite score yet: nothing to rescale)
+                const float ca = ma[nt] == -INFINITY ? 0.f : exp2f(ma[nt] - na);
+                const float cb = mb[nt] == -INFINITY ? 0.f : exp2f(mb[nt] - nb);
+                ma[nt] = na;
+                mb[nt] = nb;
+                la[nt] *= ca;
+                lb[nt] *= cb;
+#pragma unroll
+                for (int i = 0; i < DM; ++i) {
+                    o[nt][i][0] *= ca * cv;
+                    o[nt][i][1] *= cb * cv;
+                    o[nt][i][2] *= ca * cv;
+                    o[nt][i][3] *= cb * cv;
+                }
+            }
+        }
+        const float vinv = 1.f / vref;
+
+        // P^T as the B operand: exp2, times 2^14 vs / vref, rounded, transposed
+        uint32_t pb[MT][NT][QT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const float na = ma[nt] == -INFINITY ? 0.f : ma[nt], nb = mb[nt] == -INFINITY ? 0.f : mb[nt];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                const float vs = vscale[mt * 16 / BS] * vinv * kUp;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float ea = exp2f(s[mt][nt][2 * h] - na), eb = exp2f(s[mt][nt][2 * h + 1] - nb);
+                    la[nt] += ea;
+                    lb[nt] += eb;
+                    const float ya = ea * vs, yb = eb * vs;
+                    const uint32_t hi = dev::Mma<__half>::pack(ya, yb);
+                    pb[mt][nt][0][h] = dev::movmatrix_trans(hi);
+                    if constexpr (kSplit) {
+                        const __half2 hh = *reinterpret_cast<const __half2 *>(&hi);
+                        pb[mt][nt][1][h] = dev::movmatrix_trans(
+                            dev::Mma<__half>::pack(ya - __low2float(hh), yb - __high2float(hh)));
+                    }
+                }
+            }
+        }
+
+        // O^T += V^T P^T, 32 dims (two 16 x 16 matrices of codes) at a time
+        const bool partial = valid < TS;
+#pragma unroll
+        for (int dp = 0; dp < DM / 2; ++dp) {
+            float loc[NT][2][4];
+            if constexpr (kSplit) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        loc[nt][0][e] = loc[nt][1][e] = 0.f;
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                const uint8_t *vt = stage + (mt * 16 / BS) * C::kRecord + C::kTile;
+                uint32_t v[4];
+                dev::ldsm_b8_x2_trans(
+                    dev::smem_addr(vt + tile_unit<D>(mt * 16 % BS + (lane & 15), 2 * dp + (lane >> 4))), v[0], v[1],
+                    v[2], v[3]);
+                if (partial) {
+                    // rows past the context may hold anything (NaN): zero their codes
+                    const int left = min(max(valid - mt * 16 - 4 * q4, 0), 4);
+                    const uint32_t keep = left == 4 ? 0xffffffffu : (1u << (8 * left)) - 1u;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        v[e] &= keep;
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t a[4] = {dev::e4m3x2_to_f16x2(v[2 * h] & 0xffffu),
+                                           dev::e4m3x2_to_f16x2(v[2 * h + 1] & 0xffffu),
+                                           dev::e4m3x2_to_f16x2(v[2 * h] >> 16),
+                                           dev::e4m3x2_to_f16x2(v[2 * h + 1] >> 16)};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int t = 0; t < QT; ++t) {
+                            if constexpr (kSplit)
+                                dev::Mma<__half>::run(loc[nt][h], a, pb[mt][nt][t][0], pb[mt][nt][t][1]);
+                            else
+                                dev::Mma<__half>::run(o[nt][2 * dp + h], a, pb[mt][nt][t][0], pb[mt][nt][t][1]);
+                        }
+                }
+            }
+            if constexpr (kSplit) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            o[nt][2 * dp + h][e] += loc[nt][h][e];
+            }
+        }
+        __syncwarp();
+        if (lane == 0)
+            dev::mbar_arrive(dev::smem_addr(&c.empty[st]));
+    }
+
+    // partial rows of this warp
+    float *mine = c.macc + warp * rows_cap * SA;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        float sa = la[nt], sb = lb[nt];
+#pragma unroll
+        for (int o_ = 4; o_ < 32; o_ <<= 1) {
+            sa += __shfl_xor_sync(0xffffffffu, sa, o_);
+            sb += __shfl_xor_sync(0xffffffffu, sb, o_);
+        }
+        const int ra = nt * 8 + 2 * q4, rb = ra + 1;
+        if (ra < it.rows) {
+#pragma unroll
+            for (int dm = 0; dm < DM; ++dm) {
+                mine[ra * SA + dm * 16 + r8] = o[nt][dm][0] * (1.f / kUp) * vref;
+                mine[ra * SA + dm * 16 + r8 + 8] = o[nt][dm][2] * (1.f / kUp) * vref;
+            }
+        }
+        if (rb < it.rows) {
+#pragma unroll
+            for (int dm = 0; dm < DM; ++dm) {
+                mine[rb * SA + dm * 16 + r8] = o[nt][dm][1] * (1.f / kUp) * vref;
+                mine[rb * SA + dm * 16 + r8 + 8] = o[nt][dm][3] * (1.f / kUp) * vref;
+            }
+        }
+        if (r8 == 0) {
+            // a NaN score makes the sum and every output NaN; the merge takes such a
+            // row with a sum of 1, so that the NaN outputs, not the sum, carry it on
+            const bool na = sa != sa, nb = sb != sb;
+            c.mml[(warp * kHeadsPerItem + ra) * 2] =
+                ra < it.rows && (na || sa > 0.f) ? (na ? 0.f : ma[nt]) : -INFINITY;
+            c.mml[(warp * kHeadsPerItem + ra) * 2 + 1] = na ? 1.f : sa;
+            c.mml[(warp * kHeadsPerItem + rb) * 2] =
+                rb < it.rows && (nb || sb > 0.f) ? (nb ? 0.f : mb[nt]) : -INFINITY;
+            c.mml[(warp * kHeadsPerItem + rb) * 2 + 1] = nb ? 1.f : sb;
+        }
+    }
+    return true;
+}
+
+// (fp32 with 16 rows needs more registers than two CTAs per SM leave it)
+template <typename T, int D, int BS, int NT>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 && NT == 2 ? 1 : 2)
+    pa_q8_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ Q8Params q8,
+                        const __grid_constant__ CUtensorMap map)
+{
+    using C = Cfg8<D, BS>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem =
+        reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int rows_cap = item_rows_cap(p);
+    const SmemLayout lay = make_layout8(C::kStages, C::kStageBytes, C::kBPS, rows_cap, D, sizeof(T));
+    const CtaState c = cta_state(smem, lay, C::kStages);
+    init_cta(p, c, C::kStages);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    if (warp == kConsumerWarps) {
+        Producer8<T, D, BS, NT> pr(p, q8, &map, c, lane);
+        walk_balanced<kModePlain>(p, BS, C::kBPS, pr, lane);
+        pr.finish();
+        return;
+    }
+    uint32_t g = 0;    // stages consumed (same count in every warp)
+    uint32_t sph = 0;  // consumer barrier phase
+    for (uint32_t n = 0;; ++n) {
+        const uint32_t slot = n % kItemSlots;
+        if (!warp_wait(p, c, &c.item_full[slot], (n / kItemSlots) & 1u))
+            break;
+        const Item it = load_item(&c.items[slot]);
+        if (it.seq < 0)
+            break;
+        if (!consume_item8<T, D, BS, NT>(p, c, it, slot, g, warp, lane, rows_cap))
+            break;
+        if (threadIdx.x == 0)
+            probe_split_last(p, it, c);
+        if (!consumer_sync(p, c, sph))
+            break;
+        finalize_item<T, D, false>(p, it, c.macc, c.mml, rows_cap, threadIdx.x, nullptr, *c.merge == 2);
+        if (!finish_item<T, D, false>(p, it, c, sph, warp, lane, nullptr))
+            break;
+        if (*c.abort)
+            break;
+    }
+}
+
+template <typename T, int D, int BS>
+cudaError_t launch_q8_impl(const Q8Launch &L, cudaStream_t stream)
+{
+    using C = Cfg8<D, BS>;
+    const DecodeParams &p = L.p;
+    void *kern = p.group <= kNarrowRows ? reinterpret_cast<void *>(&pa_q8_decode_kernel<T, D, BS, 1>)
+                                        : reinterpret_cast<void *>(&pa_q8_decode_kernel<T, D, BS, 2>);
+    const size_t smem =
+        make_layout8(C::kStages, C::kStageBytes, C::kBPS, item_rows_cap(p), D, sizeof(T)).total;
+    const size_t smem_max =
+        make_layout8(C::kStages, C::kStageBytes, C::kBPS, kHeadsPerItem, D, sizeof(T)).total;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    const int per_sm = cached_occupancy(kern, dev, smem, smem_max);
+    if (per_sm <= 0)
+        return cudaErrorInvalidConfiguration;
+    void *args[] = {const_cast<DecodeParams *>(&L.p), const_cast<Q8Params *>(&L.q8),
+                    const_cast<CUtensorMap *>(&L.map)};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(min(per_sm, kMaxCtasPerSm) * L.sm_count));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelExC(&cfg, kern, args);
+}
+
+template <typename T>
+cudaError_t launch_q8_dispatch(const Q8Launch &L, cudaStream_t stream)
+{
+    if (L.head_dim == 128 && L.block_size == 16)
+        return launch_q8_impl<T, 128, 16>(L, stream);
+    if (L.head_dim == 128 && L.block_size == 32)
+        return launch_q8_impl<T, 128, 32>(L, stream);
+    if (L.head_dim == 64 && L.block_size == 16)
+        return launch_q8_impl<T, 64, 16>(L, stream);
+    if (L.head_dim == 64 && L.block_size == 32)
+        return launch_q8_impl<T, 64, 32>(L, stream);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace pagedkv
