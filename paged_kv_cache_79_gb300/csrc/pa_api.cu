@@ -197,7 +197,7 @@ int sm_count(int device)
     return n;
 }
 
-int cached_occupancy(void *kernel, int device, size_t smem, size_t max_smem)
+int cached_occupancy(void *kernel, int device, size_t smem, size_t max_smem, int threads)
 {
     std::lock_guard<std::mutex> lk(g_mu);
     const auto key = std::make_tuple(kernel, device, smem);
@@ -226,7 +226,7 @@ int cached_occupancy(void *kernel, int device, size_t smem, size_t max_smem)
         g_smem_limit[lkey] = max_smem;
     }
     int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kThreads, smem) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess) {
         cudaGetLastError();
         return 0;
     }

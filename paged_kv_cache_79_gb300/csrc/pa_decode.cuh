@@ -2517,8 +2517,6 @@ inline size_t smem_bytes_for(int rows, int pfx_rows = 0)
     return make_layout(C::kStages, C::kStageBytes, rows, D, sizeof(T), pfx_rows).total;
 }
 
-int cached_occupancy(void *kernel, int device, size_t smem, size_t max_smem);
-
 // The persistent grid of a launch: its kernel instance's resident CTAs per SM (at
 // most kMaxCtasPerSm) times the SMs, or L.grid if that is smaller; 0 if the
 // configuration cannot launch.  pa_decode_plan sizes its plan with the same count.

@@ -230,7 +230,7 @@ size_t decode_smem_bytes_bf16(int head_dim, int block_size, int group);
 
 // Resident CTAs per SM of `kernel` with `smem` dynamic shared memory on `device`
 // (raises the kernel's dynamic shared-memory limit to `max_smem` first).  Cached.
-int cached_occupancy(void *kernel, int device, size_t smem, size_t max_smem);
+int cached_occupancy(void *kernel, int device, size_t smem, size_t max_smem, int threads = kThreads);
 
 // Number of SMs of `device` (cached).
 int sm_count(int device);

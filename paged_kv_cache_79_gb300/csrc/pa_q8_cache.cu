@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
 #pragma unroll
         for (int i = 0; i < kHold; ++i) {
             const int row = i * RP + lane / LR;
-            w[i] = row < r.rows ? __ldg(reinterpret_cast<const uint4 *>(src + row * row_stride))
+            w[i] = row < r.rows ? __ldcg(reinterpret_cast<const uint4 *>(src + row * row_stride))
                                 : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
         for (int i = kHold; i < kPasses && i * RP < r.rows; ++i) {
             const int row = i * RP + lane / LR;
             if (row < r.rows) {
-                widen(x, __ldg(reinterpret_cast<const uint4 *>(src + row * row_stride)), src);
+                widen(x, __ldcg(reinterpret_cast<const uint4 *>(src + row * row_stride)), src);
 #pragma unroll
                 for (int e = 0; e < E; ++e)
                     top = fmaxf(top, finite_abs(x[e]));
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
             put(i, w[i]);
         for (int i = kHold; i < kPasses && i * RP < r.rows; ++i) {
             const int row = i * RP + lane / LR;
-            put(i, row < r.rows ? __ldg(reinterpret_cast<const uint4 *>(src + row * row_stride))
+            put(i, row < r.rows ? __ldcg(reinterpret_cast<const uint4 *>(src + row * row_stride))
                                 : make_uint4(0, 0, 0, 0));
         }
         if (r.off != 0 && s > old) {

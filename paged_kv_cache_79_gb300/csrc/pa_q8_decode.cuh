@@ -40,26 +40,38 @@
 // a movmatrix transpose per 8 x 8 half, as in the 16-bit kernel.
 #pragma once
 
+// Stream positions charged per unit for its fixed cost, in this kernel's ring stages
+// (8 KB at 128 dims, half of pa_decode's): 64 ragged sequences of 64 / 8 heads took
+// 162, 153, 146 and 146 us with 4, 8, 12 and 16.
+#ifndef PA_UNIT_COST
+#define PA_UNIT_COST 12
+#endif
 #include "pa_decode.cuh"
 
 namespace pagedkv {
 
 #ifndef PA_Q8_STAGE_TOKENS
-#define PA_Q8_STAGE_TOKENS 64  // tokens per ring stage
+#define PA_Q8_STAGE_TOKENS 32  // tokens per ring stage
 #endif
 #ifndef PA_Q8_RING_BYTES
-#define PA_Q8_RING_BYTES 65536  // shared memory of the stage ring
+#define PA_Q8_RING_BYTES 81920  // shared memory of the stage ring (two CTAs per SM)
 #endif
 
-template <int D, int BS>
+// NT: groups of 8 query rows an item may have (1 or 2).  The ring is as large as the
+// residency leaves room for beside the merge rows: two CTAs per SM, or one for fp32 with
+// 16 rows, whose registers allow no more (ragged batch of 13 heads per kv head, 128
+// dims: 43 us on two CTAs with 64 KB each, 48 on one with 80 KB).
+template <typename T, int D, int BS, int NT>
 struct Cfg8 {
+    static constexpr int kCtas = sizeof(T) == 4 && NT == 2 ? 1 : 2;
+    static constexpr int kRing = kCtas == 1 ? 131072 : NT == 2 && D == 128 ? 65536 : PA_Q8_RING_BYTES;
     static constexpr int kTile = BS * D;          // K (or V) codes of one (block, kv head)
     static constexpr int kRecord = 2 * kTile;     // K tile, then V tile
     static constexpr int kStageTokens = PA_Q8_STAGE_TOKENS;
     static constexpr int kBPS = kStageTokens / BS;
     static constexpr int kStageBytes = kBPS * kRecord;
-    static constexpr int kStagesRaw = (PA_Q8_RING_BYTES / kStageBytes) / kConsumerWarps * kConsumerWarps;
-    static constexpr int kStages = kStagesRaw < kConsumerWarps ? kConsumerWarps : kStagesRaw;
+    static constexpr int kStages = kRing / kStageBytes;
+    static_assert(kStages >= kConsumerWarps, "a stage per consumer warp");
     static_assert(kStageTokens % BS == 0 && 32 % kBPS == 0, "a stage is a whole number of blocks");
     static_assert(kTile % 1024 == 0, "tiles start on the swizzle's 1024-byte period");
 };
@@ -74,7 +86,9 @@ __device__ __forceinline__ uint32_t tile_unit(int tok, int u)
     return (uint32_t)(row * 128 + ((unit ^ (row & 7)) << 4));
 }
 
-// Shared memory: as make_layout, with 16 bytes of scales per block of a stage in the
+constexpr int kThreads8 = kThreads + 32;  // one warp more than pa_decode: the scales'
+
+// Shared memory: as make_layout, with 8 bytes of scales per block of a stage in the
 // place of the fused append's rows.
 __host__ __device__ inline SmemLayout make_layout8(int stages, int stage_bytes, int bps, int rows, int D,
                                                    int elem_bytes)
@@ -92,11 +106,11 @@ __host__ __device__ inline SmemLayout make_layout8(int stages, int stage_bytes, 
     L.q = o;
     o += (uint32_t)(kItemSlots * (rows <= kNarrowRows ? kNarrowRows : kHeadsPerItem) * D * elem_bytes);
     L.newrow = o;  // the scales
-    o += (uint32_t)(stages * bps * 16);
+    o += (uint32_t)(stages * bps * 8);
     L.newinfo = o;
     o = (o + 15u) & ~15u;
-    L.bars = o;
-    o += (2u * (uint32_t)stages + 2u * kItemSlots + 1u) * 8u;
+    L.bars = o;  // as make_layout's, then one per stage for its scales
+    o += (3u * (uint32_t)stages + 2u * kItemSlots + 1u) * 8u;
     o = (o + 15u) & ~15u;
     L.flag = o;
     o += 16u + 4u * kConsumerWarps;
@@ -109,13 +123,12 @@ __host__ __device__ inline SmemLayout make_layout8(int stages, int stage_bytes, 
 
 // ---------------------------------------------------------------------------
 // Producer warp: as pa_decode's, with one tiled copy per block (K and V tiles of a kv
-// head are adjacent) and one 16-byte copy of its scales.
+// head are adjacent).
 // ---------------------------------------------------------------------------
 template <typename T, int D, int BS, int NT>
 struct Producer8 {
-    using C = Cfg8<D, BS>;
+    using C = Cfg8<T, D, BS, NT>;
     const DecodeParams &p;
-    const Q8Params &q8;
     const CUtensorMap *map;
     const CtaState &c;
     int lane;
@@ -123,9 +136,8 @@ struct Producer8 {
     uint32_t n;  // items published
     bool failed;
 
-    __device__ Producer8(const DecodeParams &p_, const Q8Params &q8_, const CUtensorMap *map_,
-                         const CtaState &c_, int lane_)
-        : p(p_), q8(q8_), map(map_), c(c_), lane(lane_), g(0), n(0), failed(false)
+    __device__ Producer8(const DecodeParams &p_, const CUtensorMap *map_, const CtaState &c_, int lane_)
+        : p(p_), map(map_), c(c_), lane(lane_), g(0), n(0), failed(false)
     {
         if (lane == 0)
             dev::tma_prefetch_desc(map);
@@ -163,9 +175,11 @@ struct Producer8 {
         }
         ++n;
         const int32_t *row = p.block_tables + (size_t)it.tseq * p.max_blocks;
+        // one coalesced read per 32 blocks, a window ahead
+        int next = it.j0 + lane < it.j1 ? row[it.j0 + lane] : -1;
         for (int jb = it.j0; jb < it.j1; jb += 32) {
-            const int j = jb + lane;
-            c.blk[lane] = (j < it.j1) ? row[j] : -1;  // one coalesced read per 32 blocks
+            c.blk[lane] = next;
+            next = jb + 32 + lane < it.j1 ? row[jb + 32 + lane] : -1;
             __syncwarp();
             uint32_t issued = 0;
             ok = 1;
@@ -192,30 +206,15 @@ struct Producer8 {
                 return 0;
             }
             const uint32_t fb = dev::smem_addr(&c.full[st]);
-            uint8_t *const sc = c.newrow + (size_t)st * C::kBPS * 16;
-            uint32_t bytes = (uint32_t)nbs * C::kRecord;
-#pragma unroll
-            for (int b = 0; b < C::kBPS; ++b) {
-                if (b < nbs) {
-                    const int id = c.blk[i + b];
-                    if (id >= 0 && id < p.num_blocks)
-                        bytes += 16;
-                    else  // an entry outside the pool reads zeros, scales too
-                        *reinterpret_cast<uint4 *>(sc + b * 16) = make_uint4(0, 0, 0, 0);
-                }
-            }
-            dev::mbar_arrive_expect_tx(fb, bytes);
+            dev::mbar_arrive_expect_tx(fb, (uint32_t)nbs * C::kRecord);
             const uint32_t dst = dev::smem_addr(c.ring + (size_t)st * C::kStageBytes);
 #pragma unroll
             for (int b = 0; b < C::kBPS; ++b) {
                 if (b < nbs) {
                     const int id = c.blk[i + b];
-                    const bool in = id >= 0 && id < p.num_blocks;
-                    dev::tma_load_4d(dst + (uint32_t)b * C::kRecord, map, 0, 0, it.kvh, in ? id : -1, fb);
-                    if (in)
-                        dev::bulk_load(dev::smem_addr(sc + b * 16),
-                                       q8.scales + (size_t)id * q8.block_bytes + (size_t)(it.kvh >> 1) * 16,
-                                       16, fb);
+                    // an entry outside the pool reads zeros
+                    dev::tma_load_4d(dst + (uint32_t)b * C::kRecord, map, 0, 0, it.kvh,
+                                     id >= 0 && id < p.num_blocks ? id : -1, fb);
                 }
             }
         }
@@ -246,6 +245,75 @@ struct Producer8 {
     }
 };
 
+// ---------------------------------------------------------------------------
+// Scale warp: walks the same items as the producer and brings each stage's scales into
+// shared memory by plain loads.  (A 16-byte bulk copy of them behind every block's tiles
+// made the producer the bottleneck: 189 us instead of 161 for 64 sequences of 64 / 8
+// heads, 16-token blocks, with the copy merely left out.)  A lane has one block of a
+// window of 32: the loads of the next window's ids and scales are in flight while the
+// stages of this one are handed over.
+// ---------------------------------------------------------------------------
+template <typename T, int D, int BS, int NT>
+struct ScaleWarp {
+    using C = Cfg8<T, D, BS, NT>;
+    const DecodeParams &p;
+    const Q8Params &q8;
+    const CtaState &c;
+    uint64_t *sfull;  // per stage: its scales are in shared memory
+    int lane;
+    uint32_t g;  // stages handed over
+
+    __device__ ScaleWarp(const DecodeParams &p_, const Q8Params &q8_, const CtaState &c_, uint64_t *sfull_,
+                         int lane_)
+        : p(p_), q8(q8_), c(c_), sfull(sfull_), lane(lane_), g(0)
+    {
+    }
+
+    __device__ int block_id(const Item &it, const int32_t *row, int j) const
+    {
+        return j < it.j1 ? row[j] : -1;
+    }
+    __device__ float2 scales_of(const Item &it, int id) const
+    {
+        if (id < 0 || id >= p.num_blocks)
+            return make_float2(0.f, 0.f);  // reads zeros, as the producer's copy does
+        return __ldcg(reinterpret_cast<const float2 *>(q8.scales + (size_t)id * q8.block_bytes) + it.kvh);
+    }
+
+    __device__ bool emit(const Item &it)
+    {
+        const int32_t *row = p.block_tables + (size_t)it.tseq * p.max_blocks;
+        int id = block_id(it, row, it.j0 + lane);
+        int next_id = block_id(it, row, it.j0 + 32 + lane);
+        float2 s = scales_of(it, id);
+        for (int jb = it.j0; jb < it.j1; jb += 32) {
+            const float2 next_s = scales_of(it, next_id);
+            next_id = block_id(it, row, jb + 64 + lane);
+            const int cnt = min(32, it.j1 - jb);
+            for (int i = 0; i < cnt; i += C::kBPS, ++g) {
+                const uint32_t st = g % C::kStages;
+                int ok = 1;
+                if (lane == 0)
+                    ok = dev::mbar_wait_abortable(dev::smem_addr(&c.empty[st]), ((g / C::kStages) & 1u) ^ 1u,
+                                                  p.wait_ns, c.abort);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (ok != 1) {
+                    if (ok == 0 && lane == 0)
+                        raise_error(p, c.abort, PA_DEVERR_TIMEOUT_EMPTY);
+                    return false;
+                }
+                if (lane >= i && lane < i + C::kBPS)
+                    reinterpret_cast<float2 *>(c.newrow)[st * C::kBPS + lane - i] = s;
+                __syncwarp();
+                if (lane == 0)
+                    dev::mbar_arrive(dev::smem_addr(&sfull[st]));
+            }
+            s = next_s;
+        }
+        return true;
+    }
+};
+
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -271,9 +339,10 @@ __device__ __forceinline__ void load_row(float (&x)[N], const T *src)
 // ---------------------------------------------------------------------------
 template <typename T, int D, int BS, int NT>
 __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaState &c, const Item &it,
-                                              uint32_t slot, uint32_t &g, int warp, int lane, int rows_cap)
+                                              uint64_t *sfull, uint32_t slot, uint32_t &g, int warp, int lane,
+                                              int rows_cap)
 {
-    using C = Cfg8<D, BS>;
+    using C = Cfg8<T, D, BS, NT>;
     constexpr bool kSplit = sizeof(T) == 4;  // two fp16 terms for q and p
     constexpr int QT = kSplit ? 2 : 1;
     constexpr int TS = C::kStageTokens;
@@ -356,7 +425,8 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
         if (((j - it.j0) / C::kBPS + rot) % kConsumerWarps != warp)
             continue;
         const uint32_t st = g % C::kStages;
-        if (!warp_wait(p, c, &c.full[st], (g / C::kStages) & 1u))
+        if (!warp_wait(p, c, &sfull[st], (g / C::kStages) & 1u) ||
+            !warp_wait(p, c, &c.full[st], (g / C::kStages) & 1u))
             return false;
         const int nbs = min(C::kBPS, it.j1 - j);  // blocks in this stage
         const int valid = min(nbs * BS, it.len - j * BS);
@@ -365,7 +435,7 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
         float vmax = vref;
 #pragma unroll
         for (int b = 0; b < C::kBPS; ++b) {
-            const float2 s2 = reinterpret_cast<const float2 *>(c.newrow)[(st * C::kBPS + b) * 2 + (it.kvh & 1)];
+            const float2 s2 = reinterpret_cast<const float2 *>(c.newrow)[st * C::kBPS + b];
             kscale[b] = s2.x;
             vscale[b] = b < nbs ? s2.y : 0.f;
             vmax = fmaxf(vmax, vscale[b]);
@@ -386,9 +456,13 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
                 *reinterpret_cast<uint4 *>(&w1[4 * u]) =
                     *reinterpret_cast<const uint4 *>(kt + tile_unit<D>(tk + 2, unit));
             }
+            // even and odd k-steps into accumulators of their own: shorter chains
+            float s2[NT][2][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-                s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    s2[nt][0][e] = s2[nt][1][e] = 0.f;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
                 const uint32_t a[4] = {dev::e4m3x2_to_f16x2(w0[ks] & 0xffffu), dev::e4m3x2_to_f16x2(w1[ks] & 0xffffu),
@@ -397,8 +471,13 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int t = 0; t < QT; ++t)
-                        dev::Mma<__half>::run(s[mt][nt], a, qb[nt][t][ks][0], qb[nt][t][ks][1]);
+                        dev::Mma<__half>::run(s2[nt][ks & 1], a, qb[nt][t][ks][0], qb[nt][t][ks][1]);
             }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    s[mt][nt][e] = s2[nt][0][e] + s2[nt][1][e];
         }
 
         // scale, mask, maximum; a new reference where a score passes the old by more
@@ -578,27 +657,217 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
     return true;
 }
 
-// (fp32 with 16 rows needs more registers than two CTAs per SM leave it)
+// Four consecutive outputs in the storage type.
+template <typename T>
+__device__ __forceinline__ void store4(T *dst, const float (&x)[4])
+{
+    if constexpr (sizeof(T) == 4)
+        *reinterpret_cast<float4 *>(dst) = make_float4(x[0], x[1], x[2], x[3]);
+    else
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(dev::Mma<T>::pack(x[0], x[1]), dev::Mma<T>::pack(x[2], x[3]));
+}
+
+// ---------------------------------------------------------------------------
+// Merge the four consumer states of one item and store it, as finalize_item does, four
+// columns per thread and D / 4 threads per row, so that a row's weights are computed
+// once per thread (2.3 us to 0.4 us per 8-row item).  With own_in_smem the rows stay in
+// the first warp's accumulator rows and their log2-sum-exp in its `ml` entries.
+// ---------------------------------------------------------------------------
+template <typename T, int D>
+__device__ __forceinline__ void finalize8(const DecodeParams &p, const Item &it, float *acc, float *ml,
+                                          int rows_cap, int tid, bool own_in_smem)
+{
+    constexpr int S = D + kAccPad;
+    constexpr int LR = D / 4;  // threads on a row: a warp or half of one
+#pragma unroll 2
+    for (int r = tid / LR; r < it.rows; r += 32 * kConsumerWarps / LR) {
+        const int col = tid % LR * 4;
+        float mc[kConsumerWarps], lc[kConsumerWarps];
+        float4 v[kConsumerWarps];
+        float M = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < kConsumerWarps; ++c) {
+            const float2 x = *reinterpret_cast<const float2 *>(&ml[(c * kHeadsPerItem + r) * 2]);
+            mc[c] = x.x;
+            lc[c] = x.y;
+            v[c] = *reinterpret_cast<const float4 *>(&acc[(c * rows_cap + r) * S + col]);
+            M = fmaxf(M, mc[c]);
+        }
+        float L = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < kConsumerWarps; ++c) {
+            if (mc[c] != -INFINITY) {  // (a warp without stages left no rows)
+                const float w = exp2f(mc[c] - M);
+                L += w * lc[c];
+                o[0] += w * v[c].x;
+                o[1] += w * v[c].y;
+                o[2] += w * v[c].z;
+                o[3] += w * v[c].w;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            o[e] = L > 0.f ? o[e] / L : 0.f;
+        const float lse = L > 0.f ? M + log2f(L) : -INFINITY;
+        if (!it.partial) {
+            store4(reinterpret_cast<T *>(p.out) + ((size_t)it.seq * p.num_q_heads + it.qrow0 + r) * D + col, o);
+        } else if (own_in_smem) {
+            *reinterpret_cast<float4 *>(&acc[r * S + col]) = make_float4(o[0], o[1], o[2], o[3]);
+            // every lane on the row has read its entries
+            __syncwarp(LR == 32 ? 0xffffffffu : 0xffffu << (tid & 16));
+            if (col == 0)
+                ml[r * 2] = lse;
+        } else {
+            const size_t pr = (size_t)it.prow0 + r;
+            *reinterpret_cast<float4 *>(p.part_o + pr * D + col) = make_float4(o[0], o[1], o[2], o[3]);
+            if (col == 0)
+                p.part_lse[pr] = lse;
+        }
+    }
+}
+
+// Merge the nparts <= 32 partials of a split unit into its output rows, as
+// merge_split_unit does, with all of a warp's rows and up to four parts of each in flight
+// at once instead of one row after the other (six parts of 13 rows: 8 us to 3).  own: the
+// unit is completed by its own second part, whose rows finalize8 left in acc and ml.
+template <typename T, int D, int NT>
+__device__ __forceinline__ void merge8(const DecodeParams &p, const Item &it, int warp, int lane,
+                                       const float *acc, const float *ml, bool own)
+{
+    constexpr int S = D + kAccPad;
+    constexpr int VEC = D / 32;
+    constexpr int RW = NT * 8 / kConsumerWarps;  // rows of a warp: warp, warp + 4, ...
+    const long long total = ((long long)it.total_hi << 32) | (long long)it.total_lo;
+    const long long G = balanced_grid(total, it.divisor());
+    const int slot = lane < it.nparts ? (int)split_slot(it, lane, total, G) * kHeadsPerItem : 0;
+    const bool mine = own && slot == it.prow0 / kHeadsPerItem * kHeadsPerItem;
+    float w[RW];
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+        const int r = warp + i * kConsumerWarps;
+        w[i] = -INFINITY;
+        if (lane < it.nparts && r < it.rows)
+            w[i] = mine ? ml[r * 2] : __ldcg(p.part_lse + slot + r);
+    }
+    const int my_part = __ffs(__ballot_sync(0xffffffffu, mine && lane < it.nparts)) - 1;
+    float o[RW][VEC];
+#pragma unroll
+    for (int i = 0; i < RW; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            o[i][e] = 0.f;
+    bool weighted = false;
+    for (int k0 = 0; k0 < it.nparts; k0 += 4) {
+        float v[4][RW][VEC];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int k = min(k0 + u, it.nparts - 1);
+            const int row = __shfl_sync(0xffffffffu, slot, k);
+#pragma unroll
+            for (int i = 0; i < RW; ++i) {
+                const int r = min(warp + i * kConsumerWarps, it.rows - 1);
+                const float *src = p.part_o + (size_t)(row + r) * D + lane * VEC;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    v[u][i][e] = k == my_part ? acc[r * S + lane * VEC + e] : __ldcg(src + e);
+            }
+        }
+        if (!weighted) {  // the weights, while the first rows are on their way
+            weighted = true;
+#pragma unroll
+            for (int i = 0; i < RW; ++i) {
+                const float M = dev::warp_max(w[i]);
+                w[i] = M == -INFINITY ? 0.f : exp2f(w[i] - M);
+                const float W = dev::warp_sum(w[i]);
+                w[i] = W > 0.f ? w[i] / W : 0.f;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+#pragma unroll
+            for (int i = 0; i < RW; ++i) {
+                const float wk = __shfl_sync(0xffffffffu, w[i], min(k0 + u, 31));
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    if (k0 + u < it.nparts)
+                        o[i][e] = fmaf(wk, v[u][i][e], o[i][e]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+        const int r = warp + i * kConsumerWarps;
+        if (r < it.rows) {
+            T *dst = reinterpret_cast<T *>(p.out) + ((size_t)it.seq * p.num_q_heads + it.qrow0 + r) * D + lane * VEC;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                dst[e] = dev::from_float<T>(o[i][e]);
+        }
+    }
+}
+
+// End of an item, as finish_item: the barrier before the merge buffers are used again
+// and, for a split unit, the count and the merge.  False on a timeout.
+template <typename T, int D, int NT>
+__device__ __forceinline__ bool finish8(const DecodeParams &p, const Item &it, const CtaState &c, uint32_t &sph,
+                                        int warp, int lane)
+{
+    if (!consumer_sync(p, c, sph))
+        return false;
+    if (!it.partial)
+        return true;
+    bool merge = *c.merge == 2, own = merge;
+    if (!merge) {
+        if (threadIdx.x == 0) {
+            dev::fence_acq_rel_gpu();
+            const bool last = count_partial(p, it, *c.ctr_seen);
+            if (last)
+                dev::fence_acq_rel_gpu();
+            *c.merge = last ? 1 : 0;
+        }
+        if (!consumer_sync(p, c, sph))
+            return false;
+        merge = *c.merge == 1;
+    }
+    if (merge) {
+        if (it.nparts <= 32)
+            merge8<T, D, NT>(p, it, warp, lane, c.macc, c.mml, own);
+        else
+            merge_split_unit<T, D, false>(p, it, warp, lane, nullptr);
+    }
+    // (own rows are read before the next item's take their place)
+    return own ? consumer_sync(p, c, sph) : true;
+}
+
 template <typename T, int D, int BS, int NT>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 && NT == 2 ? 1 : 2)
+__global__ void __launch_bounds__(kThreads8, Cfg8<T, D, BS, NT>::kCtas)
     pa_q8_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ Q8Params q8,
                         const __grid_constant__ CUtensorMap map)
 {
-    using C = Cfg8<D, BS>;
+    using C = Cfg8<T, D, BS, NT>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem =
         reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int rows_cap = item_rows_cap(p);
     const SmemLayout lay = make_layout8(C::kStages, C::kStageBytes, C::kBPS, rows_cap, D, sizeof(T));
     const CtaState c = cta_state(smem, lay, C::kStages);
+    uint64_t *const sfull = c.csync + 1;
+    if (threadIdx.x < C::kStages)
+        dev::mbar_init(dev::smem_addr(&sfull[threadIdx.x]), 1);
+    dev::fence_mbar_init();
     init_cta(p, c, C::kStages);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     if (warp == kConsumerWarps) {
-        Producer8<T, D, BS, NT> pr(p, q8, &map, c, lane);
+        Producer8<T, D, BS, NT> pr(p, &map, c, lane);
         walk_balanced<kModePlain>(p, BS, C::kBPS, pr, lane);
         pr.finish();
+        return;
+    }
+    if (warp > kConsumerWarps) {
+        ScaleWarp<T, D, BS, NT> sw(p, q8, c, sfull, lane);
+        walk_balanced<kModePlain>(p, BS, C::kBPS, sw, lane);
         return;
     }
     uint32_t g = 0;    // stages consumed (same count in every warp)
@@ -610,36 +879,34 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 && NT == 2 ? 1 : 2)
         const Item it = load_item(&c.items[slot]);
         if (it.seq < 0)
             break;
-        if (!consume_item8<T, D, BS, NT>(p, c, it, slot, g, warp, lane, rows_cap))
+        if (!consume_item8<T, D, BS, NT>(p, c, it, sfull, slot, g, warp, lane, rows_cap))
             break;
         if (threadIdx.x == 0)
             probe_split_last(p, it, c);
         if (!consumer_sync(p, c, sph))
             break;
-        finalize_item<T, D, false>(p, it, c.macc, c.mml, rows_cap, threadIdx.x, nullptr, *c.merge == 2);
-        if (!finish_item<T, D, false>(p, it, c, sph, warp, lane, nullptr))
+        finalize8<T, D>(p, it, c.macc, c.mml, rows_cap, threadIdx.x, *c.merge == 2);
+        if (!finish8<T, D, NT>(p, it, c, sph, warp, lane))
             break;
         if (*c.abort)
             break;
     }
 }
 
-template <typename T, int D, int BS>
+template <typename T, int D, int BS, int NT>
 cudaError_t launch_q8_impl(const Q8Launch &L, cudaStream_t stream)
 {
-    using C = Cfg8<D, BS>;
+    using C = Cfg8<T, D, BS, NT>;
     const DecodeParams &p = L.p;
-    void *kern = p.group <= kNarrowRows ? reinterpret_cast<void *>(&pa_q8_decode_kernel<T, D, BS, 1>)
-                                        : reinterpret_cast<void *>(&pa_q8_decode_kernel<T, D, BS, 2>);
+    void *kern = reinterpret_cast<void *>(&pa_q8_decode_kernel<T, D, BS, NT>);
     const size_t smem =
         make_layout8(C::kStages, C::kStageBytes, C::kBPS, item_rows_cap(p), D, sizeof(T)).total;
-    const size_t smem_max =
-        make_layout8(C::kStages, C::kStageBytes, C::kBPS, kHeadsPerItem, D, sizeof(T)).total;
+    const size_t smem_max = make_layout8(C::kStages, C::kStageBytes, C::kBPS, NT * 8, D, sizeof(T)).total;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
-    const int per_sm = cached_occupancy(kern, dev, smem, smem_max);
+    const int per_sm = cached_occupancy(kern, dev, smem, smem_max, kThreads8);
     if (per_sm <= 0)
         return cudaErrorInvalidConfiguration;
     void *args[] = {const_cast<DecodeParams *>(&L.p), const_cast<Q8Params *>(&L.q8),
@@ -649,7 +916,7 @@ cudaError_t launch_q8_impl(const Q8Launch &L, cudaStream_t stream)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(min(per_sm, kMaxCtasPerSm) * L.sm_count));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kThreads8);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -657,17 +924,25 @@ cudaError_t launch_q8_impl(const Q8Launch &L, cudaStream_t stream)
     return cudaLaunchKernelExC(&cfg, kern, args);
 }
 
+// Items of at most 8 query rows take one group of the products' 8 columns.
+template <typename T, int D, int BS>
+cudaError_t launch_q8_rows(const Q8Launch &L, cudaStream_t stream)
+{
+    return L.p.group <= kNarrowRows ? launch_q8_impl<T, D, BS, 1>(L, stream)
+                                    : launch_q8_impl<T, D, BS, 2>(L, stream);
+}
+
 template <typename T>
 cudaError_t launch_q8_dispatch(const Q8Launch &L, cudaStream_t stream)
 {
     if (L.head_dim == 128 && L.block_size == 16)
-        return launch_q8_impl<T, 128, 16>(L, stream);
+        return launch_q8_rows<T, 128, 16>(L, stream);
     if (L.head_dim == 128 && L.block_size == 32)
-        return launch_q8_impl<T, 128, 32>(L, stream);
+        return launch_q8_rows<T, 128, 32>(L, stream);
     if (L.head_dim == 64 && L.block_size == 16)
-        return launch_q8_impl<T, 64, 16>(L, stream);
+        return launch_q8_rows<T, 64, 16>(L, stream);
     if (L.head_dim == 64 && L.block_size == 32)
-        return launch_q8_impl<T, 64, 32>(L, stream);
+        return launch_q8_rows<T, 64, 32>(L, stream);
     return cudaErrorInvalidValue;
 }
 
