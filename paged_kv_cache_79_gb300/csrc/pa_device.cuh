@@ -203,6 +203,25 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x)
     return d;
 }
 
+// Four e4m3 codes as two fp16 pairs (codes 0, 1 and 2, 3).
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t x, uint32_t &lo, uint32_t &hi)
+{
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(x));
+}
+
+// 2^x; results below the normal range are 0.
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Two fp32 values as two e4m3 codes (lo in the low byte), to nearest even.
 __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi)
 {

@@ -421,15 +421,15 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
     }
     float vref = FLT_MIN;  // largest vs so far (its inverse is finite, also for scales of 0)
     const int rot = it.rot();
-    for (int j = it.j0; j < it.j1; j += C::kBPS, ++g) {
-        if (((j - it.j0) / C::kBPS + rot) % kConsumerWarps != warp)
-            continue;
-        const uint32_t st = g % C::kStages;
-        if (!warp_wait(p, c, &sfull[st], (g / C::kStages) & 1u) ||
-            !warp_wait(p, c, &c.full[st], (g / C::kStages) & 1u))
+    const int stages = (it.j1 - it.j0 + C::kBPS - 1) / C::kBPS;
+    for (int i = (warp - rot) & (kConsumerWarps - 1); i < stages; i += kConsumerWarps) {
+        const int j = it.j0 + i * C::kBPS;
+        const uint32_t st = (g + i) % C::kStages, phase = ((g + i) / C::kStages) & 1u;
+        if (!warp_wait(p, c, &sfull[st], phase) || !warp_wait(p, c, &c.full[st], phase))
             return false;
         const int nbs = min(C::kBPS, it.j1 - j);  // blocks in this stage
         const int valid = min(nbs * BS, it.len - j * BS);
+        const bool partial = valid < TS;
         const uint8_t *stage = c.ring + (size_t)st * C::kStageBytes;
         float kscale[C::kBPS], vscale[C::kBPS];
         float vmax = vref;
@@ -465,8 +465,9 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
                     s2[nt][0][e] = s2[nt][1][e] = 0.f;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                const uint32_t a[4] = {dev::e4m3x2_to_f16x2(w0[ks] & 0xffffu), dev::e4m3x2_to_f16x2(w1[ks] & 0xffffu),
-                                       dev::e4m3x2_to_f16x2(w0[ks] >> 16), dev::e4m3x2_to_f16x2(w1[ks] >> 16)};
+                uint32_t a[4];
+                dev::e4m3x4_to_f16x4(w0[ks], a[0], a[2]);
+                dev::e4m3x4_to_f16x4(w1[ks], a[1], a[3]);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -493,9 +494,10 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
                 const float ga = fa[nt] * ksc, gb = fb[nt] * ksc;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const bool ok = mt * 16 + tok0 + 2 * h < valid;
-                    s[mt][nt][2 * h] = ok ? s[mt][nt][2 * h] * ga : -INFINITY;
-                    s[mt][nt][2 * h + 1] = ok ? s[mt][nt][2 * h + 1] * gb : -INFINITY;
+                    s[mt][nt][2 * h] *= ga;
+                    s[mt][nt][2 * h + 1] *= gb;
+                    if (partial && mt * 16 + tok0 + 2 * h >= valid)
+                        s[mt][nt][2 * h] = s[mt][nt][2 * h + 1] = -INFINITY;
                     mxa = fmaxf(mxa, s[mt][nt][2 * h]);
                     mxb = fmaxf(mxb, s[mt][nt][2 * h + 1]);
                 }
@@ -543,7 +545,7 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
                 const float vs = vscale[mt * 16 / BS] * vinv * kUp;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const float ea = exp2f(s[mt][nt][2 * h] - na), eb = exp2f(s[mt][nt][2 * h + 1] - nb);
+                    const float ea = dev::ex2(s[mt][nt][2 * h] - na), eb = dev::ex2(s[mt][nt][2 * h + 1] - nb);
                     la[nt] += ea;
                     lb[nt] += eb;
                     const float ya = ea * vs, yb = eb * vs;
@@ -559,7 +561,6 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
         }
 
         // O^T += V^T P^T, 32 dims (two 16 x 16 matrices of codes) at a time
-        const bool partial = valid < TS;
 #pragma unroll
         for (int dp = 0; dp < DM / 2; ++dp) {
             float loc[NT][2][4];
@@ -587,10 +588,9 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const uint32_t a[4] = {dev::e4m3x2_to_f16x2(v[2 * h] & 0xffffu),
-                                           dev::e4m3x2_to_f16x2(v[2 * h + 1] & 0xffffu),
-                                           dev::e4m3x2_to_f16x2(v[2 * h] >> 16),
-                                           dev::e4m3x2_to_f16x2(v[2 * h + 1] >> 16)};
+                    uint32_t a[4];
+                    dev::e4m3x4_to_f16x4(v[2 * h], a[0], a[2]);
+                    dev::e4m3x4_to_f16x4(v[2 * h + 1], a[1], a[3]);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -616,6 +616,8 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
         if (lane == 0)
             dev::mbar_arrive(dev::smem_addr(&c.empty[st]));
     }
+
+    g += stages;
 
     // partial rows of this warp
     float *mine = c.macc + warp * rows_cap * SA;
@@ -679,7 +681,6 @@ __device__ __forceinline__ void finalize8(const DecodeParams &p, const Item &it,
 {
     constexpr int S = D + kAccPad;
     constexpr int LR = D / 4;  // threads on a row: a warp or half of one
-#pragma unroll 2
     for (int r = tid / LR; r < it.rows; r += 32 * kConsumerWarps / LR) {
         const int col = tid % LR * 4;
         float mc[kConsumerWarps], lc[kConsumerWarps];
