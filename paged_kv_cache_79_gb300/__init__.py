@@ -23,6 +23,7 @@ calls on tensors that are not CUDA tensors raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import List, Optional, Sequence, Tuple
 
 from ._lib import load as _load, library_path  # noqa: F401
@@ -665,21 +666,32 @@ def pa_scatter_blocks(staging_k, staging_v, k_cache, v_cache, block_ids, stream=
 # ----------------------------------------------------------------------------
 # the 8-bit cache, and tables built on the GPU
 # ----------------------------------------------------------------------------
-def _device_of(*named):
-    """A context in which the tensors' device is the current one; the tensors must be
-    contiguous CUDA tensors of one device."""
-    import contextlib
+def _on_device(names, tensors):
+    """Checks that the tensors are contiguous and on one CUDA device; returns None when it is
+    the current device, else a context that makes it so."""
     import torch
-    dev = None
-    for name, t in named:
-        _cuda(t, name)
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the others on {dev}")
-    if dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+    dev = tensors[0].get_device()
+    for name, t in zip(names, tensors):
+        if not t.is_cuda or not t.is_contiguous():
+            _cuda(t, name)
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on cuda:{t.get_device()}, {names[0]} on cuda:{dev}")
+    return None if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _raw_stream(stream, tensor) -> int:
+    """As _stream, on the tensor's device (without building a stream object for the default)."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(tensor.get_device())
+    return _stream(stream)
+
+
+def _call(fn, device, *args) -> int:
+    if device is None:
+        return fn(*args)
+    with device:
+        return fn(*args)
 
 
 def _want(ok: bool, what: str) -> None:
@@ -687,6 +699,7 @@ def _want(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
+@functools.lru_cache(maxsize=None)
 def pa_q8_block_bytes(num_kv_heads: int, head_dim: int, block_size: int) -> int:
     """Bytes of one block of the 8-bit cache: codes of K and V, then the scales."""
     n = _load().pa_q8_block_bytes(num_kv_heads, head_dim, block_size)
@@ -709,11 +722,15 @@ def q8_views(kv_cache, num_kv_heads: int, head_dim: int, block_size: int):
     [num_blocks, Hkv, 2, B, d] and float32 [num_blocks, Hkv, 2], index 0 of the pair K
     and 1 V; a code stands for code * scale."""
     import torch
-    n = _load().pa_q8_scales_offset(num_kv_heads, head_dim, block_size)
-    _want(kv_cache.shape[1] == pa_q8_block_bytes(num_kv_heads, head_dim, block_size),
-          "kv_cache has another block size in bytes")
-    codes = kv_cache[:, :n].view(torch.float8_e4m3fn).unflatten(1, (num_kv_heads, 2, block_size, head_dim))
-    scales = kv_cache[:, n:n + num_kv_heads * 8].view(torch.float32).unflatten(1, (num_kv_heads, 2))
+    nb, size = kv_cache.shape
+    _want(size == pa_q8_block_bytes(num_kv_heads, head_dim, block_size) and kv_cache.is_contiguous(),
+          "kv_cache must be a contiguous [num_blocks, pa_q8_block_bytes(...)]")
+    tile = block_size * head_dim
+    at = kv_cache.storage_offset()
+    codes = kv_cache.view(torch.float8_e4m3fn).as_strided(
+        (nb, num_kv_heads, 2, block_size, head_dim), (size, 2 * tile, tile, head_dim, 1), at)
+    scales = kv_cache.view(torch.float32).as_strided((nb, num_kv_heads, 2), (size // 4, 2, 1),
+                                                     (at + num_kv_heads * 2 * tile) // 4)
     return codes, scales
 
 
@@ -723,10 +740,16 @@ def _check_batch(kv_cache, block_tables, context_lens, num_kv_heads, head_dim, b
         raise TypeError("block_tables and context_lens must be int32")
     if kv_cache.dtype != torch.uint8:
         raise TypeError("kv_cache must be uint8")
-    _want(block_tables.dim() == 2 and context_lens.shape == block_tables.shape[:1],
-          "block_tables must be [S, W] and context_lens [S]")
-    _want(kv_cache.dim() == 2 and kv_cache.shape[1] == pa_q8_block_bytes(num_kv_heads, head_dim, block_size),
-          "kv_cache must be [num_blocks, pa_q8_block_bytes(...)]")
+    if block_tables.dim() != 2 or context_lens.shape != block_tables.shape[:1]:
+        raise ValueError("block_tables must be [S, W] and context_lens [S]")
+    if kv_cache.dim() != 2 or kv_cache.shape[1] != pa_q8_block_bytes(num_kv_heads, head_dim, block_size):
+        raise ValueError("kv_cache must be [num_blocks, pa_q8_block_bytes(...)]")
+
+
+_APPEND_NAMES = ("k", "v", "kv_cache", "block_tables", "context_lens", "query_start")
+_DECODE_NAMES = ("out", "q", "kv_cache", "block_tables", "context_lens", "workspace")
+_TABLE_NAMES = ("block_tables", "context_lens", "new_tokens", "free_list", "num_free", "query_start", "granted",
+                "context_lens_out", "num_free_out", "slot_mapping")
 
 
 def pa_q8_append(k, v, kv_cache, block_tables, context_lens, block_size: int, query_start=None, stream=None):
@@ -741,18 +764,18 @@ def pa_q8_append(k, v, kv_cache, block_tables, context_lens, block_size: int, qu
     n, hkv, d = k.shape
     S, W = block_tables.shape
     _check_batch(kv_cache, block_tables, context_lens, hkv, d, block_size)
-    named = [("k", k), ("v", v), ("kv_cache", kv_cache), ("block_tables", block_tables),
-             ("context_lens", context_lens)]
+    names, tensors = _APPEND_NAMES, (k, v, kv_cache, block_tables, context_lens)
+    qs_ptr = None
     if query_start is not None:
         if query_start.dtype != torch.int32:
             raise TypeError("query_start must be int32")
         _want(query_start.shape == (S + 1,), "query_start must be [S + 1]")
-        named.append(("query_start", query_start))
-    with _device_of(*named):
-        st = _load().pa_q8_append(k.data_ptr(), v.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(), W,
-                                  context_lens.data_ptr(),
-                                  query_start.data_ptr() if query_start is not None else None, S, n,
-                                  kv_cache.shape[0], hkv, d, block_size, _dtype_code(k), _stream(stream))
+        tensors += (query_start,)
+        qs_ptr = query_start.data_ptr()
+    device = _on_device(names, tensors)
+    st = _call(_load().pa_q8_append, device, k.data_ptr(), v.data_ptr(), kv_cache.data_ptr(),
+               block_tables.data_ptr(), W, context_lens.data_ptr(), qs_ptr, S, n, kv_cache.shape[0], hkv, d,
+               block_size, _dtype_code(k), _raw_stream(stream, k))
     _check(st, "pa_q8_append")
 
 
@@ -765,6 +788,10 @@ def pa_q8_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, b
     return n
 
 
+def _q8_scratch(S, hq, hkv, d, b, W, device, stream):
+    return _launch_scratch(pa_q8_decode_workspace_size(S, hq, hkv, d, b, W), device, stream)
+
+
 def pa_q8_decode(out, q, kv_cache, block_tables, context_lens, scale: float, num_q_heads: int,
                  num_kv_heads: int, head_dim: int, block_size: int, workspace=None, stream=None):
     """out[S, Hq, d] <- decode attention over the 8-bit cache (see pa_q8_decode in
@@ -774,18 +801,16 @@ def pa_q8_decode(out, q, kv_cache, block_tables, context_lens, scale: float, num
     _want(q.shape == (S, num_q_heads, head_dim) and out.shape == q.shape, "q and out must be [S, Hq, d]")
     if out.dtype != q.dtype:
         raise TypeError("q and out must have one dtype")
-    named = [("out", out), ("q", q), ("kv_cache", kv_cache), ("block_tables", block_tables),
-             ("context_lens", context_lens)]
-    if workspace is not None:
-        named.append(("workspace", workspace))
-    with _device_of(*named):
-        if workspace is None:
-            workspace = _launch_scratch(pa_q8_decode_workspace_size(S, num_q_heads, num_kv_heads, head_dim,
-                                                                    block_size, W), q.device, stream)
-        st = _load().pa_q8_decode(out.data_ptr(), q.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(), W,
-                                  context_lens.data_ptr(), S, kv_cache.shape[0], float(scale), num_q_heads,
-                                  num_kv_heads, head_dim, block_size, _dtype_code(q), workspace.data_ptr(),
-                                  workspace.numel() * workspace.element_size(), _stream(stream))
+    device = _on_device(_DECODE_NAMES, (out, q, kv_cache, block_tables, context_lens))
+    if workspace is None:
+        workspace = _call(_q8_scratch, device, S, num_q_heads, num_kv_heads, head_dim, block_size, W, q.device,
+                          stream)
+    else:
+        _on_device(_DECODE_NAMES[5:] + _DECODE_NAMES[:1], (workspace, out))
+    st = _call(_load().pa_q8_decode, device, out.data_ptr(), q.data_ptr(), kv_cache.data_ptr(),
+               block_tables.data_ptr(), W, context_lens.data_ptr(), S, kv_cache.shape[0], float(scale), num_q_heads,
+               num_kv_heads, head_dim, block_size, _dtype_code(q), workspace.data_ptr(),
+               workspace.numel() * workspace.element_size(), _raw_stream(stream, q))
     _check(st, "pa_q8_decode")
     return out
 
@@ -799,9 +824,9 @@ def pa_q8_copy_blocks(kv_cache, src_dst_pairs, stream=None):
     n = src_dst_pairs.shape[0]
     if n == 0:
         return
-    with _device_of(("kv_cache", kv_cache), ("src_dst_pairs", src_dst_pairs)):
-        st = _load().pa_q8_copy_blocks(kv_cache.data_ptr(), src_dst_pairs.data_ptr(), n, kv_cache.shape[0],
-                                       _block_bytes(kv_cache), _stream(stream))
+    device = _on_device(("kv_cache", "src_dst_pairs"), (kv_cache, src_dst_pairs))
+    st = _call(_load().pa_q8_copy_blocks, device, kv_cache.data_ptr(), src_dst_pairs.data_ptr(), n,
+               kv_cache.shape[0], _block_bytes(kv_cache), _raw_stream(stream, kv_cache))
     _check(st, "pa_q8_copy_blocks")
 
 
@@ -832,11 +857,11 @@ def pa_build_tables(block_tables, context_lens, new_tokens, free_list, num_free,
         context_lens_out = context_lens
     if num_free_out is None:
         num_free_out = num_free
-    named = [("block_tables", block_tables), ("context_lens", context_lens), ("new_tokens", new_tokens),
-             ("free_list", free_list), ("num_free", num_free), ("query_start", query_start),
-             ("granted", granted), ("context_lens_out", context_lens_out), ("num_free_out", num_free_out)]
-    for name, t in named:
-        if t.dtype != torch.int32:
+    tensors = (block_tables, context_lens, new_tokens, free_list, num_free, query_start, granted, context_lens_out,
+               num_free_out, slot_mapping)
+    int32 = torch.int32
+    for name, t in zip(_TABLE_NAMES, tensors[:-1]):
+        if t.dtype != int32:
             raise TypeError(f"{name} must be int32")
     if slot_mapping.dtype != torch.int64:
         raise TypeError("slot_mapping must be int64")
@@ -846,12 +871,12 @@ def pa_build_tables(block_tables, context_lens, new_tokens, free_list, num_free,
     _want(query_start.shape == (S + 1,), "query_start must be [S + 1]")
     _want(num_free.numel() == 1 and num_free_out.numel() == 1, "num_free and num_free_out hold one number")
     _want(free_list.dim() == 1 and slot_mapping.dim() == 1, "free_list and slot_mapping must have one dimension")
-    with _device_of(*named, ("slot_mapping", slot_mapping)):
-        st = _load().pa_build_tables(block_tables.data_ptr(), W, context_lens_out.data_ptr(),
-                                     context_lens.data_ptr(), new_tokens.data_ptr(), S, free_list.data_ptr(),
-                                     free_list.shape[0], num_free_out.data_ptr(), num_free.data_ptr(), block_size,
-                                     granted.data_ptr(), query_start.data_ptr(), slot_mapping.data_ptr(),
-                                     slot_mapping.shape[0], _stream(stream))
+    device = _on_device(_TABLE_NAMES, tensors)
+    st = _call(_load().pa_build_tables, device, block_tables.data_ptr(), W, context_lens_out.data_ptr(),
+               context_lens.data_ptr(), new_tokens.data_ptr(), S, free_list.data_ptr(), free_list.shape[0],
+               num_free_out.data_ptr(), num_free.data_ptr(), block_size, granted.data_ptr(),
+               query_start.data_ptr(), slot_mapping.data_ptr(), slot_mapping.shape[0],
+               _raw_stream(stream, block_tables))
     _check(st, "pa_build_tables")
 
 

@@ -248,6 +248,33 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a)
     return d;
 }
 
+// The sequence of each lane's token t0 + lane: the last s with query_start[s] <= t
+// (num_seqs: a row past the last sequence; -1: before the first).  A warp looks through
+// 32 entries at a time, so 1024 sequences take two dependent reads; with lo >= 0, a
+// sequence that starts at or before t0, it looks on from there.
+__device__ __forceinline__ int find_sequence(const int32_t *qs, int num_seqs, int t0, int lane, int lo = -1)
+{
+    int hi = lo < 0 ? num_seqs : lo;  // the answer for t0 lies in lo .. hi
+    while (lo < hi) {
+        const int step = (hi - lo + 31) / 32;
+        const int i = lo + (lane + 1) * step;
+        const bool le = i <= hi && qs[i] <= t0;
+        const int c = __popc(__ballot_sync(0xffffffffu, le));
+        lo += c * step;
+        hi = min(hi, lo + step - 1);
+    }
+    int s = lo;
+    for (int base = lo + 1; base <= num_seqs; base += 32) {
+        const int e = base + lane <= num_seqs ? qs[base + lane] : 0x7fffffff;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            s += __shfl_sync(0xffffffffu, e, i) <= t0 + lane ? 1 : 0;
+        if (__shfl_sync(0xffffffffu, e, 31) > t0 + 31)
+            break;
+    }
+    return s;
+}
+
 template <typename T>
 struct Mma;
 

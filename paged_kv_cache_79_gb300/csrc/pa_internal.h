@@ -192,7 +192,7 @@ struct Q8AppendParams {
     size_t block_bytes, scales;   // Q8Layout
     int max_blocks, num_seqs, num_tokens, num_blocks, num_kv_heads, block_size;
 };
-cudaError_t launch_q8_append(const Q8AppendParams &p, int head_dim, pa_dtype dtype,
+cudaError_t launch_q8_append(const Q8AppendParams &p, int head_dim, pa_dtype dtype, int sms,
                              cudaStream_t stream);
 
 struct TablesParams {
@@ -207,8 +207,9 @@ struct TablesParams {
     int32_t *query_start;
     int64_t *slots;
     int max_blocks, num_seqs, num_blocks, block_size, num_slots;
+    bool slots_apart;             // set by the launcher: a second kernel writes `slots`
 };
-cudaError_t launch_build_tables(const TablesParams &p, cudaStream_t stream);
+cudaError_t launch_build_tables(TablesParams p, cudaStream_t stream);
 
 // Persistent grid (CTAs) of a balanced-split launch of the plain decode with a
 // plan; 0 if the configuration cannot launch.

@@ -89,6 +89,10 @@ pa_status pa_q8_append(const void *k, const void *v, void *kv_cache, const int32
         check_sizes(num_blocks, max_blocks_per_seq, num_kv_heads, head_dim, block_size, dtype);
     if (st != PA_OK)
         return st;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return cuda_fail(e);
     const Q8Layout l = q8_layout(block_size, num_kv_heads, head_dim);
     Q8AppendParams p;
     p.k = k;
@@ -105,7 +109,7 @@ pa_status pa_q8_append(const void *k, const void *v, void *kv_cache, const int32
     p.num_blocks = num_blocks;
     p.num_kv_heads = num_kv_heads;
     p.block_size = block_size;
-    const cudaError_t e = launch_q8_append(p, head_dim, dtype, static_cast<cudaStream_t>(stream));
+    e = launch_q8_append(p, head_dim, dtype, sm_count(dev), static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
 

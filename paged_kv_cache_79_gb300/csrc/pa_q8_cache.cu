@@ -51,32 +51,6 @@ __device__ __forceinline__ Run run_at(const Q8AppendParams &p, int t, int s, int
     return r;
 }
 
-// The sequence of each lane's token t0 + lane: the last s with query_start[s] <= t
-// (num_seqs: a row past the last sequence; -1: before the first).  A warp looks through
-// 32 entries at a time, so 1024 sequences take two dependent reads.
-__device__ __forceinline__ int find_sequence(const int32_t *qs, int num_seqs, int t0, int lane)
-{
-    int lo = -1, hi = num_seqs;  // the answer for t0 lies in lo .. hi
-    while (lo < hi) {
-        const int step = (hi - lo + 31) / 32;
-        const int i = lo + (lane + 1) * step;
-        const bool le = i <= hi && qs[i] <= t0;
-        const int c = __popc(__ballot_sync(0xffffffffu, le));
-        lo += c * step;
-        hi = min(hi, lo + step - 1);
-    }
-    int s = lo;
-    for (int base = lo + 1; base <= num_seqs; base += 32) {
-        const int e = base + lane <= num_seqs ? qs[base + lane] : 0x7fffffff;
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            s += __shfl_sync(0xffffffffu, e, i) <= t0 + lane ? 1 : 0;
-        if (__shfl_sync(0xffffffffu, e, 31) > t0 + 31)
-            break;
-    }
-    return s;
-}
-
 __device__ __forceinline__ void widen(float (&x)[8], const uint4 &w, const __half *)
 {
     const __half2 *h = reinterpret_cast<const __half2 *>(&w);
@@ -104,55 +78,75 @@ __device__ __forceinline__ void widen(float (&x)[4], const uint4 &w, const float
     x[3] = __uint_as_float(w.w);
 }
 
-// |x| for the maximum: infinities and NaN do not count (their codes are NaN).
-__device__ __forceinline__ float finite_abs(float x)
+// Largest |x| of the 16 bytes as the bits of its type, without the sign: in this order
+// infinities, then NaN, lie above every finite value.
+__device__ __forceinline__ uint32_t abs_max_bits(uint32_t m, const uint4 &w, const float *)
 {
-    const float a = fabsf(x);
-    return a <= 3.402823466e38f ? a : 0.f;
+    m = max(m, w.x & 0x7fffffffu);
+    m = max(m, w.y & 0x7fffffffu);
+    m = max(m, w.z & 0x7fffffffu);
+    return max(m, w.w & 0x7fffffffu);
 }
+template <typename T>  // two 16-bit values at a time
+__device__ __forceinline__ uint32_t abs_max_bits(uint32_t m, const uint4 &w, const T *)
+{
+    m = __vmaxu2(m, w.x & 0x7fff7fffu);
+    m = __vmaxu2(m, w.y & 0x7fff7fffu);
+    m = __vmaxu2(m, w.z & 0x7fff7fffu);
+    return __vmaxu2(m, w.w & 0x7fff7fffu);
+}
+
+// A warp's maximum of those bits as fp32 (infinite or NaN when some value is).
+__device__ __forceinline__ float warp_abs_max(uint32_t m, const float *)
+{
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, m));
+}
+__device__ __forceinline__ float warp_abs_max(uint32_t m, const __nv_bfloat16 *)
+{
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16)) << 16);
+}
+__device__ __forceinline__ float warp_abs_max(uint32_t m, const __half *)
+{
+    return __half2float(__ushort_as_half(
+        (unsigned short)__reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16))));
+}
+
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
 
 __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d)
 {
-    const float nan = __uint_as_float(0x7fffffffu);
-    a = fabsf(a) < INFINITY ? a : nan;
-    b = fabsf(b) < INFINITY ? b : nan;
-    c = fabsf(c) < INFINITY ? c : nan;
-    d = fabsf(d) < INFINITY ? d : nan;
     return dev::f32x2_to_e4m3x2(a, b) | (dev::f32x2_to_e4m3x2(c, d) << 16);
 }
 
-// x / s: a product with the exact inverse for the powers of two that this kernel
-// writes, a division for other scales that a caller put into the cache.
-struct Divide {
-    float s, inv;
-    bool pow2;
-    __device__ explicit Divide(float s_)
-    {
-        s = s_;
-        inv = 1.f / s_;
-        pow2 = (__float_as_uint(s_) & 0x7fffffu) == 0;
-    }
-    __device__ float operator()(float x) const { return pow2 ? x * inv : x / s; }
-};
+// x / s with NaN for values that are not finite (the conversion would make infinities
+// +-448).
+__device__ __forceinline__ float quotient(float x, float s)
+{
+    return finite(x) ? x / s : __uint_as_float(0x7fffffffu);
+}
 
 // Four codes times `ratio`, rounded again.
 __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio)
 {
-    const uint32_t h0 = dev::e4m3x2_to_f16x2(w & 0xffffu), h1 = dev::e4m3x2_to_f16x2(w >> 16);
+    uint32_t h0, h1;
+    dev::e4m3x4_to_f16x4(w, h0, h1);
     const float2 f0 = __half22float2(*reinterpret_cast<const __half2 *>(&h0));
     const float2 f1 = __half22float2(*reinterpret_cast<const __half2 *>(&h1));
     return encode4(f0.x * ratio, f0.y * ratio, f1.x * ratio, f1.y * ratio);
 }
 
-template <typename T, int D, int BS>
-__global__ void __launch_bounds__(32 * kAppendWarps)
+// kRows: rows of a run whose loads are kept in registers, and all in flight at once; a
+// longer run's other rows are read twice.
+template <typename T, int D, int BS, int kRows>
+__global__ void __launch_bounds__(32 * kAppendWarps, kRows == BS ? 2 : 4)
     q8_append_kernel(const __grid_constant__ Q8AppendParams p)
 {
     constexpr int E = 16 / (int)sizeof(T);    // elements of a 16-byte load
     constexpr int LR = D / E;                 // lanes on one row
     constexpr int RP = 32 / LR;               // rows a warp loads at once
     constexpr int kPasses = BS / RP;
-    constexpr int kHold = kPasses < 16 ? kPasses : 16;  // loads kept in registers
+    constexpr int kHold = kRows / RP < 16 ? kRows / RP : 16;
+    static_assert(kHold >= 1, "a load at least");
     __shared__ Run runs[kChunk];
     __shared__ int num_runs;
     dev::grid_dependency_wait();  // lengths, tables, rows and cache may come from the previous kernel
@@ -162,11 +156,19 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
         const int t0 = blockIdx.x * kChunk, t = t0 + lane;
         Run r = {t, 0, 0, 0};
         if (p.query_start) {
-            const int s = find_sequence(p.query_start, p.num_seqs, t0, lane);
-            if (t < p.num_tokens && s >= 0 && s < p.num_seqs) {
-                const int start = p.query_start[s];
-                r = run_at(p, t, s, start, p.query_start[s + 1] - start);
+            // a decode step's rows: one per sequence, so that row t is sequence t's; a look
+            // at those entries saves the search
+            const int at = min(t, p.num_seqs), next = min(t + 1, p.num_seqs);
+            int start = p.query_start[at], end = p.query_start[next], s = t;
+            if (!__all_sync(0xffffffffu, t >= p.num_tokens || (t < p.num_seqs && start == t && end == t + 1))) {
+                s = dev::find_sequence(p.query_start, p.num_seqs, t0, lane);
+                if (s >= 0 && s < p.num_seqs) {
+                    start = p.query_start[s];
+                    end = p.query_start[s + 1];
+                }
             }
+            if (t < p.num_tokens && s >= 0 && s < p.num_seqs)
+                r = run_at(p, t, s, start, end - start);
         } else if (t < p.num_tokens && t < p.num_seqs) {
             r = run_at(p, t, t, t, 1);
         }
@@ -182,69 +184,85 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
     for (int task = blockIdx.y * kAppendWarps + warp; task < tasks; task += gridDim.y * kAppendWarps) {
         const Run r = runs[task / tiles];
         const int tile = task % tiles;
-        const int h = tile >> 1;
         const T *src = reinterpret_cast<const T *>((tile & 1) ? p.v : p.k) +
-                       ((size_t)r.token * p.num_kv_heads + h) * D + (lane % LR) * E;
+                       ((size_t)r.token * p.num_kv_heads + (tile >> 1)) * D + (lane % LR) * E;
         const size_t row_stride = (size_t)p.num_kv_heads * D;
         uint8_t *const block = p.cache + (size_t)r.block * p.block_bytes;
         uint8_t *const codes = block + (size_t)tile * (BS * D);
         float *const scale = reinterpret_cast<float *>(block + p.scales) + tile;
         const float old = r.off == 0 ? 0.f : *scale;
+        const int row0 = lane / LR;  // this lane's rows: row0, row0 + RP, ...
+        auto load = [&](int i) {
+            const int row = i * RP + row0;
+            return row < r.rows ? __ldcg(reinterpret_cast<const uint4 *>(src + row * row_stride))
+                                : make_uint4(0, 0, 0, 0);
+        };
 
         uint4 w[kHold];
-        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < kHold; ++i)
+            w[i] = load(i);
+        uint32_t bits = 0;
+#pragma unroll
+        for (int i = 0; i < kHold; ++i)
+            bits = abs_max_bits(bits, w[i], src);
+        for (int i = kHold; i < kPasses && i * RP < r.rows; ++i)
+            bits = abs_max_bits(bits, load(i), src);
+        float top = warp_abs_max(bits, src);
         float x[E];
-#pragma unroll
-        for (int i = 0; i < kHold; ++i) {
-            const int row = i * RP + lane / LR;
-            w[i] = row < r.rows ? __ldcg(reinterpret_cast<const uint4 *>(src + row * row_stride))
-                                : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < kHold; ++i) {
-            widen(x, w[i], src);
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                top = fmaxf(top, finite_abs(x[e]));
-        }
-        // (rows past what the registers hold are read twice: fp32, 128 dims, 32-row blocks)
-        for (int i = kHold; i < kPasses && i * RP < r.rows; ++i) {
-            const int row = i * RP + lane / LR;
-            if (row < r.rows) {
-                widen(x, __ldcg(reinterpret_cast<const uint4 *>(src + row * row_stride)), src);
+        const bool odd = !finite(top);  // some value is infinite or NaN: leave those out
+        if (odd) {
+            top = 0.f;
+            for (int i = 0; i < kPasses && i * RP < r.rows; ++i) {
+                widen(x, load(i), src);
 #pragma unroll
                 for (int e = 0; e < E; ++e)
-                    top = fmaxf(top, finite_abs(x[e]));
+                    top = finite(x[e]) ? fmaxf(top, fabsf(x[e])) : top;
             }
+            top = dev::warp_max(top);
         }
-        top = dev::warp_max(top);
         // 448 = 1.75 * 2^8: the exponent of top / 448, one more where top's mantissa
         // passes 1.75's; at least the smallest normal scale
         const int e2 = max((int)((__float_as_uint(top) + 0x1fffffu) >> 23) - 8, 1);
         const float need = __uint_as_float((uint32_t)e2 << 23);
         const float s = fmaxf(old, need);
-        const Divide div(s);
-        auto put = [&](int i, const uint4 &v) {
-            const int row = i * RP + lane / LR;
-            if (row >= r.rows)
-                return;
-            widen(x, v, src);
-            uint8_t *dst = codes + (size_t)(r.off + row) * D + (lane % LR) * E;
-            const uint32_t c0 = encode4(div(x[0]), div(x[1]), div(x[2]), div(x[3]));
-            if constexpr (E == 8) {
-                const uint32_t c1 = encode4(div(x[4]), div(x[5]), div(x[6]), div(x[7]));
-                *reinterpret_cast<uint2 *>(dst) = make_uint2(c0, c1);
-            } else {
-                *reinterpret_cast<uint32_t *>(dst) = c0;
+        auto put = [&](int i) {
+            const int row = i * RP + row0;
+            if (row < r.rows) {
+                uint8_t *dst = codes + (size_t)(r.off + row) * D + (lane % LR) * E;
+                const uint32_t c0 = encode4(x[0], x[1], x[2], x[3]);
+                if constexpr (E == 8)
+                    *reinterpret_cast<uint2 *>(dst) = make_uint2(c0, encode4(x[4], x[5], x[6], x[7]));
+                else
+                    *reinterpret_cast<uint32_t *>(dst) = c0;
             }
         };
+        if (!odd && (__float_as_uint(s) & 0x7fffffu) == 0) {
+            const float inv = 1.f / s;  // exact: a power of two
 #pragma unroll
-        for (int i = 0; i < kHold; ++i)
-            put(i, w[i]);
-        for (int i = kHold; i < kPasses && i * RP < r.rows; ++i) {
-            const int row = i * RP + lane / LR;
-            put(i, row < r.rows ? __ldcg(reinterpret_cast<const uint4 *>(src + row * row_stride))
-                                : make_uint4(0, 0, 0, 0));
+            for (int i = 0; i < kHold; ++i) {
+                widen(x, w[i], src);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    x[e] *= inv;
+                put(i);
+            }
+            for (int i = kHold; i < kPasses && i * RP < r.rows; ++i) {
+                widen(x, load(i), src);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    x[e] *= inv;
+                put(i);
+            }
+        } else {
+            // values that are not finite, or a scale of the caller's own
+            for (int i = 0; i < kPasses && i * RP < r.rows; ++i) {
+                widen(x, load(i), src);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    x[e] = quotient(x[e], s);
+                put(i);
+            }
         }
         if (r.off != 0 && s > old) {
             const float ratio = old / s;
@@ -260,20 +278,30 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
                 reinterpret_cast<uint4 *>(codes)[v] = q;
             }
         }
-        if (lane == 0 && (r.off == 0 || s > old))
+        if (lane == 0 && (r.off == 0 || s != old))
             *scale = s;
     }
 }
 
 template <typename T, int D, int BS>
-cudaError_t launch(const Q8AppendParams &p, cudaStream_t stream)
+cudaError_t launch(const Q8AppendParams &p, int sms, cudaStream_t stream)
 {
-    // CTAs over the chunks, then over a chunk's tiles: one tile per warp for the number
-    // of blocks a chunk can be expected to touch
+    // Short runs (up to four rows per sequence on average, as in a decode step) take the
+    // variant that keeps four rows: more CTAs fit an SM, and a step's tiles all run at
+    // once.
+    const bool few = p.num_tokens <= 4ll * p.num_seqs;
+    // CTAs over the chunks, then over a chunk's tiles: at most one tile per warp for the
+    // number of blocks a chunk can be expected to touch, and no more than FILL CTAs per SM
+    // in all, so that long prompts' CTAs find their sequences once for several tiles each.
     const long long chunks = (p.num_tokens + kChunk - 1) / kChunk;
     const long long runs = p.query_start ? (p.num_tokens + BS - 1) / BS + p.num_seqs : p.num_tokens;
     const long long per_chunk = ((runs < p.num_tokens ? runs : p.num_tokens) + chunks - 1) / chunks;
-    const long long y = (per_chunk * 2 * p.num_kv_heads + kAppendWarps - 1) / kAppendWarps;
+    const long long most = (per_chunk * 2 * p.num_kv_heads + kAppendWarps - 1) / kAppendWarps;
+#ifndef FILL
+#define FILL 12
+#endif
+    const long long fill = ((long long)FILL * sms + chunks - 1) / chunks;
+    const long long y = most < fill ? most : fill;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -283,24 +311,26 @@ cudaError_t launch(const Q8AppendParams &p, cudaStream_t stream)
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, q8_append_kernel<T, D, BS>, p);
+    return few ? cudaLaunchKernelEx(&cfg, q8_append_kernel<T, D, BS, 4>, p)
+               : cudaLaunchKernelEx(&cfg, q8_append_kernel<T, D, BS, BS>, p);
 }
 
 template <typename T>
-cudaError_t dispatch(const Q8AppendParams &p, int head_dim, cudaStream_t stream)
+cudaError_t dispatch(const Q8AppendParams &p, int head_dim, int sms, cudaStream_t stream)
 {
     if (head_dim == 128)
-        return p.block_size == 16 ? launch<T, 128, 16>(p, stream) : launch<T, 128, 32>(p, stream);
-    return p.block_size == 16 ? launch<T, 64, 16>(p, stream) : launch<T, 64, 32>(p, stream);
+        return p.block_size == 16 ? launch<T, 128, 16>(p, sms, stream) : launch<T, 128, 32>(p, sms, stream);
+    return p.block_size == 16 ? launch<T, 64, 16>(p, sms, stream) : launch<T, 64, 32>(p, sms, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_q8_append(const Q8AppendParams &p, int head_dim, pa_dtype dtype, cudaStream_t stream)
+cudaError_t launch_q8_append(const Q8AppendParams &p, int head_dim, pa_dtype dtype, int sms,
+                             cudaStream_t stream)
 {
-    return dtype == PA_F32   ? dispatch<float>(p, head_dim, stream)
-           : dtype == PA_F16 ? dispatch<__half>(p, head_dim, stream)
-                             : dispatch<__nv_bfloat16>(p, head_dim, stream);
+    return dtype == PA_F32   ? dispatch<float>(p, head_dim, sms, stream)
+           : dtype == PA_F16 ? dispatch<__half>(p, head_dim, sms, stream)
+                             : dispatch<__nv_bfloat16>(p, head_dim, sms, stream);
 }
 
 }  // namespace pagedkv
