@@ -22,6 +22,7 @@ calls on tensors that are not CUDA tensors raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 from typing import List, Optional, Sequence, Tuple
@@ -666,17 +667,34 @@ def pa_scatter_blocks(staging_k, staging_v, k_cache, v_cache, block_ids, stream=
 # ----------------------------------------------------------------------------
 # the 8-bit cache, and tables built on the GPU
 # ----------------------------------------------------------------------------
+# (These calls take a few microseconds on the GPU for a small batch, so what the binding
+# looks up per call is looked up once: library functions, dtype codes, block sizes.)
+@functools.lru_cache(maxsize=None)
+def _fn(name: str):
+    return getattr(_load(), name)
+
+
+@functools.lru_cache(maxsize=None)
+def _dtypes():
+    import torch
+    return {torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16}
+
+
+def _code(t) -> int:
+    code = _dtypes().get(t.dtype)
+    return _dtype_code(t) if code is None else code
+
+
 def _on_device(names, tensors):
     """Checks that the tensors are contiguous and on one CUDA device; returns None when it is
     the current device, else a context that makes it so."""
     import torch
     dev = tensors[0].get_device()
     for name, t in zip(names, tensors):
-        if not t.is_cuda or not t.is_contiguous():
+        if t.get_device() != dev or not t.is_cuda or not t.is_contiguous():
             _cuda(t, name)
-        if t.get_device() != dev:
             raise ValueError(f"{name} is on cuda:{t.get_device()}, {names[0]} on cuda:{dev}")
-    return None if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+    return None if dev == torch._C._cuda_getDevice() else torch.cuda.device(dev)
 
 
 def _raw_stream(stream, tensor) -> int:
@@ -687,11 +705,14 @@ def _raw_stream(stream, tensor) -> int:
     return _stream(stream)
 
 
-def _call(fn, device, *args) -> int:
+def _call(name: str, device, *args) -> None:
     if device is None:
-        return fn(*args)
-    with device:
-        return fn(*args)
+        st = _fn(name)(*args)
+    else:
+        with device:
+            st = _fn(name)(*args)
+    if st != PA_OK:
+        _check(st, name)
 
 
 def _want(ok: bool, what: str) -> None:
@@ -747,7 +768,7 @@ def _check_batch(kv_cache, block_tables, context_lens, num_kv_heads, head_dim, b
 
 
 _APPEND_NAMES = ("k", "v", "kv_cache", "block_tables", "context_lens", "query_start")
-_DECODE_NAMES = ("out", "q", "kv_cache", "block_tables", "context_lens", "workspace")
+_DECODE_NAMES = ("out", "q", "kv_cache", "block_tables", "context_lens")
 _TABLE_NAMES = ("block_tables", "context_lens", "new_tokens", "free_list", "num_free", "query_start", "granted",
                 "context_lens_out", "num_free_out", "slot_mapping")
 
@@ -764,7 +785,7 @@ def pa_q8_append(k, v, kv_cache, block_tables, context_lens, block_size: int, qu
     n, hkv, d = k.shape
     S, W = block_tables.shape
     _check_batch(kv_cache, block_tables, context_lens, hkv, d, block_size)
-    names, tensors = _APPEND_NAMES, (k, v, kv_cache, block_tables, context_lens)
+    tensors = (k, v, kv_cache, block_tables, context_lens)
     qs_ptr = None
     if query_start is not None:
         if query_start.dtype != torch.int32:
@@ -772,11 +793,9 @@ def pa_q8_append(k, v, kv_cache, block_tables, context_lens, block_size: int, qu
         _want(query_start.shape == (S + 1,), "query_start must be [S + 1]")
         tensors += (query_start,)
         qs_ptr = query_start.data_ptr()
-    device = _on_device(names, tensors)
-    st = _call(_load().pa_q8_append, device, k.data_ptr(), v.data_ptr(), kv_cache.data_ptr(),
-               block_tables.data_ptr(), W, context_lens.data_ptr(), qs_ptr, S, n, kv_cache.shape[0], hkv, d,
-               block_size, _dtype_code(k), _raw_stream(stream, k))
-    _check(st, "pa_q8_append")
+    device = _on_device(_APPEND_NAMES, tensors)
+    _call("pa_q8_append", device, k.data_ptr(), v.data_ptr(), kv_cache.data_ptr(),
+          block_tables.data_ptr(), W, context_lens.data_ptr(), qs_ptr, S, n, kv_cache.shape[0], hkv, d, block_size, _code(k), _raw_stream(stream, k))
 
 
 def pa_q8_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
@@ -786,10 +805,6 @@ def pa_q8_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, b
     if n == ctypes.c_size_t(-1).value:
         raise PagedKVError(PA_ERR_INVALID, "pa_q8_decode_workspace_size")
     return n
-
-
-def _q8_scratch(S, hq, hkv, d, b, W, device, stream):
-    return _launch_scratch(pa_q8_decode_workspace_size(S, hq, hkv, d, b, W), device, stream)
 
 
 def pa_q8_decode(out, q, kv_cache, block_tables, context_lens, scale: float, num_q_heads: int,
@@ -803,15 +818,15 @@ def pa_q8_decode(out, q, kv_cache, block_tables, context_lens, scale: float, num
         raise TypeError("q and out must have one dtype")
     device = _on_device(_DECODE_NAMES, (out, q, kv_cache, block_tables, context_lens))
     if workspace is None:
-        workspace = _call(_q8_scratch, device, S, num_q_heads, num_kv_heads, head_dim, block_size, W, q.device,
-                          stream)
-    else:
-        _on_device(_DECODE_NAMES[5:] + _DECODE_NAMES[:1], (workspace, out))
-    st = _call(_load().pa_q8_decode, device, out.data_ptr(), q.data_ptr(), kv_cache.data_ptr(),
-               block_tables.data_ptr(), W, context_lens.data_ptr(), S, kv_cache.shape[0], float(scale), num_q_heads,
-               num_kv_heads, head_dim, block_size, _dtype_code(q), workspace.data_ptr(),
-               workspace.numel() * workspace.element_size(), _raw_stream(stream, q))
-    _check(st, "pa_q8_decode")
+        with device or contextlib.nullcontext():
+            workspace = _launch_scratch(pa_q8_decode_workspace_size(S, num_q_heads, num_kv_heads, head_dim,
+                                                                    block_size, W), q.device, stream)
+    elif workspace.get_device() != q.get_device() or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on the device of q")
+    _call("pa_q8_decode", device, out.data_ptr(), q.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(), W,
+          context_lens.data_ptr(), S, kv_cache.shape[0], float(scale), num_q_heads, num_kv_heads, head_dim,
+          block_size, _code(q), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+          _raw_stream(stream, q))
     return out
 
 
@@ -825,9 +840,8 @@ def pa_q8_copy_blocks(kv_cache, src_dst_pairs, stream=None):
     if n == 0:
         return
     device = _on_device(("kv_cache", "src_dst_pairs"), (kv_cache, src_dst_pairs))
-    st = _call(_load().pa_q8_copy_blocks, device, kv_cache.data_ptr(), src_dst_pairs.data_ptr(), n,
-               kv_cache.shape[0], _block_bytes(kv_cache), _raw_stream(stream, kv_cache))
-    _check(st, "pa_q8_copy_blocks")
+    _call("pa_q8_copy_blocks", device, kv_cache.data_ptr(), src_dst_pairs.data_ptr(), n, kv_cache.shape[0],
+          _block_bytes(kv_cache), _raw_stream(stream, kv_cache))
 
 
 def pa_q8_swap_blocks(src_cache, dst_cache, src_dst_pairs, stream=None):
@@ -866,18 +880,17 @@ def pa_build_tables(block_tables, context_lens, new_tokens, free_list, num_free,
     if slot_mapping.dtype != torch.int64:
         raise TypeError("slot_mapping must be int64")
     S, W = block_tables.shape
-    _want(context_lens.shape == (S,) and new_tokens.shape == (S,) and granted.shape == (S,) and
-          context_lens_out.shape == (S,), "context_lens, new_tokens, granted and context_lens_out must be [S]")
+    one = (S,)
+    _want(context_lens.shape == one and new_tokens.shape == one and granted.shape == one and
+          context_lens_out.shape == one, "context_lens, new_tokens, granted and context_lens_out must be [S]")
     _want(query_start.shape == (S + 1,), "query_start must be [S + 1]")
     _want(num_free.numel() == 1 and num_free_out.numel() == 1, "num_free and num_free_out hold one number")
     _want(free_list.dim() == 1 and slot_mapping.dim() == 1, "free_list and slot_mapping must have one dimension")
     device = _on_device(_TABLE_NAMES, tensors)
-    st = _call(_load().pa_build_tables, device, block_tables.data_ptr(), W, context_lens_out.data_ptr(),
-               context_lens.data_ptr(), new_tokens.data_ptr(), S, free_list.data_ptr(), free_list.shape[0],
-               num_free_out.data_ptr(), num_free.data_ptr(), block_size, granted.data_ptr(),
-               query_start.data_ptr(), slot_mapping.data_ptr(), slot_mapping.shape[0],
-               _raw_stream(stream, block_tables))
-    _check(st, "pa_build_tables")
+    _call("pa_build_tables", device, block_tables.data_ptr(), W, context_lens_out.data_ptr(),
+          context_lens.data_ptr(), new_tokens.data_ptr(), S, free_list.data_ptr(), free_list.shape[0],
+          num_free_out.data_ptr(), num_free.data_ptr(), block_size, granted.data_ptr(), query_start.data_ptr(),
+          slot_mapping.data_ptr(), slot_mapping.shape[0], _raw_stream(stream, block_tables))
 
 
 def pa_kv_transfer_worthwhile(reusable_tokens: int, threshold_tokens: int = 64) -> bool:

@@ -135,17 +135,24 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio)
     return encode4(f0.x * ratio, f0.y * ratio, f1.x * ratio, f1.y * ratio);
 }
 
+constexpr int hold(int rows, int elem_bytes, int head_dim)  // loads of 16 bytes that a lane keeps
+{
+    return rows * head_dim * elem_bytes / 512 < 16 ? rows * head_dim * elem_bytes / 512 : 16;
+}
+
 // kRows: rows of a run whose loads are kept in registers, and all in flight at once; a
-// longer run's other rows are read twice.
+// longer run's other rows are read twice.  Up to eight loads per lane leave room for four
+// CTAs on an SM (16 prompts, 40 heads, 16-row blocks: 92 us with two, 81 with three, 80
+// with four).
 template <typename T, int D, int BS, int kRows>
-__global__ void __launch_bounds__(32 * kAppendWarps, kRows == BS ? 2 : 4)
+__global__ void __launch_bounds__(32 * kAppendWarps, hold(kRows, sizeof(T), D) <= 8 ? 4 : 2)
     q8_append_kernel(const __grid_constant__ Q8AppendParams p)
 {
     constexpr int E = 16 / (int)sizeof(T);    // elements of a 16-byte load
     constexpr int LR = D / E;                 // lanes on one row
     constexpr int RP = 32 / LR;               // rows a warp loads at once
     constexpr int kPasses = BS / RP;
-    constexpr int kHold = kRows / RP < 16 ? kRows / RP : 16;
+    constexpr int kHold = hold(kRows, sizeof(T), D);
     static_assert(kHold >= 1, "a load at least");
     __shared__ Run runs[kChunk];
     __shared__ int num_runs;
@@ -291,16 +298,14 @@ cudaError_t launch(const Q8AppendParams &p, int sms, cudaStream_t stream)
     // once.
     const bool few = p.num_tokens <= 4ll * p.num_seqs;
     // CTAs over the chunks, then over a chunk's tiles: at most one tile per warp for the
-    // number of blocks a chunk can be expected to touch, and no more than FILL CTAs per SM
-    // in all, so that long prompts' CTAs find their sequences once for several tiles each.
+    // number of blocks a chunk can be expected to touch, and no more than twelve CTAs per
+    // SM in all, so that long prompts' CTAs find their sequences once for several tiles
+    // each (16 prompts, 40 heads: 96, 92 and 95 us with 6, 12 and 20).
     const long long chunks = (p.num_tokens + kChunk - 1) / kChunk;
     const long long runs = p.query_start ? (p.num_tokens + BS - 1) / BS + p.num_seqs : p.num_tokens;
     const long long per_chunk = ((runs < p.num_tokens ? runs : p.num_tokens) + chunks - 1) / chunks;
     const long long most = (per_chunk * 2 * p.num_kv_heads + kAppendWarps - 1) / kAppendWarps;
-#ifndef FILL
-#define FILL 12
-#endif
-    const long long fill = ((long long)FILL * sms + chunks - 1) / chunks;
+    const long long fill = (12ll * sms + chunks - 1) / chunks;
     const long long y = most < fill ? most : fill;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
