@@ -64,7 +64,12 @@ namespace pagedkv {
 template <typename T, int D, int BS, int NT>
 struct Cfg8 {
     static constexpr int kCtas = sizeof(T) == 4 && NT == 2 ? 1 : 2;
-    static constexpr int kRing = kCtas == 1 ? 131072 : NT == 2 && D == 128 ? 65536 : PA_Q8_RING_BYTES;
+    static constexpr int kRing = kCtas == 1                                    ? 131072
+                                 : D == 128 && (NT == 2 || sizeof(T) == 4) ? 65536
+                                                                           : PA_Q8_RING_BYTES;
+    // Item descriptors in flight: one per consumer warp where a warp may have an item to
+    // itself, room permitting.
+    static constexpr int kSlots = NT == 1 ? 4 : kItemSlots;
     static constexpr int kTile = BS * D;          // K (or V) codes of one (block, kv head)
     static constexpr int kRecord = 2 * kTile;     // K tile, then V tile
     static constexpr int kStageTokens = PA_Q8_STAGE_TOKENS;
@@ -90,8 +95,8 @@ constexpr int kThreads8 = kThreads + 32;  // one warp more than pa_decode: the s
 
 // Shared memory: as make_layout, with 8 bytes of scales per block of a stage in the
 // place of the fused append's rows.
-__host__ __device__ inline SmemLayout make_layout8(int stages, int stage_bytes, int bps, int rows, int D,
-                                                   int elem_bytes)
+__host__ __device__ inline SmemLayout make_layout8(int stages, int stage_bytes, int bps, int slots, int rows,
+                                                   int D, int elem_bytes)
 {
     SmemLayout L;
     uint32_t o = (uint32_t)stages * (uint32_t)stage_bytes;
@@ -102,18 +107,18 @@ __host__ __device__ inline SmemLayout make_layout8(int stages, int stage_bytes, 
     o = (o + 127u) & ~127u;
     L.pfx = o;
     L.items = o;
-    o += kItemSlots * 64u;
+    o += (uint32_t)slots * 64u;
     L.q = o;
-    o += (uint32_t)(kItemSlots * (rows <= kNarrowRows ? kNarrowRows : kHeadsPerItem) * D * elem_bytes);
+    o += (uint32_t)(slots * (rows <= kNarrowRows ? kNarrowRows : kHeadsPerItem) * D * elem_bytes);
     L.newrow = o;  // the scales
     o += (uint32_t)(stages * bps * 8);
     L.newinfo = o;
     o = (o + 15u) & ~15u;
     L.bars = o;  // as make_layout's, then one per stage for its scales
-    o += (3u * (uint32_t)stages + 2u * kItemSlots + 1u) * 8u;
+    o += (3u * (uint32_t)stages + 2u * (uint32_t)slots + 1u) * 8u;
     o = (o + 15u) & ~15u;
-    L.flag = o;
-    o += 16u + 4u * kConsumerWarps;
+    L.flag = o;  // as make_layout's, then a second merge flag
+    o += 16u + 4u * kConsumerWarps + 4u;
     o = (o + 15u) & ~15u;
     L.blk = o;
     o += 32u * 4u;
@@ -154,10 +159,10 @@ struct Producer8 {
     __device__ bool emit(const Item &it)
     {
         constexpr uint32_t kQSlotBytes = NT * 8 * D * sizeof(T);
-        const uint32_t slot = n % kItemSlots;
+        const uint32_t slot = n % C::kSlots;
         int ok = 1;
         if (lane == 0) {
-            ok = wait_slot(&c.item_empty[slot], ((n / kItemSlots) & 1u) ^ 1u);
+            ok = wait_slot(&c.item_empty[slot], ((n / C::kSlots) & 1u) ^ 1u);
             if (ok) {
                 c.items[slot] = it;
                 const uint32_t bytes = (uint32_t)it.rows * D * sizeof(T);
@@ -228,12 +233,12 @@ struct Producer8 {
     {
         if (lane != 0)
             return;
-        for (uint32_t k = n > kItemSlots ? n - kItemSlots : 0; k < n; ++k)
-            dev::mbar_wait(dev::smem_addr(&c.item_full[k % kItemSlots]), (k / kItemSlots) & 1u,
+        for (uint32_t k = n > C::kSlots ? n - C::kSlots : 0; k < n; ++k)
+            dev::mbar_wait(dev::smem_addr(&c.item_full[k % C::kSlots]), (k / C::kSlots) & 1u,
                            kWaitTimeoutNs);
         if (!failed) {
-            const uint32_t slot = n % kItemSlots;
-            if (wait_slot(&c.item_empty[slot], ((n / kItemSlots) & 1u) ^ 1u)) {
+            const uint32_t slot = n % C::kSlots;
+            if (wait_slot(&c.item_empty[slot], ((n / C::kSlots) & 1u) ^ 1u)) {
                 c.items[slot].seq = -1;
                 dev::mbar_arrive(dev::smem_addr(&c.item_full[slot]));
             } else {
@@ -333,14 +338,41 @@ __device__ __forceinline__ void load_row(float (&x)[N], const T *src)
     }
 }
 
+// Four consecutive outputs in the storage type.
+template <typename T>
+__device__ __forceinline__ void store4(T *dst, const float (&x)[4])
+{
+    if constexpr (sizeof(T) == 4)
+        *reinterpret_cast<float4 *>(dst) = make_float4(x[0], x[1], x[2], x[3]);
+    else
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(dev::Mma<T>::pack(x[0], x[1]), dev::Mma<T>::pack(x[2], x[3]));
+}
+
+// Hand an item slot back, once every read of it has completed: `all` is made of what the
+// warp's lanes read of the query rows.
+__device__ __forceinline__ void release_item(const CtaState &c, const Item &it, uint32_t slot, int warp, int lane,
+                                             uint32_t all)
+{
+    all ^= (uint32_t)(it.seq ^ it.kvh ^ it.hg ^ it.len ^ it.j0 ^ it.j1 ^ it.qrow0 ^ it.rows ^ it.partial ^
+                      it.prow0 ^ it.tseq ^ it.packed ^ it.c_first ^ it.nparts) ^
+           it.total_lo ^ it.total_hi;
+    all = __reduce_xor_sync(0xffffffffu, all);
+    if (lane == 0)
+        dev::settle_loads(&c.sink[warp], all);
+    __syncwarp();
+    if (lane == 0)
+        dev::mbar_arrive(dev::smem_addr(&c.item_empty[slot]));
+}
+
 // ---------------------------------------------------------------------------
 // One item on one consumer warp (its share of the item's stages).  NT: 8-row groups of
-// query rows.  Ends with the warp's partial rows in its merge area.
+// query rows.  Ends with the warp's partial rows in its merge area or, `alone`, with the
+// item's output.
 // ---------------------------------------------------------------------------
 template <typename T, int D, int BS, int NT>
 __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaState &c, const Item &it,
                                               uint64_t *sfull, uint32_t slot, uint32_t &g, int warp, int lane,
-                                              int rows_cap)
+                                              int rows_cap, bool alone)
 {
     using C = Cfg8<T, D, BS, NT>;
     constexpr bool kSplit = sizeof(T) == 4;  // two fp16 terms for q and p
@@ -360,9 +392,7 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
     uint32_t qb[NT][QT][KS][2];
     float fa[NT], fb[NT];
     {
-        uint32_t all = (uint32_t)(it.seq ^ it.kvh ^ it.hg ^ it.len ^ it.j0 ^ it.j1 ^ it.qrow0 ^ it.rows ^
-                                  it.partial ^ it.prow0 ^ it.tseq ^ it.packed ^ it.c_first ^ it.nparts) ^
-                       it.total_lo ^ it.total_hi;
+        uint32_t all = 0;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float x[D / 4];
@@ -400,13 +430,7 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
             fa[nt] = __shfl_sync(0xffffffffu, down, 8 * q4) * p.scale_log2;
             fb[nt] = __shfl_sync(0xffffffffu, down, 8 * q4 + 4) * p.scale_log2;
         }
-        // every read of the slot has completed before it is handed back
-        all = __reduce_xor_sync(0xffffffffu, all);
-        if (lane == 0)
-            dev::settle_loads(&c.sink[warp], all);
-        __syncwarp();
-        if (lane == 0)
-            dev::mbar_arrive(dev::smem_addr(&c.item_empty[slot]));
+        release_item(c, it, slot, warp, lane, all);
     }
 
     float o[NT][DM][4];
@@ -644,7 +668,13 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
                 mine[rb * SA + dm * 16 + r8 + 8] = o[nt][dm][3] * (1.f / kUp) * vref;
             }
         }
-        if (r8 == 0) {
+        if (NT == 1 && alone) {
+            // the rows' sums, behind the rows
+            if (r8 == 0 && ra < it.rows)
+                mine[ra * SA + D] = sa;
+            if (r8 == 0 && rb < it.rows)
+                mine[rb * SA + D] = sb;
+        } else if (r8 == 0) {
             // a NaN score makes the sum and every output NaN; the merge takes such a
             // row with a sum of 1, so that the NaN outputs, not the sum, carry it on
             const bool na = sa != sa, nb = sb != sb;
@@ -656,17 +686,22 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
             c.mml[(warp * kHeadsPerItem + rb) * 2 + 1] = nb ? 1.f : sb;
         }
     }
+    if (NT == 1 && alone) {
+        __syncwarp();
+        constexpr int LR = D / 4;  // lanes on a row
+        for (int r = lane / LR; r < it.rows; r += 32 / LR) {
+            const int col = lane % LR * 4;
+            const float4 v = *reinterpret_cast<const float4 *>(&mine[r * SA + col]);
+            const float L = mine[r * SA + D];
+            float y[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                y[e] = L == 0.f ? 0.f : y[e] / L;
+            store4(reinterpret_cast<T *>(p.out) + ((size_t)it.seq * p.num_q_heads + it.qrow0 + r) * D + col, y);
+        }
+        __syncwarp();  // read before the next item's take their place
+    }
     return true;
-}
-
-// Four consecutive outputs in the storage type.
-template <typename T>
-__device__ __forceinline__ void store4(T *dst, const float (&x)[4])
-{
-    if constexpr (sizeof(T) == 4)
-        *reinterpret_cast<float4 *>(dst) = make_float4(x[0], x[1], x[2], x[3]);
-    else
-        *reinterpret_cast<uint2 *>(dst) = make_uint2(dev::Mma<T>::pack(x[0], x[1]), dev::Mma<T>::pack(x[2], x[3]));
 }
 
 // ---------------------------------------------------------------------------
@@ -850,11 +885,18 @@ __global__ void __launch_bounds__(kThreads8, Cfg8<T, D, BS, NT>::kCtas)
     uint8_t *smem =
         reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int rows_cap = item_rows_cap(p);
-    const SmemLayout lay = make_layout8(C::kStages, C::kStageBytes, C::kBPS, rows_cap, D, sizeof(T));
-    const CtaState c = cta_state(smem, lay, C::kStages);
+    const SmemLayout lay = make_layout8(C::kStages, C::kStageBytes, C::kBPS, C::kSlots, rows_cap, D, sizeof(T));
+    CtaState c = cta_state(smem, lay, C::kStages);
+    c.item_empty = c.item_full + C::kSlots;
+    c.csync = c.item_empty + C::kSlots;
     uint64_t *const sfull = c.csync + 1;
+    // (init_cta knows kItemSlots item slots and no scale barriers)
     if (threadIdx.x < C::kStages)
         dev::mbar_init(dev::smem_addr(&sfull[threadIdx.x]), 1);
+    if (threadIdx.x >= kItemSlots && threadIdx.x < C::kSlots) {
+        dev::mbar_init(dev::smem_addr(&c.item_full[threadIdx.x]), 1);
+        dev::mbar_init(dev::smem_addr(&c.item_empty[threadIdx.x]), kConsumerWarps);
+    }
     dev::fence_mbar_init();
     init_cta(p, c, C::kStages);
 
@@ -871,17 +913,41 @@ __global__ void __launch_bounds__(kThreads8, Cfg8<T, D, BS, NT>::kCtas)
         walk_balanced<kModePlain>(p, BS, C::kBPS, sw, lane);
         return;
     }
+    // Two merge flags in turn: warp 0 may set the next item's while another warp has yet to
+    // read this one's (it cannot be two ahead: the barrier between takes every warp).
+    volatile int *merge_now = c.merge;
+    volatile int *merge_next = reinterpret_cast<volatile int *>(smem + lay.flag + 16 + 4 * kConsumerWarps);
     uint32_t g = 0;    // stages consumed (same count in every warp)
     uint32_t sph = 0;  // consumer barrier phase
     for (uint32_t n = 0;; ++n) {
-        const uint32_t slot = n % kItemSlots;
-        if (!warp_wait(p, c, &c.item_full[slot], (n / kItemSlots) & 1u))
+        const uint32_t slot = n % C::kSlots;
+        if (!warp_wait(p, c, &c.item_full[slot], (n / C::kSlots) & 1u))
             break;
         const Item it = load_item(&c.items[slot]);
         if (it.seq < 0)
             break;
-        if (!consume_item8<T, D, BS, NT>(p, c, it, sfull, slot, g, warp, lane, rows_cap))
+        // A whole unit of at most one stage belongs to one warp, from the query rows to
+        // the output, and the warps go on to the next items without meeting (400 sequences
+        // of 20 tokens, 8 heads: 39 us to 23).  With 9 heads or more per kv head there
+        // are few such items, and the code for them costs registers that are short.
+        const bool alone = NT == 1 && !it.partial && it.j1 - it.j0 <= C::kBPS;
+        if (alone && warp != it.rot()) {
+            release_item(c, it, slot, warp, lane, 0u);
+            g += it.j1 > it.j0 ? 1 : 0;
+            if (*c.abort)
+                break;
+            continue;
+        }
+        if (!consume_item8<T, D, BS, NT>(p, c, it, sfull, slot, g, warp, lane, rows_cap, alone))
             break;
+        if (alone) {
+            if (*c.abort)
+                break;
+            continue;
+        }
+        c.merge = merge_now;
+        merge_now = merge_next;
+        merge_next = c.merge;
         if (threadIdx.x == 0)
             probe_split_last(p, it, c);
         if (!consumer_sync(p, c, sph))
@@ -901,8 +967,8 @@ cudaError_t launch_q8_impl(const Q8Launch &L, cudaStream_t stream)
     const DecodeParams &p = L.p;
     void *kern = reinterpret_cast<void *>(&pa_q8_decode_kernel<T, D, BS, NT>);
     const size_t smem =
-        make_layout8(C::kStages, C::kStageBytes, C::kBPS, item_rows_cap(p), D, sizeof(T)).total;
-    const size_t smem_max = make_layout8(C::kStages, C::kStageBytes, C::kBPS, NT * 8, D, sizeof(T)).total;
+        make_layout8(C::kStages, C::kStageBytes, C::kBPS, C::kSlots, item_rows_cap(p), D, sizeof(T)).total;
+    const size_t smem_max = make_layout8(C::kStages, C::kStageBytes, C::kBPS, C::kSlots, NT * 8, D, sizeof(T)).total;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
