@@ -190,8 +190,7 @@ __device__ __forceinline__ void ldsm_b8_x2_trans(uint32_t addr, uint32_t &r0, ui
 {
     asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
-                 : "r"(addr)
-                 : "memory");
+                 : "r"(addr));
 }
 
 // Two e4m3 codes (the low 16 bits of x) as two fp16 values: exact.

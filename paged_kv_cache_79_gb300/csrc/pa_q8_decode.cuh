@@ -364,15 +364,25 @@ __device__ __forceinline__ void release_item(const CtaState &c, const Item &it, 
         dev::mbar_arrive(dev::smem_addr(&c.item_empty[slot]));
 }
 
+// The codes of V tokens 16 mt .. + 15 of a stage, dims 32 dp .. + 31 (two 16 x 16 matrices),
+// transposed.
+template <int D, int BS>
+__device__ __forceinline__ void load_v(uint32_t (&v)[4], const uint8_t *vstage, int record, int mt, int dp, int lane)
+{
+    const uint8_t *vt = vstage + (mt * 16 / BS) * record;
+    dev::ldsm_b8_x2_trans(dev::smem_addr(vt + tile_unit<D>(mt * 16 % BS + (lane & 15), 2 * dp + (lane >> 4))),
+                          v[0], v[1], v[2], v[3]);
+}
+
 // ---------------------------------------------------------------------------
 // One item on one consumer warp (its share of the item's stages).  NT: 8-row groups of
 // query rows.  Ends with the warp's partial rows in its merge area or, `alone`, with the
-// item's output.
+// item's output.  `seen`: the counter of a split unit, read by thread 0 on the way.
 // ---------------------------------------------------------------------------
 template <typename T, int D, int BS, int NT>
 __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaState &c, const Item &it,
                                               uint64_t *sfull, uint32_t slot, uint32_t &g, int warp, int lane,
-                                              int rows_cap, bool alone)
+                                              int rows_cap, bool alone, unsigned long long &seen)
 {
     using C = Cfg8<T, D, BS, NT>;
     constexpr bool kSplit = sizeof(T) == 4;  // two fp16 terms for q and p
@@ -381,6 +391,7 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
     constexpr int MT = TS / 16;   // 16-token tiles of a stage
     constexpr int KS = D / 16;    // k-steps of K Q^T = words of a lane's share of a K row
     constexpr int DM = D / 16;    // 16-dim tiles of O^T
+    constexpr bool kEarlyV = NT == 1 && !kSplit;
     constexpr int SA = D + kAccPad;
     constexpr uint32_t kQSlotBytes = NT * 8 * D * sizeof(T);
     constexpr float kUp = 16384.f;  // 2^14: p's factor in the products
@@ -444,9 +455,16 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
             o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
     }
     float vref = FLT_MIN;  // largest vs so far (its inverse is finite, also for scales of 0)
+    float vinv = 1.f / FLT_MIN;
     const int rot = it.rot();
     const int stages = (it.j1 - it.j0 + C::kBPS - 1) / C::kBPS;
-    for (int i = (warp - rot) & (kConsumerWarps - 1); i < stages; i += kConsumerWarps) {
+    int i = (warp - rot) & (kConsumerWarps - 1);
+    if (i >= stages && threadIdx.x == 0 && it.partial)
+        seen = *reinterpret_cast<volatile unsigned long long *>(p.counters + it.c_first);
+    for (; i < stages; i += kConsumerWarps) {
+        // the counter is read behind the warp's last stage, and looked at after it
+        if (i + kConsumerWarps >= stages && threadIdx.x == 0 && it.partial)
+            seen = *reinterpret_cast<volatile unsigned long long *>(p.counters + it.c_first);
         const int j = it.j0 + i * C::kBPS;
         const uint32_t st = (g + i) % C::kStages, phase = ((g + i) / C::kStages) & 1u;
         if (!warp_wait(p, c, &sfull[st], phase) || !warp_wait(p, c, &c.full[st], phase))
@@ -465,82 +483,95 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
             vmax = fmaxf(vmax, vscale[b]);
         }
 
-        // S^T = K Q^T
-        float s[MT][NT][4];
+        // S^T = K Q^T.  All of a stage's K is read first, and its tiles take turns, even and
+        // odd k-steps in accumulators of their own, so that no product waits for the one
+        // before it.
+        uint32_t w[MT][2][KS];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             const uint8_t *kt = stage + (mt * 16 / BS) * C::kRecord;
             const int tk = mt * 16 % BS + tok0;
-            uint32_t w0[KS], w1[KS];
 #pragma unroll
             for (int u = 0; u < D / 64; ++u) {
                 const int unit = q4 * (D / 64) + u;
-                *reinterpret_cast<uint4 *>(&w0[4 * u]) =
+                *reinterpret_cast<uint4 *>(&w[mt][0][4 * u]) =
                     *reinterpret_cast<const uint4 *>(kt + tile_unit<D>(tk, unit));
-                *reinterpret_cast<uint4 *>(&w1[4 * u]) =
+                *reinterpret_cast<uint4 *>(&w[mt][1][4 * u]) =
                     *reinterpret_cast<const uint4 *>(kt + tile_unit<D>(tk + 2, unit));
             }
-            // even and odd k-steps into accumulators of their own: shorter chains
-            float s2[NT][2][4];
+        }
+        float s[MT][NT][4], s1[MT][NT][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    s2[nt][0][e] = s2[nt][1][e] = 0.f;
+                    s[mt][nt][e] = s1[mt][nt][e] = 0.f;
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
+        for (int ks = 0; ks < KS; ++ks) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
                 uint32_t a[4];
-                dev::e4m3x4_to_f16x4(w0[ks], a[0], a[2]);
-                dev::e4m3x4_to_f16x4(w1[ks], a[1], a[3]);
+                dev::e4m3x4_to_f16x4(w[mt][0][ks], a[0], a[2]);
+                dev::e4m3x4_to_f16x4(w[mt][1][ks], a[1], a[3]);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int t = 0; t < QT; ++t)
-                        dev::Mma<__half>::run(s2[nt][ks & 1], a, qb[nt][t][ks][0], qb[nt][t][ks][1]);
+                        dev::Mma<__half>::run(ks & 1 ? s1[mt][nt] : s[mt][nt], a, qb[nt][t][ks][0],
+                                              qb[nt][t][ks][1]);
             }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    s[mt][nt][e] = s2[nt][0][e] + s2[nt][1][e];
         }
 
-        // scale, mask, maximum; a new reference where a score passes the old by more
-        // than 1
+        // V's codes, on their way while the softmax runs (where registers allow)
+        uint32_t v[kEarlyV ? MT : 1][kEarlyV ? DM / 2 : 1][4];
+        if constexpr (kEarlyV) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int dp = 0; dp < DM / 2; ++dp)
+                    load_v<D, BS>(v[mt][dp], stage + C::kTile, C::kRecord, mt, dp, lane);
+        }
+
+        // Scale and mask.  A lane compares its own scores with the reference: only where
+        // one passes it by more than 1 do the lanes look for the maximum, and the warp
+        // takes a new reference.
         bool raise = vmax > vref;
-        float xa[NT], xb[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            float mxa = -INFINITY, mxb = -INFINITY;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
                 const float ksc = kscale[mt * 16 / BS];
                 const float ga = fa[nt] * ksc, gb = fb[nt] * ksc;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    s[mt][nt][2 * h] *= ga;
-                    s[mt][nt][2 * h + 1] *= gb;
+                    float &xa = s[mt][nt][2 * h], &xb = s[mt][nt][2 * h + 1];
+                    xa = (xa + s1[mt][nt][2 * h]) * ga;
+                    xb = (xb + s1[mt][nt][2 * h + 1]) * gb;
                     if (partial && mt * 16 + tok0 + 2 * h >= valid)
-                        s[mt][nt][2 * h] = s[mt][nt][2 * h + 1] = -INFINITY;
-                    mxa = fmaxf(mxa, s[mt][nt][2 * h]);
-                    mxb = fmaxf(mxb, s[mt][nt][2 * h + 1]);
+                        xa = xb = -INFINITY;
+                    raise |= xa > ma[nt] + 1.f || xb > mb[nt] + 1.f;
                 }
             }
-#pragma unroll
-            for (int o_ = 4; o_ < 32; o_ <<= 1) {
-                mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, o_));
-                mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, o_));
-            }
-            xa[nt] = mxa;
-            xb[nt] = mxb;
-            raise |= mxa > ma[nt] + 1.f || mxb > mb[nt] + 1.f;
         }
         if (__any_sync(0xffffffffu, raise)) {
             const float cv = vref / vmax;
             vref = vmax;
+            vinv = 1.f / vref;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const float na = fmaxf(ma[nt], xa[nt]), nb = fmaxf(mb[nt], xb[nt]);
+                float na = ma[nt], nb = mb[nt];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    na = fmaxf(na, fmaxf(s[mt][nt][0], s[mt][nt][2]));
+                    nb = fmaxf(nb, fmaxf(s[mt][nt][1], s[mt][nt][3]));
+                }
+#pragma unroll
+                for (int o_ = 4; o_ < 32; o_ <<= 1) {
+                    na = fmaxf(na, __shfl_xor_sync(0xffffffffu, na, o_));
+                    nb = fmaxf(nb, __shfl_xor_sync(0xffffffffu, nb, o_));
+                }
                 // (no finite score yet: nothing to rescale)
                 const float ca = ma[nt] == -INFINITY ? 0.f : exp2f(ma[nt] - na);
                 const float cb = mb[nt] == -INFINITY ? 0.f : exp2f(mb[nt] - nb);
@@ -557,7 +588,6 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
                 }
             }
         }
-        const float vinv = 1.f / vref;
 
         // P^T as the B operand: exp2, times 2^14 vs / vref, rounded, transposed
         uint32_t pb[MT][NT][QT][2];
@@ -597,24 +627,22 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
             }
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-                const uint8_t *vt = stage + (mt * 16 / BS) * C::kRecord + C::kTile;
-                uint32_t v[4];
-                dev::ldsm_b8_x2_trans(
-                    dev::smem_addr(vt + tile_unit<D>(mt * 16 % BS + (lane & 15), 2 * dp + (lane >> 4))), v[0], v[1],
-                    v[2], v[3]);
+                uint32_t (&x)[4] = v[kEarlyV ? mt : 0][kEarlyV ? dp : 0];
+                if constexpr (!kEarlyV)
+                    load_v<D, BS>(x, stage + C::kTile, C::kRecord, mt, dp, lane);
                 if (partial) {
                     // rows past the context may hold anything (NaN): zero their codes
                     const int left = min(max(valid - mt * 16 - 4 * q4, 0), 4);
                     const uint32_t keep = left == 4 ? 0xffffffffu : (1u << (8 * left)) - 1u;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        v[e] &= keep;
+                        x[e] &= keep;
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint32_t a[4];
-                    dev::e4m3x4_to_f16x4(v[2 * h], a[0], a[2]);
-                    dev::e4m3x4_to_f16x4(v[2 * h + 1], a[1], a[3]);
+                    dev::e4m3x4_to_f16x4(x[2 * h], a[0], a[2]);
+                    dev::e4m3x4_to_f16x4(x[2 * h + 1], a[1], a[3]);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -707,17 +735,23 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
 // ---------------------------------------------------------------------------
 // Merge the four consumer states of one item and store it, as finalize_item does, four
 // columns per thread and D / 4 threads per row, so that a row's weights are computed
-// once per thread (2.3 us to 0.4 us per 8-row item).  With own_in_smem the rows stay in
-// the first warp's accumulator rows and their log2-sum-exp in its `ml` entries.
+// once per thread.  `other` >= 0: the item completes a unit cut once; the other part's
+// rows lie there, and the merged rows go to the output at once.
 // ---------------------------------------------------------------------------
 template <typename T, int D>
-__device__ __forceinline__ void finalize8(const DecodeParams &p, const Item &it, float *acc, float *ml,
-                                          int rows_cap, int tid, bool own_in_smem)
+__device__ __forceinline__ void finalize8(const DecodeParams &p, const Item &it, const float *acc, const float *ml,
+                                          int rows_cap, int tid, int other)
 {
     constexpr int S = D + kAccPad;
     constexpr int LR = D / 4;  // threads on a row: a warp or half of one
     for (int r = tid / LR; r < it.rows; r += 32 * kConsumerWarps / LR) {
         const int col = tid % LR * 4;
+        float lse2 = -INFINITY;
+        float4 o2 = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (other >= 0) {
+            lse2 = __ldcg(p.part_lse + other + r);
+            o2 = __ldcg(reinterpret_cast<const float4 *>(p.part_o + (size_t)(other + r) * D + col));
+        }
         float mc[kConsumerWarps], lc[kConsumerWarps];
         float4 v[kConsumerWarps];
         float M = -INFINITY;
@@ -745,134 +779,136 @@ __device__ __forceinline__ void finalize8(const DecodeParams &p, const Item &it,
         for (int e = 0; e < 4; ++e)
             o[e] = L > 0.f ? o[e] / L : 0.f;
         const float lse = L > 0.f ? M + log2f(L) : -INFINITY;
-        if (!it.partial) {
-            store4(reinterpret_cast<T *>(p.out) + ((size_t)it.seq * p.num_q_heads + it.qrow0 + r) * D + col, o);
-        } else if (own_in_smem) {
-            *reinterpret_cast<float4 *>(&acc[r * S + col]) = make_float4(o[0], o[1], o[2], o[3]);
-            // every lane on the row has read its entries
-            __syncwarp(LR == 32 ? 0xffffffffu : 0xffffu << (tid & 16));
-            if (col == 0)
-                ml[r * 2] = lse;
-        } else {
+        if (it.partial && other < 0) {
             const size_t pr = (size_t)it.prow0 + r;
             *reinterpret_cast<float4 *>(p.part_o + pr * D + col) = make_float4(o[0], o[1], o[2], o[3]);
             if (col == 0)
                 p.part_lse[pr] = lse;
+            continue;
         }
+        if (other >= 0) {
+            const float m2 = fmaxf(lse, lse2);
+            const float w0 = exp2f(lse - m2), w1 = exp2f(lse2 - m2), W = w0 + w1;
+            o[0] = (w0 * o[0] + w1 * o2.x) / W;
+            o[1] = (w0 * o[1] + w1 * o2.y) / W;
+            o[2] = (w0 * o[2] + w1 * o2.z) / W;
+            o[3] = (w0 * o[3] + w1 * o2.w) / W;
+        }
+        store4(reinterpret_cast<T *>(p.out) + ((size_t)it.seq * p.num_q_heads + it.qrow0 + r) * D + col, o);
     }
 }
 
 // Merge the nparts <= 32 partials of a split unit into its output rows, as
-// merge_split_unit does, with all of a warp's rows and up to four parts of each in flight
-// at once instead of one row after the other (six parts of 13 rows: 8 us to 3).  own: the
-// unit is completed by its own second part, whose rows finalize8 left in acc and ml.
-template <typename T, int D, int NT>
-__device__ __forceinline__ void merge8(const DecodeParams &p, const Item &it, int warp, int lane,
-                                       const float *acc, const float *ml, bool own)
+// merge_split_unit does, RW rows and up to four parts of each in flight at once instead
+// of one row after the other (six parts of 13 rows: 8 us to 3).  The calling warp does
+// rows row, row + step, ...
+template <typename T, int D, int RW>
+__device__ __forceinline__ void merge8(const DecodeParams &p, const Item &it, int row, int step, int lane)
 {
-    constexpr int S = D + kAccPad;
     constexpr int VEC = D / 32;
-    constexpr int RW = NT * 8 / kConsumerWarps;  // rows of a warp: warp, warp + 4, ...
     const long long total = ((long long)it.total_hi << 32) | (long long)it.total_lo;
     const long long G = balanced_grid(total, it.divisor());
     const int slot = lane < it.nparts ? (int)split_slot(it, lane, total, G) * kHeadsPerItem : 0;
-    const bool mine = own && slot == it.prow0 / kHeadsPerItem * kHeadsPerItem;
-    float w[RW];
+    for (; row < it.rows; row += RW * step) {
+        float w[RW], o[RW][VEC];
 #pragma unroll
-    for (int i = 0; i < RW; ++i) {
-        const int r = warp + i * kConsumerWarps;
-        w[i] = -INFINITY;
-        if (lane < it.nparts && r < it.rows)
-            w[i] = mine ? ml[r * 2] : __ldcg(p.part_lse + slot + r);
-    }
-    const int my_part = __ffs(__ballot_sync(0xffffffffu, mine && lane < it.nparts)) - 1;
-    float o[RW][VEC];
-#pragma unroll
-    for (int i = 0; i < RW; ++i)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e)
-            o[i][e] = 0.f;
-    bool weighted = false;
-    for (int k0 = 0; k0 < it.nparts; k0 += 4) {
-        float v[4][RW][VEC];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int k = min(k0 + u, it.nparts - 1);
-            const int row = __shfl_sync(0xffffffffu, slot, k);
-#pragma unroll
-            for (int i = 0; i < RW; ++i) {
-                const int r = min(warp + i * kConsumerWarps, it.rows - 1);
-                const float *src = p.part_o + (size_t)(row + r) * D + lane * VEC;
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    v[u][i][e] = k == my_part ? acc[r * S + lane * VEC + e] : __ldcg(src + e);
-            }
-        }
-        if (!weighted) {  // the weights, while the first rows are on their way
-            weighted = true;
-#pragma unroll
-            for (int i = 0; i < RW; ++i) {
-                const float M = dev::warp_max(w[i]);
-                w[i] = M == -INFINITY ? 0.f : exp2f(w[i] - M);
-                const float W = dev::warp_sum(w[i]);
-                w[i] = W > 0.f ? w[i] / W : 0.f;
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-#pragma unroll
-            for (int i = 0; i < RW; ++i) {
-                const float wk = __shfl_sync(0xffffffffu, w[i], min(k0 + u, 31));
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    if (k0 + u < it.nparts)
-                        o[i][e] = fmaf(wk, v[u][i][e], o[i][e]);
-            }
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < RW; ++i) {
-        const int r = warp + i * kConsumerWarps;
-        if (r < it.rows) {
-            T *dst = reinterpret_cast<T *>(p.out) + ((size_t)it.seq * p.num_q_heads + it.qrow0 + r) * D + lane * VEC;
+        for (int i = 0; i < RW; ++i) {
+            const int r = row + i * step;
+            w[i] = lane < it.nparts && r < it.rows ? __ldcg(p.part_lse + slot + r) : -INFINITY;
 #pragma unroll
             for (int e = 0; e < VEC; ++e)
-                dst[e] = dev::from_float<T>(o[i][e]);
+                o[i][e] = 0.f;
+        }
+        for (int k0 = 0; k0 < it.nparts; k0 += 4) {
+            float v[4][RW][VEC];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int at = __shfl_sync(0xffffffffu, slot, min(k0 + u, it.nparts - 1));
+#pragma unroll
+                for (int i = 0; i < RW; ++i) {
+                    const float *src = p.part_o + (size_t)(at + min(row + i * step, it.rows - 1)) * D + lane * VEC;
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e)
+                        v[u][i][e] = __ldcg(src + e);
+                }
+            }
+            if (k0 == 0) {  // the weights, while the first rows are on their way
+#pragma unroll
+                for (int i = 0; i < RW; ++i) {
+                    const float M = dev::warp_max(w[i]);
+                    w[i] = M == -INFINITY ? 0.f : exp2f(w[i] - M);
+                    const float W = dev::warp_sum(w[i]);
+                    w[i] = W > 0.f ? w[i] / W : 0.f;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+#pragma unroll
+                for (int i = 0; i < RW; ++i) {
+                    const float wk = __shfl_sync(0xffffffffu, w[i], min(k0 + u, 31));
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e)
+                        if (k0 + u < it.nparts)
+                            o[i][e] = fmaf(wk, v[u][i][e], o[i][e]);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < RW; ++i) {
+            const int r = row + i * step;
+            if (r < it.rows) {
+                T *dst = reinterpret_cast<T *>(p.out) +
+                         ((size_t)it.seq * p.num_q_heads + it.qrow0 + r) * D + lane * VEC;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    dst[e] = dev::from_float<T>(o[i][e]);
+            }
         }
     }
 }
 
-// End of an item, as finish_item: the barrier before the merge buffers are used again
-// and, for a split unit, the count and the merge.  False on a timeout.
+// The other part's rows of a unit cut once, when its counter, read as `seen`, says that
+// they are there; the counter is then reset for the next launch (count_partial).  -1:
+// this part is stored and counted.
+__device__ __forceinline__ int other_part(const DecodeParams &p, const Item &it, unsigned long long seen)
+{
+    if (!it.partial || it.nparts != 2 || seen != (((unsigned long long)p.epoch << 32) | 1ull))
+        return -1;
+    dev::fence_acq_rel_gpu();  // its rows were released before its count
+    *reinterpret_cast<volatile unsigned long long *>(p.counters + it.c_first) = 0ull;
+    const long long total = ((long long)it.total_hi << 32) | (long long)it.total_lo;
+    const long long G = balanced_grid(total, it.divisor());
+    const int s0 = (int)split_slot(it, 0, total, G) * kHeadsPerItem;
+    return s0 == it.prow0 ? (int)split_slot(it, 1, total, G) * kHeadsPerItem : s0;
+}
+
+// End of an item: the barrier before the merge buffers are used again and, for a split
+// unit whose part went to its slot, the release, the count and the merge (see
+// finish_item).  False on a timeout.
 template <typename T, int D, int NT>
 __device__ __forceinline__ bool finish8(const DecodeParams &p, const Item &it, const CtaState &c, uint32_t &sph,
-                                        int warp, int lane)
+                                        int warp, int lane, bool counted, unsigned long long seen)
 {
     if (!consumer_sync(p, c, sph))
         return false;
-    if (!it.partial)
+    if (!it.partial || counted)
         return true;
-    bool merge = *c.merge == 2, own = merge;
-    if (!merge) {
-        if (threadIdx.x == 0) {
+    if (threadIdx.x == 0) {
+        dev::fence_acq_rel_gpu();
+        const bool last = count_partial(p, it, seen);
+        if (last)
             dev::fence_acq_rel_gpu();
-            const bool last = count_partial(p, it, *c.ctr_seen);
-            if (last)
-                dev::fence_acq_rel_gpu();
-            *c.merge = last ? 1 : 0;
-        }
-        if (!consumer_sync(p, c, sph))
-            return false;
-        merge = *c.merge == 1;
+        *c.merge = last ? 1 : 0;
     }
-    if (merge) {
+    if (!consumer_sync(p, c, sph))
+        return false;
+    if (*c.merge) {
         if (it.nparts <= 32)
-            merge8<T, D, NT>(p, it, warp, lane, c.macc, c.mml, own);
+            merge8<T, D, NT * 8 / kConsumerWarps>(p, it, warp, kConsumerWarps, lane);
         else
             merge_split_unit<T, D, false>(p, it, warp, lane, nullptr);
     }
-    // (own rows are read before the next item's take their place)
-    return own ? consumer_sync(p, c, sph) : true;
+    return true;
 }
 
 template <typename T, int D, int BS, int NT>
@@ -938,7 +974,8 @@ __global__ void __launch_bounds__(kThreads8, Cfg8<T, D, BS, NT>::kCtas)
                 break;
             continue;
         }
-        if (!consume_item8<T, D, BS, NT>(p, c, it, sfull, slot, g, warp, lane, rows_cap, alone))
+        unsigned long long seen = 0;  // thread 0: the split unit's counter
+        if (!consume_item8<T, D, BS, NT>(p, c, it, sfull, slot, g, warp, lane, rows_cap, alone, seen))
             break;
         if (alone) {
             if (*c.abort)
@@ -949,11 +986,12 @@ __global__ void __launch_bounds__(kThreads8, Cfg8<T, D, BS, NT>::kCtas)
         merge_now = merge_next;
         merge_next = c.merge;
         if (threadIdx.x == 0)
-            probe_split_last(p, it, c);
+            *c.merge = other_part(p, it, seen);
         if (!consumer_sync(p, c, sph))
             break;
-        finalize8<T, D>(p, it, c.macc, c.mml, rows_cap, threadIdx.x, *c.merge == 2);
-        if (!finish8<T, D, NT>(p, it, c, sph, warp, lane))
+        const int other = *c.merge;
+        finalize8<T, D>(p, it, c.macc, c.mml, rows_cap, threadIdx.x, other);
+        if (!finish8<T, D, NT>(p, it, c, sph, warp, lane, other >= 0, seen))
             break;
         if (*c.abort)
             break;
