@@ -76,7 +76,9 @@ struct Cfg8 {
     static constexpr int kBPS = kStageTokens / BS;
     static constexpr int kStageBytes = kBPS * kRecord;
     static constexpr int kStages = kRing / kStageBytes;
-    static_assert(kStages >= kConsumerWarps, "a stage per consumer warp");
+    // A warp gets ahead of another by kSlots items of one stage at most (they share the
+    // item slots), or by one round of stages: less than a ring, which the waits rely on.
+    static_assert(kStages >= kSlots + kConsumerWarps, "the warps stay within one ring of each other");
     static_assert(kStageTokens % BS == 0 && 32 % kBPS == 0, "a stage is a whole number of blocks");
     static_assert(kTile % 1024 == 0, "tiles start on the swizzle's 1024-byte period");
 };
@@ -391,7 +393,6 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
     constexpr int MT = TS / 16;   // 16-token tiles of a stage
     constexpr int KS = D / 16;    // k-steps of K Q^T = words of a lane's share of a K row
     constexpr int DM = D / 16;    // 16-dim tiles of O^T
-    constexpr bool kEarlyV = NT == 1 && !kSplit;
     constexpr int SA = D + kAccPad;
     constexpr uint32_t kQSlotBytes = NT * 8 * D * sizeof(T);
     constexpr float kUp = 16384.f;  // 2^14: p's factor in the products
@@ -467,6 +468,14 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
             seen = *reinterpret_cast<volatile unsigned long long *>(p.counters + it.c_first);
         const int j = it.j0 + i * C::kBPS;
         const uint32_t st = (g + i) % C::kStages, phase = ((g + i) / C::kStages) & 1u;
+        // The scales' barrier first.  Consecutive uses of a stage may belong to different
+        // warps (the ring need not be a multiple of four stages), and a wait by parity
+        // must not begin while the use before is still under way: it would take the use
+        // before that one for its own.  Stages' data may land out of order, so the data's
+        // barrier alone would allow it.  The scale warp hands the stages over in order, each
+        // after its previous use was released, so behind its barrier the data's is in the
+        // right phase; and its own barrier is, because this warp has passed an earlier stage
+        // or an item's end less than a ring ago.
         if (!warp_wait(p, c, &sfull[st], phase) || !warp_wait(p, c, &c.full[st], phase))
             return false;
         const int nbs = min(C::kBPS, it.j1 - j);  // blocks in this stage
@@ -483,55 +492,43 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
             vmax = fmaxf(vmax, vscale[b]);
         }
 
-        // S^T = K Q^T.  All of a stage's K is read first, and its tiles take turns, even and
-        // odd k-steps in accumulators of their own, so that no product waits for the one
-        // before it.
-        uint32_t w[MT][2][KS];
+        // S^T = K Q^T, even and odd k-steps in accumulators of their own (shorter chains)
+        float s[MT][NT][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             const uint8_t *kt = stage + (mt * 16 / BS) * C::kRecord;
             const int tk = mt * 16 % BS + tok0;
+            uint32_t w0[KS], w1[KS];
 #pragma unroll
             for (int u = 0; u < D / 64; ++u) {
                 const int unit = q4 * (D / 64) + u;
-                *reinterpret_cast<uint4 *>(&w[mt][0][4 * u]) =
+                *reinterpret_cast<uint4 *>(&w0[4 * u]) =
                     *reinterpret_cast<const uint4 *>(kt + tile_unit<D>(tk, unit));
-                *reinterpret_cast<uint4 *>(&w[mt][1][4 * u]) =
+                *reinterpret_cast<uint4 *>(&w1[4 * u]) =
                     *reinterpret_cast<const uint4 *>(kt + tile_unit<D>(tk + 2, unit));
             }
-        }
-        float s[MT][NT][4], s1[MT][NT][4];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+            float s2[NT][2][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    s[mt][nt][e] = s1[mt][nt][e] = 0.f;
+                    s2[nt][0][e] = s2[nt][1][e] = 0.f;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
+            for (int ks = 0; ks < KS; ++ks) {
                 uint32_t a[4];
-                dev::e4m3x4_to_f16x4(w[mt][0][ks], a[0], a[2]);
-                dev::e4m3x4_to_f16x4(w[mt][1][ks], a[1], a[3]);
+                dev::e4m3x4_to_f16x4(w0[ks], a[0], a[2]);
+                dev::e4m3x4_to_f16x4(w1[ks], a[1], a[3]);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int t = 0; t < QT; ++t)
-                        dev::Mma<__half>::run(ks & 1 ? s1[mt][nt] : s[mt][nt], a, qb[nt][t][ks][0],
-                                              qb[nt][t][ks][1]);
+                        dev::Mma<__half>::run(s2[nt][ks & 1], a, qb[nt][t][ks][0], qb[nt][t][ks][1]);
             }
-        }
-
-        // V's codes, on their way while the softmax runs (where registers allow)
-        uint32_t v[kEarlyV ? MT : 1][kEarlyV ? DM / 2 : 1][4];
-        if constexpr (kEarlyV) {
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int dp = 0; dp < DM / 2; ++dp)
-                    load_v<D, BS>(v[mt][dp], stage + C::kTile, C::kRecord, mt, dp, lane);
+                for (int e = 0; e < 4; ++e)
+                    s[mt][nt][e] = s2[nt][0][e] + s2[nt][1][e];
         }
 
         // Scale and mask.  A lane compares its own scores with the reference: only where
@@ -547,8 +544,8 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float &xa = s[mt][nt][2 * h], &xb = s[mt][nt][2 * h + 1];
-                    xa = (xa + s1[mt][nt][2 * h]) * ga;
-                    xb = (xb + s1[mt][nt][2 * h + 1]) * gb;
+                    xa *= ga;
+                    xb *= gb;
                     if (partial && mt * 16 + tok0 + 2 * h >= valid)
                         xa = xb = -INFINITY;
                     raise |= xa > ma[nt] + 1.f || xb > mb[nt] + 1.f;
@@ -627,22 +624,21 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
             }
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-                uint32_t (&x)[4] = v[kEarlyV ? mt : 0][kEarlyV ? dp : 0];
-                if constexpr (!kEarlyV)
-                    load_v<D, BS>(x, stage + C::kTile, C::kRecord, mt, dp, lane);
+                uint32_t v[4];
+                load_v<D, BS>(v, stage + C::kTile, C::kRecord, mt, dp, lane);
                 if (partial) {
                     // rows past the context may hold anything (NaN): zero their codes
                     const int left = min(max(valid - mt * 16 - 4 * q4, 0), 4);
                     const uint32_t keep = left == 4 ? 0xffffffffu : (1u << (8 * left)) - 1u;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        x[e] &= keep;
+                        v[e] &= keep;
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint32_t a[4];
-                    dev::e4m3x4_to_f16x4(x[2 * h], a[0], a[2]);
-                    dev::e4m3x4_to_f16x4(x[2 * h + 1], a[1], a[3]);
+                    dev::e4m3x4_to_f16x4(v[2 * h], a[0], a[2]);
+                    dev::e4m3x4_to_f16x4(v[2 * h + 1], a[1], a[3]);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
