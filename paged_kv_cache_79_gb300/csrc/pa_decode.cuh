@@ -489,6 +489,7 @@ __device__ __forceinline__ bool consumer_sync(const DecodeParams &p, const CtaSt
 // ---------------------------------------------------------------------------
 template <typename T, int D, int BS, int kBPS, int kChunks, int kTileBytes, int kStages, int kCopy>
 struct Producer {
+    static constexpr bool kCountParts = true;  // emit_unit looks for CTAs without positions
     const DecodeParams &p;
     const CUtensorMap *tk;
     const CUtensorMap *tv;
@@ -959,8 +960,12 @@ __device__ __forceinline__ bool emit_unit(const DecodeParams &p, Prod &pr, const
             const long long cf = cta_of(ra, total, G);
             const long long cl = cta_of(rb - 1, total, G);
             int np = 1;
-            for (long long cc = cf + 1; cc <= cl; ++cc)
-                np += (cc * total / G < (cc + 1) * total / G) ? 1 : 0;
+            if constexpr (Prod::kCountParts) {
+                for (long long cc = cf + 1; cc <= cl; ++cc)
+                    np += (cc * total / G < (cc + 1) * total / G) ? 1 : 0;
+            } else {
+                np = (int)(cl - cf) + 1;  // every CTA up to G has positions: G <= total
+            }
             it.c_first = (int)cf;
             it.nparts = np;
         }

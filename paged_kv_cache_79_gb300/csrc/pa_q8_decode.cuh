@@ -50,8 +50,8 @@
 
 namespace pagedkv {
 
-#ifndef PA_Q8_STAGE_TOKENS
-#define PA_Q8_STAGE_TOKENS 32  // tokens per ring stage
+#ifndef PA_Q8_STAGE_BYTES
+#define PA_Q8_STAGE_BYTES 8192  // a ring stage: 32 tokens of 128 dims, 64 of 64
 #endif
 #ifndef PA_Q8_RING_BYTES
 #define PA_Q8_RING_BYTES 81920  // shared memory of the stage ring (two CTAs per SM)
@@ -72,7 +72,7 @@ struct Cfg8 {
     static constexpr int kSlots = NT == 1 ? 4 : kItemSlots;
     static constexpr int kTile = BS * D;          // K (or V) codes of one (block, kv head)
     static constexpr int kRecord = 2 * kTile;     // K tile, then V tile
-    static constexpr int kStageTokens = PA_Q8_STAGE_TOKENS;
+    static constexpr int kStageTokens = PA_Q8_STAGE_BYTES / (2 * D);
     static constexpr int kBPS = kStageTokens / BS;
     static constexpr int kStageBytes = kBPS * kRecord;
     static constexpr int kStages = kRing / kStageBytes;
@@ -95,6 +95,8 @@ __device__ __forceinline__ uint32_t tile_unit(int tok, int u)
 
 constexpr int kThreads8 = kThreads + 32;  // one warp more than pa_decode: the scales'
 
+constexpr int kMergeRows = 4;  // merge rows at least: merge8 works in them
+
 // Shared memory: as make_layout, with 8 bytes of scales per block of a stage in the
 // place of the fused append's rows.
 __host__ __device__ inline SmemLayout make_layout8(int stages, int stage_bytes, int bps, int slots, int rows,
@@ -103,7 +105,7 @@ __host__ __device__ inline SmemLayout make_layout8(int stages, int stage_bytes, 
     SmemLayout L;
     uint32_t o = (uint32_t)stages * (uint32_t)stage_bytes;
     L.acc = o;
-    o += (uint32_t)(kConsumerWarps * rows * (D + kAccPad) * 4);
+    o += (uint32_t)(kConsumerWarps * (rows > kMergeRows ? rows : kMergeRows) * (D + kAccPad) * 4);
     L.ml = o;
     o += kConsumerWarps * kHeadsPerItem * 2 * 4;
     o = (o + 127u) & ~127u;
@@ -134,6 +136,9 @@ __host__ __device__ inline SmemLayout make_layout8(int stages, int stage_bytes, 
 // ---------------------------------------------------------------------------
 template <typename T, int D, int BS, int NT>
 struct Producer8 {
+    // G = ceil(total / divisor) <= total: none is without (a division for each part, 38 of
+    // them, kept the first copy of a single sequence's one head back by 5 us)
+    static constexpr bool kCountParts = false;
     using C = Cfg8<T, D, BS, NT>;
     const DecodeParams &p;
     const CUtensorMap *map;
@@ -262,6 +267,7 @@ struct Producer8 {
 // ---------------------------------------------------------------------------
 template <typename T, int D, int BS, int NT>
 struct ScaleWarp {
+    static constexpr bool kCountParts = false;
     using C = Cfg8<T, D, BS, NT>;
     const DecodeParams &p;
     const Q8Params &q8;
@@ -794,73 +800,140 @@ __device__ __forceinline__ void finalize8(const DecodeParams &p, const Item &it,
     }
 }
 
-// Merge the nparts <= 32 partials of a split unit into its output rows, as
-// merge_split_unit does, RW rows and up to four parts of each in flight at once instead
-// of one row after the other (six parts of 13 rows: 8 us to 3).  The calling warp does
-// rows row, row + step, ...
-template <typename T, int D, int RW>
-__device__ __forceinline__ void merge8(const DecodeParams &p, const Item &it, int row, int step, int lane)
+// Floats of the merge rows (make_layout8) that merge8 may use.
+__device__ __forceinline__ int merge_room(int rows_cap, int D)
 {
-    constexpr int VEC = D / 32;
-    const long long total = ((long long)it.total_hi << 32) | (long long)it.total_lo;
-    const long long G = balanced_grid(total, it.divisor());
-    const int slot = lane < it.nparts ? (int)split_slot(it, lane, total, G) * kHeadsPerItem : 0;
-    for (; row < it.rows; row += RW * step) {
-        float w[RW], o[RW][VEC];
+    return kConsumerWarps * max(rows_cap, kMergeRows) * (D + kAccPad);
+}
+
+// Merge the partials of a split unit into its output rows by the log-sum-exp rule, all
+// consumer warps together: every (row, part)'s log2-sum-exp in one round of loads, a row's
+// weights by one warp, then the weighted rows, D / 4 threads per row with two rows and
+// eight parts of each in flight; with fewer rows than such groups of threads, several
+// groups share a row's parts.  (merge_split_unit goes row by row with four parts in
+// flight.)  `room`: the merge rows, free by now.  False on a timeout.
+template <typename T, int D>
+__device__ __forceinline__ bool merge8(const DecodeParams &p, const Item &it, const CtaState &c, uint32_t &sph,
+                                       int warp, int lane, float *room)
+{
+    constexpr int LR = D / 4;                             // threads on a row
+    constexpr int kGroups = 32 * kConsumerWarps / LR;
+    constexpr int kFlight = 8;
+    const int n = it.nparts, tid = warp * 32 + lane;
+    // every CTA up to G has positions, so the parts' slots are consecutive (split_slot)
+    auto slot = [&](int i) { return (2 * (it.c_first + i) + (i == 0 ? 1 : 0)) * kHeadsPerItem; };
+    for (int k = tid; k < it.rows * n; k += 4 * 32 * kConsumerWarps) {
+        float lse[4];
 #pragma unroll
-        for (int i = 0; i < RW; ++i) {
-            const int r = row + i * step;
-            w[i] = lane < it.nparts && r < it.rows ? __ldcg(p.part_lse + slot + r) : -INFINITY;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                o[i][e] = 0.f;
-        }
-        for (int k0 = 0; k0 < it.nparts; k0 += 4) {
-            float v[4][RW][VEC];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int at = __shfl_sync(0xffffffffu, slot, min(k0 + u, it.nparts - 1));
-#pragma unroll
-                for (int i = 0; i < RW; ++i) {
-                    const float *src = p.part_o + (size_t)(at + min(row + i * step, it.rows - 1)) * D + lane * VEC;
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e)
-                        v[u][i][e] = __ldcg(src + e);
-                }
-            }
-            if (k0 == 0) {  // the weights, while the first rows are on their way
-#pragma unroll
-                for (int i = 0; i < RW; ++i) {
-                    const float M = dev::warp_max(w[i]);
-                    w[i] = M == -INFINITY ? 0.f : exp2f(w[i] - M);
-                    const float W = dev::warp_sum(w[i]);
-                    w[i] = W > 0.f ? w[i] / W : 0.f;
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-#pragma unroll
-                for (int i = 0; i < RW; ++i) {
-                    const float wk = __shfl_sync(0xffffffffu, w[i], min(k0 + u, 31));
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e)
-                        if (k0 + u < it.nparts)
-                            o[i][e] = fmaf(wk, v[u][i][e], o[i][e]);
-                }
-            }
+        for (int u = 0; u < 4; ++u) {
+            const int x = min(k + u * 32 * kConsumerWarps, it.rows * n - 1);
+            lse[u] = __ldcg(p.part_lse + slot(x % n) + x / n);
         }
 #pragma unroll
-        for (int i = 0; i < RW; ++i) {
-            const int r = row + i * step;
-            if (r < it.rows) {
-                T *dst = reinterpret_cast<T *>(p.out) +
-                         ((size_t)it.seq * p.num_q_heads + it.qrow0 + r) * D + lane * VEC;
+        for (int u = 0; u < 4; ++u)
+            if (k + u * 32 * kConsumerWarps < it.rows * n)
+                room[k + u * 32 * kConsumerWarps] = lse[u];
+    }
+    if (!consumer_sync(p, c, sph))
+        return false;
+    for (int r = warp; r < it.rows; r += kConsumerWarps) {
+        float M = -INFINITY, W = 0.f;
+        for (int i = lane; i < n; i += 32)
+            M = fmaxf(M, room[r * n + i]);
+        M = dev::warp_max(M);
+        for (int i = lane; i < n; i += 32) {
+            const float w = M == -INFINITY ? 0.f : exp2f(room[r * n + i] - M);
+            room[r * n + i] = w;
+            W += w;
+        }
+        W = dev::warp_sum(W);
+        for (int i = lane; i < n; i += 32)
+            room[r * n + i] = W > 0.f ? room[r * n + i] / W : 0.f;
+    }
+    if (!consumer_sync(p, c, sph))
+        return false;
+    const int group = tid / LR, col = tid % LR * 4;
+    const int ways = max(kGroups / it.rows, 1);           // groups that share a row
+    const int sub = group % ways, step = kGroups / ways;
+    float *const part = room + (it.rows * n + 3) / 4 * 4 + group * D + col;
+    T *const out = reinterpret_cast<T *>(p.out) + ((size_t)it.seq * p.num_q_heads + it.qrow0) * D + col;
+    for (int r = group / ways; r < it.rows; r += 2 * step) {
+        const int r2 = min(r + step, it.rows - 1);
+        float o[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        for (int k0 = sub; k0 < n; k0 += ways * kFlight) {
+            float4 v[2][kFlight];
 #pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    dst[e] = dev::from_float<T>(o[i][e]);
+            for (int u = 0; u < kFlight; ++u) {
+                const float *src = p.part_o + (size_t)slot(min(k0 + u * ways, n - 1)) * D + col;
+                v[0][u] = __ldcg(reinterpret_cast<const float4 *>(src + (size_t)r * D));
+                v[1][u] = __ldcg(reinterpret_cast<const float4 *>(src + (size_t)r2 * D));
             }
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u) {
+                const int k = k0 + u * ways;
+                const float w0 = k < n ? room[r * n + k] : 0.f, w1 = k < n ? room[r2 * n + k] : 0.f;
+                if (k < n) {
+                    o[0][0] = fmaf(w0, v[0][u].x, o[0][0]);
+                    o[0][1] = fmaf(w0, v[0][u].y, o[0][1]);
+                    o[0][2] = fmaf(w0, v[0][u].z, o[0][2]);
+                    o[0][3] = fmaf(w0, v[0][u].w, o[0][3]);
+                    o[1][0] = fmaf(w1, v[1][u].x, o[1][0]);
+                    o[1][1] = fmaf(w1, v[1][u].y, o[1][1]);
+                    o[1][2] = fmaf(w1, v[1][u].z, o[1][2]);
+                    o[1][3] = fmaf(w1, v[1][u].w, o[1][3]);
+                }
+            }
+        }
+        if (ways > 1) {  // (step >= rows: one row for this group)
+            *reinterpret_cast<float4 *>(part) = make_float4(o[0][0], o[0][1], o[0][2], o[0][3]);
+        } else {
+            store4(out + (size_t)r * D, o[0]);
+            if (r + step < it.rows)
+                store4(out + (size_t)r2 * D, o[1]);
         }
     }
+    if (ways > 1) {
+        if (!consumer_sync(p, c, sph))
+            return false;
+        const int r = group / ways;
+        if (sub == 0 && r < it.rows) {
+            float o[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int u = 0; u < ways; ++u) {
+                const float4 v = *reinterpret_cast<const float4 *>(part + u * D);
+                o[0] += v.x;
+                o[1] += v.y;
+                o[2] += v.z;
+                o[3] += v.w;
+            }
+            store4(out + (size_t)r * D, o);
+        }
+    }
+    return consumer_sync(p, c, sph);  // the merge rows are read before the next item's come
+}
+
+// Count this CTA's part of a split unit; whether it was the last.  `seen`: the counter as
+// read before.  As count_partial, but where others have counted in this launch already
+// an add takes the place of further exchanges: the parts of one long unit finish together,
+// and each round of exchanges lets one of them through (38 parts took 20 us).
+__device__ __forceinline__ bool count8(const DecodeParams &p, const Item &it, unsigned long long seen)
+{
+    unsigned long long *ctr = p.counters + it.c_first;
+    unsigned int cnt = 0;
+    // (each failed exchange means that another CTA changed the counter: at most nparts)
+    while ((unsigned int)(seen >> 32) != p.epoch) {
+        const unsigned long long prev = atomicCAS(ctr, seen, ((unsigned long long)p.epoch << 32) | 1ull);
+        if (prev == seen) {
+            cnt = 1;
+            break;
+        }
+        seen = prev;
+    }
+    if (cnt == 0)
+        cnt = (unsigned int)atomicAdd(ctr, 1ull) + 1u;
+    const bool last = cnt == (unsigned int)it.nparts;
+    if (last)  // every part is counted: no other CTA touches this counter again
+        *reinterpret_cast<volatile unsigned long long *>(ctr) = 0ull;
+    return last;
 }
 
 // The other part's rows of a unit cut once, when its counter, read as `seen`, says that
@@ -872,18 +945,17 @@ __device__ __forceinline__ int other_part(const DecodeParams &p, const Item &it,
         return -1;
     dev::fence_acq_rel_gpu();  // its rows were released before its count
     *reinterpret_cast<volatile unsigned long long *>(p.counters + it.c_first) = 0ull;
-    const long long total = ((long long)it.total_hi << 32) | (long long)it.total_lo;
-    const long long G = balanced_grid(total, it.divisor());
-    const int s0 = (int)split_slot(it, 0, total, G) * kHeadsPerItem;
-    return s0 == it.prow0 ? (int)split_slot(it, 1, total, G) * kHeadsPerItem : s0;
+    const int s0 = (2 * it.c_first + 1) * kHeadsPerItem, s1 = 2 * (it.c_first + 1) * kHeadsPerItem;
+    return s0 == it.prow0 ? s1 : s0;
 }
 
 // End of an item: the barrier before the merge buffers are used again and, for a split
 // unit whose part went to its slot, the release, the count and the merge (see
 // finish_item).  False on a timeout.
-template <typename T, int D, int NT>
+template <typename T, int D>
 __device__ __forceinline__ bool finish8(const DecodeParams &p, const Item &it, const CtaState &c, uint32_t &sph,
-                                        int warp, int lane, bool counted, unsigned long long seen)
+                                        int warp, int lane, int rows_cap, bool counted,
+                                        unsigned long long seen)
 {
     if (!consumer_sync(p, c, sph))
         return false;
@@ -891,19 +963,19 @@ __device__ __forceinline__ bool finish8(const DecodeParams &p, const Item &it, c
         return true;
     if (threadIdx.x == 0) {
         dev::fence_acq_rel_gpu();
-        const bool last = count_partial(p, it, seen);
+        const bool last = count8(p, it, seen);
         if (last)
             dev::fence_acq_rel_gpu();
         *c.merge = last ? 1 : 0;
     }
     if (!consumer_sync(p, c, sph))
         return false;
-    if (*c.merge) {
-        if (it.nparts <= 32)
-            merge8<T, D, NT * 8 / kConsumerWarps>(p, it, warp, kConsumerWarps, lane);
-        else
-            merge_split_unit<T, D, false>(p, it, warp, lane, nullptr);
-    }
+    if (!*c.merge)
+        return true;
+    // weights and, with few rows, a row per group of threads
+    if (it.rows * it.nparts + 3 + 4 * 128 <= merge_room(rows_cap, D))
+        return merge8<T, D>(p, it, c, sph, warp, lane, c.macc);
+    merge_split_unit<T, D, false>(p, it, warp, lane, nullptr);
     return true;
 }
 
@@ -987,7 +1059,7 @@ __global__ void __launch_bounds__(kThreads8, Cfg8<T, D, BS, NT>::kCtas)
             break;
         const int other = *c.merge;
         finalize8<T, D>(p, it, c.macc, c.mml, rows_cap, threadIdx.x, other);
-        if (!finish8<T, D, NT>(p, it, c, sph, warp, lane, other >= 0, seen))
+        if (!finish8<T, D>(p, it, c, sph, warp, lane, rows_cap, other >= 0, seen))
             break;
         if (*c.abort)
             break;

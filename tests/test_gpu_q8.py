@@ -97,7 +97,10 @@ SHAPES += [("bf16", 128, 16, 12, 3, [3000, 1, 17, 4096, 2222, 16]), ("f16", 128,
            ("bf16", 128, 32, 32, 8, [1, 31, 32, 33, 5000, 40000]),        # cut over many CTAs
            ("bf16", 128, 16, 8, 1, [60000]), ("f32", 64, 16, 4, 2, [0, 3000, 0, 1, 0]),
            ("bf16", 128, 16, 40, 2, [1 + (i * 7) % 20 for i in range(500)]),   # many tiny sequences, G = 20
-           ("f16", 128, 32, 8, 8, [0, 0, 0])]
+           ("f16", 128, 32, 8, 8, [0, 0, 0]),
+           # few rows and many parts: the ways in which a unit's parts are merged
+           ("f32", 128, 16, 1, 1, [6000]), ("bf16", 64, 32, 2, 1, [20000, 3]), ("f16", 128, 32, 5, 1, [30000, 7]),
+           ("f16", 64, 16, 3, 1, [60000]), ("bf16", 128, 16, 3, 1, [9001, 9000]), ("f16", 64, 32, 16, 1, [40000])]
 
 
 @pytest.mark.parametrize("dtype,d,b,hq,hkv,lens", SHAPES, ids=lambda v: str(v).replace(" ", "")[:40])
