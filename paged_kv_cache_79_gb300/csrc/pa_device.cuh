@@ -202,6 +202,20 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x)
     return d;
 }
 
+// 16 and 8 bytes of shared memory.
+__device__ __forceinline__ void lds128(uint32_t *x, uint32_t addr)
+{
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                 : "r"(addr));
+}
+__device__ __forceinline__ float2 lds_f2(uint32_t addr)
+{
+    float2 x;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(x.x), "=f"(x.y) : "r"(addr));
+    return x;
+}
+
 // Four e4m3 codes as two fp16 pairs (codes 0, 1 and 2, 3).
 __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t x, uint32_t &lo, uint32_t &hi)
 {

@@ -372,14 +372,12 @@ __device__ __forceinline__ void release_item(const CtaState &c, const Item &it, 
         dev::mbar_arrive(dev::smem_addr(&c.item_empty[slot]));
 }
 
-// The codes of V tokens 16 mt .. + 15 of a stage, dims 32 dp .. + 31 (two 16 x 16 matrices),
-// transposed.
+// Byte offset of token tile mt (16 tokens) in a stage's K codes (V's lie kTile behind): a
+// multiple of 1024, so that the swizzle of a lane's share does not depend on mt.
 template <int D, int BS>
-__device__ __forceinline__ void load_v(uint32_t (&v)[4], const uint8_t *vstage, int record, int mt, int dp, int lane)
+__device__ __forceinline__ constexpr uint32_t tile_offset(int mt)
 {
-    const uint8_t *vt = vstage + (mt * 16 / BS) * record;
-    dev::ldsm_b8_x2_trans(dev::smem_addr(vt + tile_unit<D>(mt * 16 % BS + (lane & 15), 2 * dp + (lane >> 4))),
-                          v[0], v[1], v[2], v[3]);
+    return (uint32_t)((mt * 16 / BS) * 2 * BS * D + (mt * 16 % BS) * D);
 }
 
 // ---------------------------------------------------------------------------
@@ -405,6 +403,12 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
     const int q4 = lane & 3;       // fragment columns: query rows 8 nt + 2 q4, + 1
     const int r8 = lane >> 2;      // fragment row
     const int tok0 = 4 * (r8 >> 1) + (r8 & 1);  // this lane's tokens of a tile: tok0, tok0 + 2
+    // Its shares of them in a K tile (a row's next 16-byte unit is the address ^ 16), and its
+    // row of a V tile's first 32 dims (the next 32: ^ 32).  Tiles start on multiples of
+    // 1024 bytes, so the exclusive or acts on the swizzled unit alone.
+    const uint32_t koff0 = tile_unit<D>(tok0, q4 * (D / 64)), koff1 = tile_unit<D>(tok0 + 2, q4 * (D / 64));
+    const uint32_t voff = tile_unit<D>(lane & 15, lane >> 4);
+    const uint32_t ring = dev::smem_addr(c.ring), scales = dev::smem_addr(c.newrow);
 
     // Q^T as the B operand, and the factor each row's scores take
     uint32_t qb[NT][QT][KS][2];
@@ -487,12 +491,12 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
         const int nbs = min(C::kBPS, it.j1 - j);  // blocks in this stage
         const int valid = min(nbs * BS, it.len - j * BS);
         const bool partial = valid < TS;
-        const uint8_t *stage = c.ring + (size_t)st * C::kStageBytes;
+        const uint32_t stage = ring + st * C::kStageBytes;
         float kscale[C::kBPS], vscale[C::kBPS];
         float vmax = vref;
 #pragma unroll
         for (int b = 0; b < C::kBPS; ++b) {
-            const float2 s2 = reinterpret_cast<const float2 *>(c.newrow)[st * C::kBPS + b];
+            const float2 s2 = dev::lds_f2(scales + (st * C::kBPS + b) * 8);
             kscale[b] = s2.x;
             vscale[b] = b < nbs ? s2.y : 0.f;
             vmax = fmaxf(vmax, vscale[b]);
@@ -502,16 +506,12 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
         float s[MT][NT][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-            const uint8_t *kt = stage + (mt * 16 / BS) * C::kRecord;
-            const int tk = mt * 16 % BS + tok0;
+            const uint32_t kt = stage + tile_offset<D, BS>(mt);
             uint32_t w0[KS], w1[KS];
 #pragma unroll
             for (int u = 0; u < D / 64; ++u) {
-                const int unit = q4 * (D / 64) + u;
-                *reinterpret_cast<uint4 *>(&w0[4 * u]) =
-                    *reinterpret_cast<const uint4 *>(kt + tile_unit<D>(tk, unit));
-                *reinterpret_cast<uint4 *>(&w1[4 * u]) =
-                    *reinterpret_cast<const uint4 *>(kt + tile_unit<D>(tk + 2, unit));
+                dev::lds128(&w0[4 * u], (kt + koff0) ^ (uint32_t)(u << 4));
+                dev::lds128(&w1[4 * u], (kt + koff1) ^ (uint32_t)(u << 4));
             }
             float s2[NT][2][4];
 #pragma unroll
@@ -631,7 +631,8 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
                 uint32_t v[4];
-                load_v<D, BS>(v, stage + C::kTile, C::kRecord, mt, dp, lane);
+                dev::ldsm_b8_x2_trans((stage + C::kTile + tile_offset<D, BS>(mt) + voff) ^ (uint32_t)(dp << 5), v[0],
+                                      v[1], v[2], v[3]);
                 if (partial) {
                     // rows past the context may hold anything (NaN): zero their codes
                     const int left = min(max(valid - mt * 16 - 4 * q4, 0), 4);
