@@ -668,41 +668,49 @@ def pa_scatter_blocks(staging_k, staging_v, k_cache, v_cache, block_ids, stream=
 # the 8-bit cache, and tables built on the GPU
 # ----------------------------------------------------------------------------
 # (These calls take a few microseconds on the GPU for a small batch, so what the binding
-# looks up per call is looked up once: library functions, dtype codes, block sizes.)
+# looks up per call is looked up once: library functions, torch's types and handles.)
 @functools.lru_cache(maxsize=None)
 def _fn(name: str):
     return getattr(_load(), name)
 
 
+class _Torch:
+    """torch's attributes that the calls below use."""
+
+    def __init__(self):
+        import torch
+        self.int32, self.int64, self.uint8 = torch.int32, torch.int64, torch.uint8
+        self.codes = {torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16}
+        self.device = torch.cuda.device
+        self.current_device = torch._C._cuda_getDevice
+        self.current_stream = torch._C._cuda_getCurrentRawStream
+
+
 @functools.lru_cache(maxsize=None)
-def _dtypes():
-    import torch
-    return {torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16}
+def _torch() -> _Torch:
+    return _Torch()
 
 
 def _code(t) -> int:
-    code = _dtypes().get(t.dtype)
+    code = _torch().codes.get(t.dtype)
     return _dtype_code(t) if code is None else code
 
 
 def _on_device(names, tensors):
-    """Checks that the tensors are contiguous and on one CUDA device; returns None when it is
-    the current device, else a context that makes it so."""
-    import torch
-    dev = tensors[0].get_device()
+    """Checks that the tensors are contiguous and on one CUDA device; returns (its index,
+    None when it is the current device, else a context that makes it so)."""
+    dev = tensors[0].get_device()          # -1: not a CUDA tensor
     for name, t in zip(names, tensors):
-        if t.get_device() != dev or not t.is_cuda or not t.is_contiguous():
+        if t.get_device() != dev or dev < 0 or not t.is_contiguous():
             _cuda(t, name)
             raise ValueError(f"{name} is on cuda:{t.get_device()}, {names[0]} on cuda:{dev}")
-    return None if dev == torch._C._cuda_getDevice() else torch.cuda.device(dev)
+    T = _torch()
+    return dev, None if dev == T.current_device() else T.device(dev)
 
 
-def _raw_stream(stream, tensor) -> int:
-    """As _stream, on the tensor's device (without building a stream object for the default)."""
-    if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(tensor.get_device())
-    return _stream(stream)
+def _raw_stream(stream, dev: int) -> int:
+    """As _stream, on device `dev` (without building a stream object for the default)."""
+    return _torch().current_stream(dev) if stream is None else _stream(stream)
 
 
 def _call(name: str, device, *args) -> None:
@@ -756,10 +764,10 @@ def q8_views(kv_cache, num_kv_heads: int, head_dim: int, block_size: int):
 
 
 def _check_batch(kv_cache, block_tables, context_lens, num_kv_heads, head_dim, block_size):
-    import torch
-    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+    T = _torch()
+    if block_tables.dtype != T.int32 or context_lens.dtype != T.int32:
         raise TypeError("block_tables and context_lens must be int32")
-    if kv_cache.dtype != torch.uint8:
+    if kv_cache.dtype != T.uint8:
         raise TypeError("kv_cache must be uint8")
     if block_tables.dim() != 2 or context_lens.shape != block_tables.shape[:1]:
         raise ValueError("block_tables must be [S, W] and context_lens [S]")
@@ -778,7 +786,6 @@ def pa_q8_append(k, v, kv_cache, block_tables, context_lens, block_size: int, qu
     sequences, raising a block's scale where a row needs it (see pa_q8_append in
     include/pagedkv.h).  query_start int32 [S + 1]: first row of each sequence; None:
     one row per sequence."""
-    import torch
     _want(k.dim() == 3 and k.shape == v.shape, "k and v must be [N, Hkv, d] and alike")
     if k.dtype != v.dtype:
         raise TypeError("k and v must have one dtype")
@@ -788,14 +795,15 @@ def pa_q8_append(k, v, kv_cache, block_tables, context_lens, block_size: int, qu
     tensors = (k, v, kv_cache, block_tables, context_lens)
     qs_ptr = None
     if query_start is not None:
-        if query_start.dtype != torch.int32:
+        if query_start.dtype != _torch().int32:
             raise TypeError("query_start must be int32")
         _want(query_start.shape == (S + 1,), "query_start must be [S + 1]")
         tensors += (query_start,)
         qs_ptr = query_start.data_ptr()
-    device = _on_device(_APPEND_NAMES, tensors)
-    _call("pa_q8_append", device, k.data_ptr(), v.data_ptr(), kv_cache.data_ptr(),
-          block_tables.data_ptr(), W, context_lens.data_ptr(), qs_ptr, S, n, kv_cache.shape[0], hkv, d, block_size, _code(k), _raw_stream(stream, k))
+    dev, device = _on_device(_APPEND_NAMES, tensors)
+    _call("pa_q8_append", device, k.data_ptr(), v.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(), W,
+          context_lens.data_ptr(), qs_ptr, S, n, kv_cache.shape[0], hkv, d, block_size, _code(k),
+          _raw_stream(stream, dev))
 
 
 def pa_q8_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
@@ -816,17 +824,17 @@ def pa_q8_decode(out, q, kv_cache, block_tables, context_lens, scale: float, num
     _want(q.shape == (S, num_q_heads, head_dim) and out.shape == q.shape, "q and out must be [S, Hq, d]")
     if out.dtype != q.dtype:
         raise TypeError("q and out must have one dtype")
-    device = _on_device(_DECODE_NAMES, (out, q, kv_cache, block_tables, context_lens))
+    dev, device = _on_device(_DECODE_NAMES, (out, q, kv_cache, block_tables, context_lens))
     if workspace is None:
         with device or contextlib.nullcontext():
             workspace = _launch_scratch(pa_q8_decode_workspace_size(S, num_q_heads, num_kv_heads, head_dim,
                                                                     block_size, W), q.device, stream)
-    elif workspace.get_device() != q.get_device() or not workspace.is_contiguous():
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous and on the device of q")
     _call("pa_q8_decode", device, out.data_ptr(), q.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(), W,
           context_lens.data_ptr(), S, kv_cache.shape[0], float(scale), num_q_heads, num_kv_heads, head_dim,
           block_size, _code(q), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-          _raw_stream(stream, q))
+          _raw_stream(stream, dev))
     return out
 
 
@@ -839,9 +847,9 @@ def pa_q8_copy_blocks(kv_cache, src_dst_pairs, stream=None):
     n = src_dst_pairs.shape[0]
     if n == 0:
         return
-    device = _on_device(("kv_cache", "src_dst_pairs"), (kv_cache, src_dst_pairs))
+    dev, device = _on_device(("kv_cache", "src_dst_pairs"), (kv_cache, src_dst_pairs))
     _call("pa_q8_copy_blocks", device, kv_cache.data_ptr(), src_dst_pairs.data_ptr(), n, kv_cache.shape[0],
-          _block_bytes(kv_cache), _raw_stream(stream, kv_cache))
+          _block_bytes(kv_cache), _raw_stream(stream, dev))
 
 
 def pa_q8_swap_blocks(src_cache, dst_cache, src_dst_pairs, stream=None):
@@ -866,18 +874,17 @@ def pa_build_tables(block_tables, context_lens, new_tokens, free_list, num_free,
     the requests with new_tokens < 0, grows the others; all int32 CUDA tensors but
     slot_mapping (int64).  context_lens_out and num_free_out default to context_lens and
     num_free, updated in place."""
-    import torch
     if context_lens_out is None:
         context_lens_out = context_lens
     if num_free_out is None:
         num_free_out = num_free
     tensors = (block_tables, context_lens, new_tokens, free_list, num_free, query_start, granted, context_lens_out,
                num_free_out, slot_mapping)
-    int32 = torch.int32
+    int32 = _torch().int32
     for name, t in zip(_TABLE_NAMES, tensors[:-1]):
         if t.dtype != int32:
             raise TypeError(f"{name} must be int32")
-    if slot_mapping.dtype != torch.int64:
+    if slot_mapping.dtype != _torch().int64:
         raise TypeError("slot_mapping must be int64")
     S, W = block_tables.shape
     one = (S,)
@@ -886,11 +893,11 @@ def pa_build_tables(block_tables, context_lens, new_tokens, free_list, num_free,
     _want(query_start.shape == (S + 1,), "query_start must be [S + 1]")
     _want(num_free.numel() == 1 and num_free_out.numel() == 1, "num_free and num_free_out hold one number")
     _want(free_list.dim() == 1 and slot_mapping.dim() == 1, "free_list and slot_mapping must have one dimension")
-    device = _on_device(_TABLE_NAMES, tensors)
+    dev, device = _on_device(_TABLE_NAMES, tensors)
     _call("pa_build_tables", device, block_tables.data_ptr(), W, context_lens_out.data_ptr(),
           context_lens.data_ptr(), new_tokens.data_ptr(), S, free_list.data_ptr(), free_list.shape[0],
           num_free_out.data_ptr(), num_free.data_ptr(), block_size, granted.data_ptr(), query_start.data_ptr(),
-          slot_mapping.data_ptr(), slot_mapping.shape[0], _raw_stream(stream, block_tables))
+          slot_mapping.data_ptr(), slot_mapping.shape[0], _raw_stream(stream, dev))
 
 
 def pa_kv_transfer_worthwhile(reusable_tokens: int, threshold_tokens: int = 64) -> bool:
