@@ -447,7 +447,7 @@ pa_status pa_scatter_blocks(const void *staging_k, const void *staging_v, void *
  * (copy-on-write) and pa_q8_swap_blocks (preemption) move whole blocks.  The cache needs
  * no initialisation: a block's scale is set when its first row is written.
  * pa_q8_block_bytes / pa_q8_scales_offset: (size_t)-1 for sizes that are not built
- * (head_dim 64 or 128, block_size 16 or 32).
+ * (head_dim 64 or 128, block_size 16 or 32, up to 65535 kv heads are).
  */
 size_t pa_q8_block_bytes(int num_kv_heads, int head_dim, int block_size);
 size_t pa_q8_scales_offset(int num_kv_heads, int head_dim, int block_size);
@@ -473,7 +473,7 @@ size_t pa_q8_scales_offset(int num_kv_heads, int head_dim, int block_size);
  * they were.
  *
  * No block may be written for two sequences in one call (apply the step's copy-on-write
- * pairs first, pa_q8_copy_blocks).  Rows at negative positions, past the table's
+ * pairs first, pa_q8_copy_blocks), nor stand twice among the entries that one writes.  Rows at negative positions, past the table's
  * max_blocks_per_seq * block_size, of blocks outside [0, num_blocks), and rows of k and
  * v from query_start[num_seqs] on (padding) are skipped; nothing is accessed outside the
  * arguments.  Results do not depend on the order in which tokens arrive within a call.
@@ -561,9 +561,9 @@ pa_status pa_q8_swap_blocks(const void *src_cache, void *dst_cache, const int32_
  * it is negative; pushes past num_blocks are dropped.  Nothing is accessed outside the
  * arguments.
  *   free_list         device int32 [num_blocks]
- * Errors: PA_ERR_INVALID (null or misaligned pointer, non-positive num_blocks,
- *   block_size or max_blocks_per_seq, num_blocks or max_blocks_per_seq * block_size >=
- *   2^31), PA_ERR_CUDA.  num_seqs = 0 still pads the slot map.
+ * Errors: PA_ERR_INVALID (null or misaligned pointer, negative num_seqs or num_slots,
+ *   non-positive num_blocks, block_size or max_blocks_per_seq, num_blocks or
+ *   max_blocks_per_seq * block_size >= 2^31), PA_ERR_CUDA.  num_seqs = 0 still pads the slot map.
  */
 pa_status pa_build_tables(int32_t *block_tables, int max_blocks_per_seq, int32_t *context_lens_out,
                           const int32_t *context_lens, const int32_t *new_tokens, int num_seqs,

@@ -838,34 +838,45 @@ def pa_q8_decode(out, q, kv_cache, block_tables, context_lens, scale: float, num
     return out
 
 
+def _check_pairs(pairs, *pools):
+    T = _torch()
+    if pairs.dtype != T.int32:
+        raise TypeError("src_dst_pairs must be int32")
+    _want(pairs.dim() == 2 and pairs.shape[1] == 2, "src_dst_pairs must be [n, 2]")
+    for pool in pools:
+        if pool.dtype != T.uint8:
+            raise TypeError("the pools must be uint8")
+        _want(pool.dim() == 2, "the pools must be [num_blocks, pa_q8_block_bytes(...)]")
+
+
 def pa_q8_copy_blocks(kv_cache, src_dst_pairs, stream=None):
     """Block dst becomes a copy of block src, codes and scales, for every (src, dst) row of
     the int32 [n, 2] pairs."""
-    import torch
-    if src_dst_pairs.dtype != torch.int32:
-        raise TypeError("src_dst_pairs must be int32")
+    _check_pairs(src_dst_pairs, kv_cache)
     n = src_dst_pairs.shape[0]
     if n == 0:
         return
     dev, device = _on_device(("kv_cache", "src_dst_pairs"), (kv_cache, src_dst_pairs))
     _call("pa_q8_copy_blocks", device, kv_cache.data_ptr(), src_dst_pairs.data_ptr(), n, kv_cache.shape[0],
-          _block_bytes(kv_cache), _raw_stream(stream, dev))
+          kv_cache.shape[1], _raw_stream(stream, dev))
 
 
 def pa_q8_swap_blocks(src_cache, dst_cache, src_dst_pairs, stream=None):
     """dst pool blocks <- src pool blocks, codes and scales, for each (src, dst) pair; pools
     are 8-bit caches on the device or in pinned host memory (pairs likewise)."""
-    import torch
-    if src_dst_pairs.dtype != torch.int32:
-        raise TypeError("src_dst_pairs must be int32")
-    _want(_block_bytes(src_cache) == _block_bytes(dst_cache), "the pools have blocks of different sizes")
+    _check_pairs(src_dst_pairs, src_cache, dst_cache)
+    _want(src_cache.shape[1] == dst_cache.shape[1], "the pools have blocks of different sizes")
     if src_dst_pairs.shape[0] == 0:
         return
-    st = _load().pa_q8_swap_blocks(_dev_ptr(src_cache, "src_cache"), _dev_ptr(dst_cache, "dst_cache"),
-                                   _dev_ptr(src_dst_pairs, "src_dst_pairs"), int(src_dst_pairs.shape[0]),
-                                   int(src_cache.shape[0]), int(dst_cache.shape[0]), _block_bytes(src_cache),
-                                   _stream(stream))
-    _check(st, "pa_q8_swap_blocks")
+    src, dst = _dev_ptr(src_cache, "src_cache"), _dev_ptr(dst_cache, "dst_cache")
+    pairs = _dev_ptr(src_dst_pairs, "src_dst_pairs")
+    T = _torch()
+    devs = {t.get_device() for t in (src_cache, dst_cache, src_dst_pairs)} - {-1}
+    _want(len(devs) < 2, "the pools and pairs are on different devices")
+    dev = devs.pop() if devs else T.current_device()
+    _call("pa_q8_swap_blocks", None if dev == T.current_device() else T.device(dev), src, dst, pairs,
+          src_dst_pairs.shape[0], src_cache.shape[0], dst_cache.shape[0], src_cache.shape[1],
+          _raw_stream(stream, dev))
 
 
 def pa_build_tables(block_tables, context_lens, new_tokens, free_list, num_free, block_size: int, slot_mapping,

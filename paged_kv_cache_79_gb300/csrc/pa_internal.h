@@ -151,8 +151,8 @@ struct DecodeLaunch {
 // One block of the cache: the e4m3 codes [Hkv][K, V][B][d], then the scales, fp32
 // [Hkv, rounded up to even][K, V], padded to 128 bytes.  A kv head's K and V codes of a
 // block are adjacent, so one copy brings both as one contiguous run (a 16-bit block's
-// [B][Hkv][d] order would cut the 8-bit tile into pieces of d bytes); two heads' scales
-// are the 16 bytes a bulk copy moves at least.
+// [B][Hkv][d] order would cut the 8-bit tile into pieces of d bytes).  The scales of all
+// heads lie together, a pair of heads on each 16 bytes.
 struct Q8Layout {
     size_t scales;  // byte offset of the scales in a block
     size_t bytes;   // bytes per block

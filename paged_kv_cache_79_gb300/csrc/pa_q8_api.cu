@@ -29,8 +29,8 @@ pa_status check_sizes(int num_blocks, int max_blocks, int num_kv_heads, int head
         return PA_ERR_UNSUPPORTED;
     if ((long long)num_blocks * block_size >= (1ll << 31) || (long long)max_blocks * block_size >= (1ll << 31))
         return PA_ERR_INVALID;
-    // (the head and block strides of the tensor map must stay below 2^40 bytes)
-    if (q8_layout(block_size, num_kv_heads, head_dim).bytes >= (1ull << 40))
+    // (a block then stays below 2^30 bytes, and a run of tokens times its heads below 2^31)
+    if (num_kv_heads > 65535)
         return PA_ERR_UNSUPPORTED;
     return PA_OK;
 }

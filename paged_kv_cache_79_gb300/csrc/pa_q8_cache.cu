@@ -301,8 +301,8 @@ cudaError_t launch(const Q8AppendParams &p, int sms, cudaStream_t stream)
     // number of blocks a chunk can be expected to touch, and no more than twelve CTAs per
     // SM in all, so that long prompts' CTAs find their sequences once for several tiles
     // each (16 prompts, 40 heads: 96, 92 and 95 us with 6, 12 and 20).
-    const long long chunks = (p.num_tokens + kChunk - 1) / kChunk;
-    const long long runs = p.query_start ? (p.num_tokens + BS - 1) / BS + p.num_seqs : p.num_tokens;
+    const long long chunks = ((long long)p.num_tokens + kChunk - 1) / kChunk;
+    const long long runs = p.query_start ? ((long long)p.num_tokens + BS - 1) / BS + p.num_seqs : p.num_tokens;
     const long long per_chunk = ((runs < p.num_tokens ? runs : p.num_tokens) + chunks - 1) / chunks;
     const long long most = (per_chunk * 2 * p.num_kv_heads + kAppendWarps - 1) / kAppendWarps;
     const long long fill = (12ll * sms + chunks - 1) / chunks;

@@ -97,7 +97,7 @@ def append(cache, k, v, bt, cl, qs=None):
 
 def decode(cache, q, bt, cl, scale):
     """(out, abs, smax): out [S, Hq, d] float64; abs = sum p |v| / sum p, the size that
-    rounding errors of p are relative to; smax [S, Hq] = largest scale * sum |q k|."""
+    rounding errors of p are relative to; smax [S, Hq] = largest |scale| * sum |q k|."""
     s_, hq, d = q.shape
     g = hq // cache.hkv
     out = np.zeros((s_, hq, d))
@@ -118,7 +118,7 @@ def decode(cache, q, bt, cl, scale):
             p = np.exp(sc - sc.max())
             out[s, h] = p @ val / p.sum()
             size[s, h] = p @ np.abs(val) / p.sum()
-            smax[s, h] = np.max(scale * (np.abs(key) @ np.abs(q[s, h])))
+            smax[s, h] = np.max(abs(scale) * (np.abs(key) @ np.abs(q[s, h])))
     return out, size, smax
 
 

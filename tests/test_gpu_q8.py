@@ -2,7 +2,7 @@
 quantising append byte for byte, the decode within the rounding of its terms.
 
 Tolerance of the decode, elementwise, with u_T = finfo(T).eps / 2 the output's rounding,
-A = sum p |v| / sum p and S = max_t scale * sum |q k| (both from the model):
+A = sum p |v| / sum p and S = max_t |scale| * sum |q k| (both from the model):
     u_T max(|out|, N_T) + A (r + 2 ds + (n / 16 + 8) 2^-23)
 N_T the type's smallest normal number: below it the steps no longer shrink with the
     value, so the output's rounding stays half the smallest step, u_T N_T (fp16: 2^-25)
@@ -328,6 +328,81 @@ def test_a_cache_past_four_gigabytes():
     assert not cache[:n - m].any()
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.2, 3.0])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_softmax_scales_of_any_sign(dtype, scale):
+    c, q, bt, cl = decode_case(23, dtype, 64, 16, 6, 2, [700, 1, 33, 0], spread=20.0, exps=(-6, -4))
+    check_decode(run_decode(c, q, bt, cl, scale, 6), c, q, bt, cl, scale, dtype)
+
+
+@pytest.mark.parametrize("dtype,hq,hkv", [("f16", 13, 1), ("f32", 30, 2), ("bf16", 17, 1)])
+def test_many_short_sequences_of_wide_groups(dtype, hq, hkv):
+    """Units of one stage with more than 8 rows, empty ones between them."""
+    lens = [(i * 11) % 37 for i in range(350)] + [1200]
+    c, q, bt, cl = decode_case(24, dtype, 128, 16, hq, hkv, lens)
+    check_decode(run_decode(c, q, bt, cl, 0.1, hq), c, q, bt, cl, 0.1, dtype)
+
+
+def test_infinite_and_nan_queries_stay_in_their_rows():
+    c, q, bt, cl = decode_case(25, "f16", 128, 16, 8, 2, [900, 20], stale=False)
+    bad = q.clone()
+    bad[0, 3, 5], bad[1, 6, 0] = float("nan"), float("inf")
+    got = run_decode(c, bad, bt, cl, 0.1, 8)
+    assert got[0, 3].isnan().all() and got[1, 6].isnan().all()
+    got[0, 3] = got[1, 6] = 0                             # the other rows: as without them
+    want, size, smax = M.decode(c, q.double().numpy(), bt, cl, 0.1)
+    want[0, 3] = want[1, 6] = 0
+    assert (np.abs(got.double().cpu().numpy() - want) <= tolerance("f16", 128, want, size, smax, cl)).all()
+
+
+def test_views_at_an_offset_and_refused_tensors():
+    """Slices of larger buffers: rows of q and out, blocks of a cache; nothing around them
+    changes.  Strided and misaligned ones are refused."""
+    hq, hkv, b, d = 4, 2, 16, 64
+    c, q, bt, cl = decode_case(26, "f16", d, b, hq, hkv, [70, 9, 33], stale=False)
+    want = run_decode(c, q, bt, cl, 0.1, hq)
+    pool = torch.full((len(c.raw) + 4, c.raw.shape[1]), 0x5A, dtype=torch.uint8, device=DEV)
+    cache = pool[2:-2]
+    cache.copy_(dev(c.raw))
+    codes, scales = P.q8_views(cache, hkv, d, b)
+    assert torch.equal(scales.cpu(), torch.from_numpy(c.scales.copy()))
+    assert torch.equal(codes.view(torch.uint8).cpu(), torch.from_numpy(c.codes.copy()))
+    qq = torch.zeros(5, hq, d, dtype=torch.float16, device=DEV)
+    qq[1:4] = q.to(DEV)
+    outs = torch.full((5, hq, d), 7.0, dtype=torch.float16, device=DEV)
+    tables, lens = torch.cat([dev(bt)[:1], dev(bt)]), torch.cat([dev(cl)[:1], dev(cl)])
+    P.pa_q8_decode(outs[1:4], qq[1:4], cache, tables[1:], lens[1:], 0.1, hq, hkv, d, b)
+    assert torch.equal(outs[1:4], want) and (outs[0] == 7).all() and (outs[4] == 7).all()
+    k = torch.randn(5, hkv, d, device=DEV, dtype=torch.float16)
+    cl2 = cl + 1
+    bt2 = np.concatenate([bt, np.full((3, 1), -1, dtype=np.int32)], axis=1)
+    P.pa_q8_append(k[1:4], k[2:], cache, dev(bt2), dev(cl2), b)
+    M.append(c, k[1:4].double().cpu().numpy(), k[2:].double().cpu().numpy(), bt2, cl2)
+    assert np.array_equal(cache.cpu().numpy(), c.raw)
+    assert (pool[:2] == 0x5A).all() and (pool[-2:] == 0x5A).all()
+    with pytest.raises(ValueError, match="contiguous"):
+        P.pa_q8_decode(outs[::2], qq[::2], cache, dev(bt), dev(cl), 0.1, hq, hkv, d, b)
+    with pytest.raises(ValueError, match="contiguous"):
+        P.pa_q8_append(k[:3], k[:3], cache, torch.cat([dev(bt2)] * 2, 1)[:, ::2][:, :bt2.shape[1]], dev(cl2), b)
+    flat = torch.zeros(3 * hq * d + 8, dtype=torch.float16, device=DEV)
+    with pytest.raises(P.PagedKVError):                   # 2 bytes off a 16-byte boundary
+        P.pa_q8_decode(want, flat[1:1 + 3 * hq * d].view(3, hq, d), cache, dev(bt), dev(cl), 0.1, hq, hkv, d, b)
+    with pytest.raises(ValueError, match="CUDA"):
+        P.pa_q8_decode(want, q.to(DEV), cache, torch.from_numpy(bt), dev(cl), 0.1, hq, hkv, d, b)
+
+
+def test_empty_batches():
+    cache = P.alloc_q8_cache(3, 2, 64, 16)
+    e = torch.zeros(0, 4, 64, device=DEV)
+    bt, cl = torch.zeros(0, 2, dtype=torch.int32, device=DEV), torch.zeros(0, dtype=torch.int32, device=DEV)
+    P.pa_q8_decode(e, e, cache, bt, cl, 0.1, 4, 2, 64, 16)
+    P.pa_q8_append(e[:, :2].contiguous(), e[:, :2].contiguous(), cache, bt, cl, 16)
+    one = torch.zeros(1, 2, dtype=torch.int32, device=DEV)
+    P.pa_q8_append(e[:, :2].contiguous(), e[:, :2].contiguous(), cache, one, one[0, :1].contiguous(), 16,
+                   query_start=torch.zeros(2, dtype=torch.int32, device=DEV))
+    assert not cache.any()
+
+
 # ---- append ------------------------------------------------------------------
 def append_case(seed, dtype, d, b, hkv, old, new, spread=0.7, extra=3):
     """A cache whose sequences hold `old` rows, and rows for `new` more."""
@@ -475,6 +550,21 @@ def test_append_in_a_graph():
         torch.cuda.synchronize()
         M.append(c, k.double().cpu().numpy(), v.double().cpu().numpy(), bt, cl)
     assert np.array_equal(cache.cpu().numpy(), c.raw)
+
+
+def test_appends_on_two_streams_at_once():
+    hkv, b, d = 3, 16, 128
+    jobs = []
+    for i, st in enumerate([torch.cuda.Stream(), torch.cuda.Stream()]):
+        c, k, v, bt, cl, qs = append_case(70 + i, "bf16", d, b, hkv, [5, 40, 0], [100, 3, 17 + i])
+        jobs.append((c, k, v, bt, cl, qs, dev(c.raw), [x.to(DEV) for x in (k, v)] + [dev(x) for x in (bt, cl, qs)], st))
+    torch.cuda.synchronize()
+    for c, k, v, bt, cl, qs, cache, (kd, vd, btd, cld, qsd), st in jobs:
+        P.pa_q8_append(kd, vd, cache, btd, cld, b, query_start=qsd, stream=st)
+    torch.cuda.synchronize()
+    for c, k, v, bt, cl, qs, cache, _, _ in jobs:
+        M.append(c, k.double().numpy(), v.double().numpy(), bt, cl, qs)
+        assert np.array_equal(cache.cpu().numpy(), c.raw)
 
 
 # ---- block moves ---------------------------------------------------------------

@@ -107,6 +107,37 @@ def test_out_of_range_inputs_stay_inside():
     check(bt, cl, np.full(reqs, -1), free, 28, b, 3)  # more blocks released than the list holds
 
 
+@pytest.mark.parametrize("slots", [4095, 4096, 4097, 9000])
+def test_slot_maps_around_the_second_kernel(slots):
+    """Up to 4096 slots one kernel writes the map, above a second one: exact fits and
+    padding on both sides, few requests and many."""
+    b = 16
+    for reqs, each in ((1, slots), (1, slots - 1), (3, slots // 3), (700, 5), (2050, 1)):
+        width = (each + 40) // b + 2
+        rng, bt, cl, free, nfree = batch(slots + reqs, reqs, b, width, reqs * width, 40)
+        check(bt, cl, np.full(reqs, each), free, nfree, b, slots)
+
+
+def test_two_at_once_on_side_streams():
+    jobs = []
+    for i, n in enumerate((30, 5000)):                  # one kernel, two kernels
+        rng, bt, cl, free, nfree = batch(40 + i, 20, 16, 300, 6000, 60)
+        new = rng.integers(0, n // 20 + 1, size=20)
+        new[3] = -1
+        t = [dev(x) for x in (bt, cl, new.astype(np.int32), free, np.array([nfree], dtype=np.int32))]
+        out = [torch.zeros(n, dtype=torch.int64, device=DEV), torch.zeros(21, dtype=torch.int32, device=DEV),
+               torch.zeros(20, dtype=torch.int32, device=DEV)]
+        jobs.append((t, out, M.build_tables(bt, cl, new, free, nfree, 16, n), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for t, out, _, st in jobs:
+        P.pa_build_tables(*t, 16, *out, stream=st)
+    torch.cuda.synchronize()
+    for t, out, want, _ in jobs:
+        got = (t[0], t[1], t[3], t[4], out[2], out[1], out[0])
+        for name, g, w in zip(NAMES, got, want):
+            assert np.array_equal(np.asarray(g.cpu()).reshape(np.shape(w)), w), name
+
+
 def test_no_requests():
     slots, qs = torch.full((5,), 7, dtype=torch.int64, device=DEV), torch.full((1,), 7, dtype=torch.int32, device=DEV)
     e = torch.zeros(0, dtype=torch.int32, device=DEV)

@@ -33,7 +33,8 @@ def test_block_layout(hkv, d, b):
 
 
 def test_layout_of_sizes_that_are_not_built():
-    for hkv, d, b in ((0, 128, 16), (4, 96, 16), (4, 256, 16), (4, 128, 8), (4, 128, 64), (-1, 64, 32)):
+    for hkv, d, b in ((0, 128, 16), (4, 96, 16), (4, 256, 16), (4, 128, 8), (4, 128, 64), (-1, 64, 32),
+                      (65536, 64, 16)):
         with pytest.raises(P.PagedKVError):
             P.pa_q8_block_bytes(hkv, d, b)
     with pytest.raises(ValueError):
@@ -58,6 +59,7 @@ def _append(**kw):
     (dict(NB=0), P.PA_ERR_INVALID), (dict(Hkv=0), P.PA_ERR_INVALID), (dict(NB=1 << 28), P.PA_ERR_INVALID),
     (dict(W=1 << 28), P.PA_ERR_INVALID),
     (dict(D=96), P.PA_ERR_UNSUPPORTED), (dict(B=8), P.PA_ERR_UNSUPPORTED), (dict(dt=5), P.PA_ERR_UNSUPPORTED),
+    (dict(Hkv=1 << 16), P.PA_ERR_UNSUPPORTED),
     (dict(S=0), P.PA_OK), (dict(N=0), P.PA_OK),
 ])
 def test_append_refusals(kw, want):
@@ -79,6 +81,7 @@ def _decode(**kw):
     (dict(Hq=5), P.PA_ERR_INVALID), (dict(Hq=0), P.PA_ERR_INVALID), (dict(Hkv=0), P.PA_ERR_INVALID),
     (dict(NB=0), P.PA_ERR_INVALID), (dict(W=0), P.PA_ERR_INVALID), (dict(NB=1 << 27), P.PA_ERR_INVALID),
     (dict(D=32), P.PA_ERR_UNSUPPORTED), (dict(B=64), P.PA_ERR_UNSUPPORTED), (dict(dt=3), P.PA_ERR_UNSUPPORTED),
+    (dict(Hq=1 << 17, Hkv=1 << 16), P.PA_ERR_UNSUPPORTED),
     (dict(S=0), P.PA_OK),
 ])
 def test_decode_refusals(kw, want):
@@ -154,6 +157,30 @@ def test_binding_refuses_wrong_tensors():
         P.pa_build_tables(bt, cl, cl, qs, one, 16, slots, cl, cl)
     with pytest.raises(ValueError, match="num_free"):
         P.pa_build_tables(bt, cl, cl, qs, cl, 16, slots, qs, cl)
+
+
+def test_binding_refuses_wrong_moves():
+    cache = torch.zeros(4, P.pa_q8_block_bytes(2, 64, 16), dtype=torch.uint8)
+    pairs = torch.zeros(3, 2, dtype=torch.int32)
+    for wrong in (pairs[0], pairs[:, :1].contiguous(), torch.zeros(3, 3, dtype=torch.int32)):
+        with pytest.raises(ValueError, match=r"\[n, 2\]"):
+            P.pa_q8_copy_blocks(cache, wrong)
+        with pytest.raises(ValueError, match=r"\[n, 2\]"):
+            P.pa_q8_swap_blocks(cache, cache, wrong)
+    with pytest.raises(TypeError):
+        P.pa_q8_copy_blocks(cache, pairs.long())
+    with pytest.raises(TypeError):
+        P.pa_q8_copy_blocks(cache.view(torch.int32), pairs)
+    with pytest.raises(ValueError, match="pools"):
+        P.pa_q8_copy_blocks(cache.view(-1), pairs)
+    with pytest.raises(ValueError, match="different sizes"):
+        P.pa_q8_swap_blocks(cache, torch.zeros(4, 256, dtype=torch.uint8), pairs)
+    with pytest.raises(ValueError, match="CUDA"):
+        P.pa_q8_copy_blocks(cache, pairs)
+    with pytest.raises(ValueError, match="pinned"):
+        P.pa_q8_swap_blocks(cache, cache, pairs)
+    P.pa_q8_copy_blocks(cache, pairs[:0])
+    P.pa_q8_swap_blocks(cache, cache, pairs[:0])
 
 
 # ---- the models' pins -----------------------------------------------------------
