@@ -490,6 +490,7 @@ __device__ __forceinline__ bool consumer_sync(const DecodeParams &p, const CtaSt
 template <typename T, int D, int BS, int kBPS, int kChunks, int kTileBytes, int kStages, int kCopy>
 struct Producer {
     static constexpr bool kCountParts = true;  // emit_unit looks for CTAs without positions
+    static constexpr int kLead = kUnitCost;    // a unit's charged positions lie before its stages
     const DecodeParams &p;
     const CUtensorMap *tk;
     const CUtensorMap *tv;
@@ -912,7 +913,7 @@ __device__ __forceinline__ bool emit_unit(const DecodeParams &p, Prod &pr, const
                                           long long cta, int bps, int div)
 {
     const long long ns = su.ns;
-    const long long ra = a + kUnitCost;  // first real stage
+    const long long ra = a + Prod::kLead;  // first real stage
     const long long rb = ra + ns;
     Item it;
     it.len = su.len;

@@ -142,7 +142,7 @@ constexpr int hold(int rows, int elem_bytes, int head_dim)  // loads of 16 bytes
 
 // kRows: rows of a run whose loads are kept in registers, and all in flight at once; a
 // longer run's other rows are read twice.  Up to eight loads per lane leave room for four
-// CTAs on an SM (16 prompts, 40 heads, 16-row blocks: 92 us with two, 81 with three, 80
+// CTAs on an SM (16 prompts, 40 heads, 16-row blocks: 92 us with two, 81 with three, 79
 // with four).
 template <typename T, int D, int BS, int kRows>
 __global__ void __launch_bounds__(32 * kAppendWarps, hold(kRows, sizeof(T), D) <= 8 ? 4 : 2)
@@ -295,17 +295,17 @@ cudaError_t launch(const Q8AppendParams &p, int sms, cudaStream_t stream)
 {
     // Short runs (up to four rows per sequence on average, as in a decode step) take the
     // variant that keeps four rows: more CTAs fit an SM, and a step's tiles all run at
-    // once.
+    // once (256 single tokens, 8 heads, 32-row blocks: 3.2 us against 6.1).
     const bool few = p.num_tokens <= 4ll * p.num_seqs;
     // CTAs over the chunks, then over a chunk's tiles: at most one tile per warp for the
-    // number of blocks a chunk can be expected to touch, and no more than twelve CTAs per
+    // number of blocks a chunk can be expected to touch, and no more than twenty CTAs per
     // SM in all, so that long prompts' CTAs find their sequences once for several tiles
-    // each (16 prompts, 40 heads: 96, 92 and 95 us with 6, 12 and 20).
+    // each (16 prompts, 40 heads: 82.4, 79.2 and 78.4 us with 6, 12 and 20).
     const long long chunks = ((long long)p.num_tokens + kChunk - 1) / kChunk;
     const long long runs = p.query_start ? ((long long)p.num_tokens + BS - 1) / BS + p.num_seqs : p.num_tokens;
     const long long per_chunk = ((runs < p.num_tokens ? runs : p.num_tokens) + chunks - 1) / chunks;
     const long long most = (per_chunk * 2 * p.num_kv_heads + kAppendWarps - 1) / kAppendWarps;
-    const long long fill = (12ll * sms + chunks - 1) / chunks;
+    const long long fill = (20ll * sms + chunks - 1) / chunks;
     const long long y = most < fill ? most : fill;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -41,10 +41,11 @@
 #pragma once
 
 // Stream positions charged per unit for its fixed cost, in this kernel's ring stages
-// (8 KB at 128 dims, half of pa_decode's): 64 ragged sequences of 64 / 8 heads took
-// 162, 153, 146 and 146 us with 4, 8, 12 and 16.
+// (8 KB at 128 dims, half of pa_decode's).  With 6, 8, 12, 16 and 20: 64 ragged sequences
+// of 64 / 8 heads took 140.7, 140.6, 141.4, 142.3 and 144.6 us, 8 of 40 / 40 heads 25.5,
+// 25.2, 25.9, 26.6 and 25.9, 32 log-uniform ones of 32 / 8 heads 302, 300, 303, 306, 302.
 #ifndef PA_UNIT_COST
-#define PA_UNIT_COST 12
+#define PA_UNIT_COST 8
 #endif
 #include "pa_decode.cuh"
 
@@ -93,6 +94,11 @@ __device__ __forceinline__ uint32_t tile_unit(int tok, int u)
     return (uint32_t)(row * 128 + ((unit ^ (row & 7)) << 4));
 }
 
+// Half of a unit's charged positions lie before its stages and half behind: both parts of
+// a unit cut in the middle store, count and merge.  (152 units of 26 stages on 304 CTAs,
+// each cut once: 15.8 us with all of the charge before the stages, 13.8 with half.)
+constexpr int kLead8 = kUnitCost / 2;
+
 constexpr int kThreads8 = kThreads + 32;  // one warp more than pa_decode: the scales'
 
 constexpr int kMergeRows = 4;  // merge rows at least: merge8 works in them
@@ -139,6 +145,7 @@ struct Producer8 {
     // G = ceil(total / divisor) <= total: none is without (a division for each part, 38 of
     // them, kept the first copy of a single sequence's one head back by 5 us)
     static constexpr bool kCountParts = false;
+    static constexpr int kLead = kLead8;
     using C = Cfg8<T, D, BS, NT>;
     const DecodeParams &p;
     const CUtensorMap *map;
@@ -268,6 +275,7 @@ struct Producer8 {
 template <typename T, int D, int BS, int NT>
 struct ScaleWarp {
     static constexpr bool kCountParts = false;
+    static constexpr int kLead = kLead8;
     using C = Cfg8<T, D, BS, NT>;
     const DecodeParams &p;
     const Q8Params &q8;
@@ -299,6 +307,15 @@ struct ScaleWarp {
         int id = block_id(it, row, it.j0 + lane);
         int next_id = block_id(it, row, it.j0 + 32 + lane);
         float2 s = scales_of(it, id);
+        // A split unit's counter takes this launch's epoch here, so that the parts' counts
+        // need no exchange (0.4 us of 12 where two parts of every unit end together): a value
+        // read as another epoch's changes to this one's only.
+        unsigned long long *const ctr = p.counters + it.c_first;
+        if (it.partial && lane == 0) {
+            const unsigned long long seen = *reinterpret_cast<volatile unsigned long long *>(ctr);
+            if ((unsigned int)(seen >> 32) != p.epoch)
+                atomicCAS(ctr, seen, (unsigned long long)p.epoch << 32);
+        }
         for (int jb = it.j0; jb < it.j1; jb += 32) {
             const float2 next_s = scales_of(it, next_id);
             next_id = block_id(it, row, jb + 64 + lane);
@@ -801,6 +818,8 @@ __device__ __forceinline__ void finalize8(const DecodeParams &p, const Item &it,
     }
 }
 
+constexpr int kFlight = 8;  // parts of a split unit that a thread reads at once
+
 // Floats of the merge rows (make_layout8) that merge8 may use.
 __device__ __forceinline__ int merge_room(int rows_cap, int D)
 {
@@ -808,7 +827,7 @@ __device__ __forceinline__ int merge_room(int rows_cap, int D)
 }
 
 // Merge the partials of a split unit into its output rows by the log-sum-exp rule, all
-// consumer warps together: every (row, part)'s log2-sum-exp in one round of loads, a row's
+// consumer warps together, where they are many: every (row, part)'s log2-sum-exp in one round of loads, a row's
 // weights by one warp, then the weighted rows, D / 4 threads per row with two rows and
 // eight parts of each in flight; with fewer rows than such groups of threads, several
 // groups share a row's parts.  (merge_split_unit goes row by row with four parts in
@@ -819,7 +838,6 @@ __device__ __forceinline__ bool merge8(const DecodeParams &p, const Item &it, co
 {
     constexpr int LR = D / 4;                             // threads on a row
     constexpr int kGroups = 32 * kConsumerWarps / LR;
-    constexpr int kFlight = 8;
     const int n = it.nparts, tid = warp * 32 + lane;
     // every CTA up to G has positions, so the parts' slots are consecutive (split_slot)
     auto slot = [&](int i) { return (2 * (it.c_first + i) + (i == 0 ? 1 : 0)) * kHeadsPerItem; };
@@ -912,8 +930,70 @@ __device__ __forceinline__ bool merge8(const DecodeParams &p, const Item &it, co
     return consumer_sync(p, c, sph);  // the merge rows are read before the next item's come
 }
 
+// The same with a row for each thread group and nothing to exchange: rounds of eight
+// parts' log2-sum-exps and rows, read at once.  (152 units of 13 rows of 64 dims, each cut
+// once: 15.7 us against merge8's 17.5; 104 cut in three: 13.5 against 15.4.)
+template <typename T, int D>
+__device__ __forceinline__ void merge_few(const DecodeParams &p, const Item &it, int tid)
+{
+    constexpr int LR = D / 4;
+    const int n = it.nparts, col = tid % LR * 4;
+    for (int r = tid / LR; r < it.rows; r += 32 * kConsumerWarps / LR) {
+        float M = -INFINITY, W = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int k0 = 0; k0 < n; k0 += kFlight) {
+            float lse[kFlight];
+            float4 v[kFlight];
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) {
+                // (the parts' slots: merge8)
+                const int k = min(k0 + i, n - 1);
+                const int row = (2 * (it.c_first + k) + (k == 0 ? 1 : 0)) * kHeadsPerItem + r;
+                lse[i] = __ldcg(p.part_lse + row);
+                v[i] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + (size_t)row * D + col));
+            }
+            float m = M;
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i)
+                m = fmaxf(m, lse[i]);
+            const float c = M == -INFINITY ? 0.f : exp2f(M - m);
+            M = m;
+            W *= c;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                o[e] *= c;
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) {
+                if (k0 + i < n && lse[i] != -INFINITY) {
+                    const float w = exp2f(lse[i] - M);
+                    W += w;
+                    o[0] = fmaf(w, v[i].x, o[0]);
+                    o[1] = fmaf(w, v[i].y, o[1]);
+                    o[2] = fmaf(w, v[i].z, o[2]);
+                    o[3] = fmaf(w, v[i].w, o[3]);
+                }
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            o[e] = W > 0.f ? o[e] / W : 0.f;
+        store4(reinterpret_cast<T *>(p.out) + ((size_t)it.seq * p.num_q_heads + it.qrow0 + r) * D + col, o);
+    }
+}
+
+// Whether merge_few's rounds take less than merge8's two exchanges: up to 16 parts, or 40
+// where the rows fill the groups of threads once.  (4 rows of 128 dims, 38 parts, one
+// sequence of 32 / 8 heads: 19.4 us against 20.6; 8 rows, 38 parts: 16.4 against 14.6; 1
+// row, 38 parts: 12.6 against 11.3.)
+template <int D>
+__device__ __forceinline__ bool few_rounds(const Item &it)
+{
+    constexpr int kGroups = 128 * kConsumerWarps / D;
+    return it.nparts <= (it.rows > kGroups / 2 && it.rows <= kGroups ? 40 : 16);
+}
+
 // Count this CTA's part of a split unit; whether it was the last.  `seen`: the counter as
-// read before.  As count_partial, but where others have counted in this launch already
+// read before.  As count_partial, but where the counter has this launch's epoch already
 // an add takes the place of further exchanges: the parts of one long unit finish together,
 // and each round of exchanges lets one of them through (38 parts took 20 us).
 __device__ __forceinline__ bool count8(const DecodeParams &p, const Item &it, unsigned long long seen)
@@ -973,6 +1053,10 @@ __device__ __forceinline__ bool finish8(const DecodeParams &p, const Item &it, c
         return false;
     if (!*c.merge)
         return true;
+    if (few_rounds<D>(it)) {
+        merge_few<T, D>(p, it, warp * 32 + lane);
+        return true;
+    }
     // weights and, with few rows, a row per group of threads
     if (it.rows * it.nparts + 3 + 4 * 128 <= merge_room(rows_cap, D))
         return merge8<T, D>(p, it, c, sph, warp, lane, c.macc);

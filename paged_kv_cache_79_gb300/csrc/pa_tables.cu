@@ -190,7 +190,8 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const __grid_
 
 // The slot map from the finished tables: kSlotsPerWarp consecutive slots per warp, whose
 // requests one search finds (few, since a warp's reads of them depend on each other: 64
-// prompts of up to 8000 tokens took 12.2 us with 256, 1001 mixed requests 17.2).
+// prompts of up to 8000 tokens take 10.5 us, with 256 11.9; 1001 mixed requests 11.8 and
+// 16.1; with 32 slots 10.9 and 11.0).
 constexpr int kSlotWarps = 8;
 constexpr int kSlotsPerWarp = 64;
 __global__ void __launch_bounds__(32 * kSlotWarps) build_slots_kernel(const __grid_constant__ TablesParams p)
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(32 * kSlotWarps) build_slots_kernel(const __gr
     const long long base = ((long long)blockIdx.x * kSlotWarps + (threadIdx.x >> 5)) * kSlotsPerWarp;
     const int total = p.query_start[p.num_seqs];
     const int B = p.block_size;
-    int s = -1, start = 0, end = 0;  // the lane's request and its slots
+    int s = -1, end = 0;  // the lane's request, and the end of its slots
     for (int k = 0; k < kSlotsPerWarp / 32; ++k) {
         const long long t0 = base + k * 32;
         if (t0 >= p.num_slots)
@@ -210,7 +211,6 @@ __global__ void __launch_bounds__(32 * kSlotWarps) build_slots_kernel(const __gr
         if (t0 < total && !__all_sync(0xffffffffu, s >= 0 && t < end)) {
             s = min(dev::find_sequence(p.query_start, p.num_seqs, (int)t0, lane,
                                        k == 0 ? -1 : __shfl_sync(0xffffffffu, s, 31)), p.num_seqs - 1);
-            start = p.query_start[s];
             end = p.query_start[s + 1];
         }
         int64_t slot = -1;

@@ -100,7 +100,9 @@ SHAPES += [("bf16", 128, 16, 12, 3, [3000, 1, 17, 4096, 2222, 16]), ("f16", 128,
            ("f16", 128, 32, 8, 8, [0, 0, 0]),
            # few rows and many parts: the ways in which a unit's parts are merged
            ("f32", 128, 16, 1, 1, [6000]), ("bf16", 64, 32, 2, 1, [20000, 3]), ("f16", 128, 32, 5, 1, [30000, 7]),
-           ("f16", 64, 16, 3, 1, [60000]), ("bf16", 128, 16, 3, 1, [9001, 9000]), ("f16", 64, 32, 16, 1, [40000])]
+           ("f16", 64, 16, 3, 1, [60000]), ("bf16", 128, 16, 3, 1, [9001, 9000]), ("f16", 64, 32, 16, 1, [40000]),
+           ("bf16", 64, 16, 32, 2, [4077, 4077]), ("f16", 128, 32, 32, 8, [4096]), ("f32", 64, 16, 16, 2, [9000, 8000]),
+           ("f16", 64, 32, 247, 19, [1664, 40, 1664, 1600]), ("bf16", 128, 16, 26, 2, [3000, 5000, 2990])]
 
 
 @pytest.mark.parametrize("dtype,d,b,hq,hkv,lens", SHAPES, ids=lambda v: str(v).replace(" ", "")[:40])
