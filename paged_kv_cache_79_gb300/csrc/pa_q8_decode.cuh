@@ -41,11 +41,11 @@
 #pragma once
 
 // Stream positions charged per unit for its fixed cost, in this kernel's ring stages
-// (8 KB at 128 dims, half of pa_decode's).  With 6, 8, 12, 16 and 20: 64 ragged sequences
-// of 64 / 8 heads took 140.7, 140.6, 141.4, 142.3 and 144.6 us, 8 of 40 / 40 heads 25.5,
-// 25.2, 25.9, 26.6 and 25.9, 32 log-uniform ones of 32 / 8 heads 302, 300, 303, 306, 302.
+// (8 KB, half of pa_decode's at 128 dims).  With 4, 6, 8, 10, 12 and 16: 64 ragged sequences
+// of 64 / 8 heads take 143, 140.4, 139.6, 139.4, 139.4 and 140.4 us, 8 of 40 / 40 heads 23.6,
+// 23.9, 23.7, 23.7, 24.2 and 24.9, 37 of 39 / 3 heads 19.5, 18.7, 18.4, 18.1, 18.0 and 18.3.
 #ifndef PA_UNIT_COST
-#define PA_UNIT_COST 8
+#define PA_UNIT_COST 10
 #endif
 #include "pa_decode.cuh"
 
@@ -60,8 +60,9 @@ namespace pagedkv {
 
 // NT: groups of 8 query rows an item may have (1 or 2).  The ring is as large as the
 // residency leaves room for beside the merge rows: two CTAs per SM, or one for fp32 with
-// 16 rows, whose registers allow no more (ragged batch of 13 heads per kv head, 128
-// dims: 43 us on two CTAs with 64 KB each, 48 on one with 80 KB).
+// 16 rows, whose registers allow no more.  (16 sequences of 2000 tokens, 104 / 8 heads, 128
+// dims: 30.7 us on two CTAs with 64 KB each, 34.8 on one with 80 KB; fp32 with 64 / 8
+// heads 23.3 and 29.4; fp32 with 104 / 8 37.1 on one CTA with 128 KB, 47.1 on two.)
 template <typename T, int D, int BS, int NT>
 struct Cfg8 {
     static constexpr int kCtas = sizeof(T) == 4 && NT == 2 ? 1 : 2;
