@@ -1122,7 +1122,7 @@ __global__ void __launch_bounds__(kThreads8, Cfg8<T, D, BS, NT>::kCtas)
             break;
         // A whole unit of at most one stage belongs to one warp, from the query rows to
         // the output, and the warps go on to the next items without meeting (400 sequences
-        // of 20 tokens, 8 heads: 39 us to 23).  With 9 heads or more per kv head there
+        // of 20 tokens, 8 heads: 39.6 us to 23.9).  With 9 heads or more per kv head there
         // are few such items, and the code for them costs registers that are short.
         const bool alone = NT == 1 && !it.partial && it.j1 - it.j0 <= C::kBPS;
         if (alone && warp != it.rot()) {
