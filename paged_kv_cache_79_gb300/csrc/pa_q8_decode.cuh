@@ -812,12 +812,15 @@ __device__ __forceinline__ void finalize8(const DecodeParams &p, const Item &it,
             continue;
         }
         if (other >= 0) {
+            // (a part whose scores are all -inf has no weight; without any weight: zeros)
             const float m2 = fmaxf(lse, lse2);
-            const float w0 = exp2f(lse - m2), w1 = exp2f(lse2 - m2), W = w0 + w1;
-            o[0] = (w0 * o[0] + w1 * o2.x) / W;
-            o[1] = (w0 * o[1] + w1 * o2.y) / W;
-            o[2] = (w0 * o[2] + w1 * o2.z) / W;
-            o[3] = (w0 * o[3] + w1 * o2.w) / W;
+            const float w0 = lse == -INFINITY ? 0.f : exp2f(lse - m2);
+            const float w1 = lse2 == -INFINITY ? 0.f : exp2f(lse2 - m2);
+            const float W = w0 + w1;
+            o[0] = W > 0.f ? (w0 * o[0] + w1 * o2.x) / W : 0.f;
+            o[1] = W > 0.f ? (w0 * o[1] + w1 * o2.y) / W : 0.f;
+            o[2] = W > 0.f ? (w0 * o[2] + w1 * o2.z) / W : 0.f;
+            o[3] = W > 0.f ? (w0 * o[3] + w1 * o2.w) / W : 0.f;
         }
         store4(reinterpret_cast<T *>(p.out) + ((size_t)it.seq * p.num_q_heads + it.qrow0 + r) * D + col, o);
     }
