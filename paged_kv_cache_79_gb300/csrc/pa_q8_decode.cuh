@@ -757,6 +757,22 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
     return true;
 }
 
+// One part of a split unit joins its row's merge: M the largest log2-sum-exp of the parts
+// at hand (a part without any weight, -inf, adds nothing).  A unit cut once is merged by
+// finalize8 or by merge_few, as its parts happen to end; both add them in slot order with
+// these operations, so that the result has the same bits either way.
+__device__ __forceinline__ void add_part(float (&o)[4], float &W, float M, float lse, const float4 &v)
+{
+    if (lse != -INFINITY) {
+        const float w = exp2f(lse - M);
+        W = __fadd_rn(W, w);
+        o[0] = __fmaf_rn(w, v.x, o[0]);
+        o[1] = __fmaf_rn(w, v.y, o[1]);
+        o[2] = __fmaf_rn(w, v.z, o[2]);
+        o[3] = __fmaf_rn(w, v.w, o[3]);
+    }
+}
+
 // ---------------------------------------------------------------------------
 // Merge the four consumer states of one item and store it, as finalize_item does, four
 // columns per thread and D / 4 threads per row, so that a row's weights are computed
@@ -811,16 +827,16 @@ __device__ __forceinline__ void finalize8(const DecodeParams &p, const Item &it,
                 p.part_lse[pr] = lse;
             continue;
         }
-        if (other >= 0) {
-            // (a part whose scores are all -inf has no weight; without any weight: zeros)
-            const float m2 = fmaxf(lse, lse2);
-            const float w0 = lse == -INFINITY ? 0.f : exp2f(lse - m2);
-            const float w1 = lse2 == -INFINITY ? 0.f : exp2f(lse2 - m2);
-            const float W = w0 + w1;
-            o[0] = W > 0.f ? (w0 * o[0] + w1 * o2.x) / W : 0.f;
-            o[1] = W > 0.f ? (w0 * o[1] + w1 * o2.y) / W : 0.f;
-            o[2] = W > 0.f ? (w0 * o[2] + w1 * o2.z) / W : 0.f;
-            o[3] = W > 0.f ? (w0 * o[3] + w1 * o2.w) / W : 0.f;
+        if (other >= 0) {  // both parts by slot, not by which of them ended first
+            const bool ahead = it.prow0 < other;
+            const float M2 = fmaxf(lse, lse2);
+            float W = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
+            const float4 mine = make_float4(o[0], o[1], o[2], o[3]);
+            add_part(y, W, M2, ahead ? lse : lse2, ahead ? mine : o2);
+            add_part(y, W, M2, ahead ? lse2 : lse, ahead ? o2 : mine);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                o[e] = W > 0.f ? y[e] / W : 0.f;
         }
         store4(reinterpret_cast<T *>(p.out) + ((size_t)it.seq * p.num_q_heads + it.qrow0 + r) * D + col, o);
     }
@@ -971,16 +987,9 @@ __device__ __forceinline__ void merge_few(const DecodeParams &p, const Item &it,
             for (int e = 0; e < 4; ++e)
                 o[e] *= c;
 #pragma unroll
-            for (int i = 0; i < kFlight; ++i) {
-                if (k0 + i < n && lse[i] != -INFINITY) {
-                    const float w = exp2f(lse[i] - M);
-                    W += w;
-                    o[0] = fmaf(w, v[i].x, o[0]);
-                    o[1] = fmaf(w, v[i].y, o[1]);
-                    o[2] = fmaf(w, v[i].z, o[2]);
-                    o[3] = fmaf(w, v[i].w, o[3]);
-                }
-            }
+            for (int i = 0; i < kFlight; ++i)
+                if (k0 + i < n)
+                    add_part(o, W, M, lse[i], v[i]);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e)

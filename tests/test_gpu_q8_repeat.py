@@ -31,7 +31,7 @@ def cut_units(stages, fraction, d, b, hkv, gen):
     return cache, bt, tokens - torch.arange(seqs, device=DEV, dtype=torch.int32) % 5
 
 
-def calls(dtype, q, cache, bt, cl, scale, hq, hkv, d, b, rounds):
+def calls(q, cache, bt, cl, scale, hq, hkv, d, b, rounds):
     """Ten outputs at a time, from memory and from the L2 cache in turn."""
     ws = torch.zeros(P.pa_q8_decode_workspace_size(len(cl), hq, hkv, d, b, bt.shape[1]), dtype=torch.uint8, device=DEV)
     flush = torch.zeros(64 << 20, dtype=torch.float32, device=DEV)
@@ -55,7 +55,30 @@ def test_rows_whose_scores_all_overflow_are_zero(dtype, value, d, b, hq, hkv, st
     scales[:, :, 0] = 1.0
     q = torch.randn(len(cl), hq, d, device=DEV, generator=gen).to(TD[dtype])
     q[:, ::2] = value
-    for outs in calls(dtype, q, cache, bt, cl, -1.0, hq, hkv, d, b, 6):
+    for outs in calls(q, cache, bt, cl, -1.0, hq, hkv, d, b, 6):
         for out in outs:
             assert not out[:, ::2].any() and torch.isfinite(out[:, 1::2].float()).all()
+    assert P.pa_device_errors() == 0
+
+
+@pytest.mark.parametrize("dtype,d,b,hq,hkv,stages,fraction", [
+    ("f32", 128, 16, 64, 8, 600, 0.5),         # two CTAs' shares per unit, both the same length
+    ("f32", 128, 32, 16, 8, 500, 0.7),         # cuts at every place of a unit
+    ("f32", 64, 16, 32, 8, 400, 0.6),
+    ("f32", 128, 16, 8, 8, 26, 0.5),           # short parts that end within a microsecond
+    ("f32", 128, 16, 96, 8, 500, 0.5),         # 12 rows per unit
+    ("bf16", 128, 16, 16, 8, 30, 0.6),
+    ("f16", 64, 32, 26, 2, 20, 0.7),           # 13 rows per unit
+])
+def test_units_cut_once_repeat_bit_for_bit(dtype, d, b, hq, hkv, stages, fraction):
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    cache, bt, cl = cut_units(stages, fraction, d, b, hkv, gen)
+    q = torch.randn(len(cl), hq, d, device=DEV, generator=gen).to(TD[dtype])
+    first = None
+    for outs in calls(q, cache, bt, cl, 0.1, hq, hkv, d, b, 20):
+        if first is None:
+            first = outs[0].clone()
+        for out in outs:
+            assert torch.equal(out, first), f"{(out != first).sum().item()} of {out.numel()} values differ"
+    assert torch.isfinite(first.float()).all()
     assert P.pa_device_errors() == 0
