@@ -854,8 +854,7 @@ __device__ __forceinline__ int merge_room(int rows_cap, int D)
 // consumer warps together, where they are many: every (row, part)'s log2-sum-exp in one round of loads, a row's
 // weights by one warp, then the weighted rows, D / 4 threads per row with two rows and
 // eight parts of each in flight; with fewer rows than such groups of threads, several
-// groups share a row's parts.  (merge_split_unit goes row by row with four parts in
-// flight.)  `room`: the merge rows, free by now.  False on a timeout.
+// groups share a row's parts.  `room`: the merge rows, free by now.  False on a timeout.
 template <typename T, int D>
 __device__ __forceinline__ bool merge8(const DecodeParams &p, const Item &it, const CtaState &c, uint32_t &sph,
                                        int warp, int lane, float *room)
@@ -1070,14 +1069,11 @@ __device__ __forceinline__ bool finish8(const DecodeParams &p, const Item &it, c
         return false;
     if (!*c.merge)
         return true;
-    if (few_rounds<D>(it)) {
-        merge_few<T, D>(p, it, warp * 32 + lane);
-        return true;
-    }
-    // weights and, with few rows, a row per group of threads
-    if (it.rows * it.nparts + 3 + 4 * 128 <= merge_room(rows_cap, D))
+    // merge8 needs room for weights and, with few rows, a row per group of threads; a unit of
+    // more parts (8 rows of 64 dims: over 223) takes merge_few's rounds, 60000 tokens 33.5 us.
+    if (!few_rounds<D>(it) && it.rows * it.nparts + 3 + 4 * 128 <= merge_room(rows_cap, D))
         return merge8<T, D>(p, it, c, sph, warp, lane, c.macc);
-    merge_split_unit<T, D, false>(p, it, warp, lane, nullptr);
+    merge_few<T, D>(p, it, warp * 32 + lane);
     return true;
 }
 

@@ -61,6 +61,25 @@ def test_rows_whose_scores_all_overflow_are_zero(dtype, value, d, b, hq, hkv, st
     assert P.pa_device_errors() == 0
 
 
+@pytest.mark.parametrize("dtype,value", [("f32", 2.0 ** 126), ("bf16", 2.0 ** 126)])
+@pytest.mark.parametrize("hq,tokens", [(16, 60000), (4, 60000), (1, 60000), (16, 6000), (5, 1500)])
+def test_overflowing_rows_of_one_unit_in_many_parts(dtype, value, hq, tokens):
+    """The same for a single unit over all CTAs, more parts than fit the merge's room too."""
+    d, b = 64, 16
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    cache = filled_cache(tokens // b + 1, 1, d, b, gen)
+    codes, scales = P.q8_views(cache, 1, d, b)
+    codes[:, :, 0] = torch.full((), 64.0, device=DEV).to(codes.dtype)
+    scales[:, :, 0] = 1.0
+    bt = torch.randperm(len(cache), device=DEV, generator=gen).int()[None]
+    cl = torch.tensor([tokens], dtype=torch.int32, device=DEV)
+    q = torch.randn(1, hq, d, device=DEV, generator=gen).to(TD[dtype])
+    q[:, ::2] = value
+    out = torch.empty_like(q)
+    P.pa_q8_decode(out, q, cache, bt, cl, -1.0, hq, 1, d, b)
+    assert not out[:, ::2].any() and torch.isfinite(out[:, 1::2].float()).all()
+
+
 @pytest.mark.parametrize("dtype,d,b,hq,hkv,stages,fraction", [
     ("f32", 128, 16, 64, 8, 600, 0.5),         # two CTAs' shares per unit, both the same length
     ("f32", 128, 32, 16, 8, 500, 0.7),         # cuts at every place of a unit
