@@ -497,11 +497,14 @@ pa_status pa_q8_append(const void *k, const void *v, void *kv_cache, const int32
  *
  * As pa_decode with partition_size 0, with K_t and V_t = code * scale of their block and
  * kv head.  q and out are `dtype`; scores, softmax statistics and sums are fp32.  The
- * codes enter the products exactly; queries and probabilities enter them in fp16 (fp32
- * queries and outputs: two fp16 terms, about 22 bits).  Scales may be any finite,
- * non-negative values, powers of two or not.  T = 0 yields a zero row; rows past T are
- * never counted, whatever they hold; a table entry outside [0, num_blocks) reads zeros; a
- * NaN among a sequence's codes makes the outputs that it enters NaN.  num_q_heads /
+ * codes enter the products exactly; queries, and probabilities times V's scale, enter them in
+ * fp16 (fp32 queries and outputs: two fp16 terms, about 22 bits).  Scales may be any finite,
+ * non-negative values, powers of two or not, and as far apart as they like: no block's scale
+ * takes precision from the blocks that carry the weight (V scales more than 2^6 apart cost up
+ * to a sixth of the time).  Sums of probability times |code * scale| have to stay within
+ * fp32's range.  T = 0 yields a zero row, and so does a row whose scores are all -inf; rows
+ * past T are never counted, whatever they hold; a table entry outside [0, num_blocks) reads
+ * zeros; a NaN among a sequence's codes makes the outputs that it enters NaN.  num_q_heads /
  * num_kv_heads may be any size (16 query heads at a time share a read of the cache).
  * Workspace: pa_q8_decode_workspace_size bytes, used as pa_decode's: calls that may
  * overlap need one each, replays of a captured graph start clean.  Waits are bounded and

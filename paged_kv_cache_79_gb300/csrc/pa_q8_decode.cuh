@@ -23,16 +23,27 @@
 //        [2^10, 2^11), then rounded to fp16.  fp16 queries lose nothing (elements more
 //        than 2^24 below the largest aside), bf16 ones neither (8 significant bits);
 //        fp32 ones are split into two fp16 terms, 22 significant bits.
-//   p    exp2(s - ref), at most 2 (ref follows the maximum), enters as 2^14 p: the fp16
-//        rounding is at most 2^-11 of the value down to p = 2^-28.  fp32 outputs take p
-//        as two fp16 terms.  The sum of p is kept in fp32 from the unrounded values.
+//   p vs the probability times V's scale, over a reference (Scales, below) that makes it at
+//        most 2, enters as 2^14 times that: the fp16 rounding is at most 2^-11 of the value,
+//        or 2^-39 of the reference.  fp32 outputs take it as two fp16 terms, 2^-22 of the
+//        value or as little.  The sum of p is kept in fp32 from unrounded values.
 // Scores, sums, running maxima and outputs are fp32; fp32 outputs also add each
 // stage's products to the running output with an fp32 add, since the tensor pipe's own
 // accumulation truncates.
 //
-// Scales.  ks multiplies the fp32 scores.  vs multiplies p before its rounding, divided
-// by the largest vs the warp has met in the item (vref), so that 2^14 p vs / vref stays in
-// fp16's range whatever the scales; a larger vs rescales the accumulator once.
+// Scales.  ks multiplies the fp32 scores.  vs = 2^e f, 1/2 < f <= 1, multiplies p before its
+// rounding, over 2^k mu.  mu is the mantissa (1 <= mu < 2) of the first vs that is not 0, so that
+// scales that are alike but for powers of two round nothing.  k is the largest e the warp
+// has met in the item, as long as the e lie within kSpread of each other: then each row's
+// largest product is within that of the reference.  Scales that are further apart take a
+// slower path from there on, as a block whose vs is large while its p is nothing must
+// not push the blocks that count out of fp16's range: each row has a second reference
+// beside the scores' maximum m, w = the largest s + e, and a k of its own, ceil(w - m); the
+// products are 2^(s - m + e - k) f / mu, the power taken as a whole (p alone may be below
+// fp32's range although the product counts), and the accumulator follows new references by
+// 2^(m - m' + k - k').  (16 sequences of 2000 tokens, 104 / 8 heads, fp16: 32.3 us, with scales
+// 10 binades apart 35.3; 64 sequences, 64 / 8 heads, bf16: 140.0 and 145.1.  Rows' own k
+// throughout took 35.5 of the former.)
 //
 // Layout of the products (16 tokens at a time).  S^T[token x row] = K Q^T: row r of the
 // A tile is token 4 (r / 2) + r % 2 for r < 8 and that plus 2 for r >= 8, and the k order
@@ -108,8 +119,8 @@ constexpr int kThreads8 = kThreads + 32;  // one warp more than pa_decode: the s
 
 constexpr int kMergeRows = 4;  // merge rows at least: merge8 works in them
 
-// Shared memory: as make_layout, with 8 bytes of scales per block of a stage in the
-// place of the fused append's rows.
+// Shared memory: as make_layout, with the scales of a stage's blocks and the range of their
+// exponents (8 bytes each) in the place of the fused append's rows.
 __host__ __device__ inline SmemLayout make_layout8(int stages, int stage_bytes, int bps, int slots, int rows,
                                                    int D, int elem_bytes)
 {
@@ -126,7 +137,7 @@ __host__ __device__ inline SmemLayout make_layout8(int stages, int stage_bytes, 
     L.q = o;
     o += (uint32_t)(slots * (rows <= kNarrowRows ? kNarrowRows : kHeadsPerItem) * D * elem_bytes);
     L.newrow = o;  // the scales
-    o += (uint32_t)(stages * bps * 8);
+    o += (uint32_t)(stages * (bps + 1) * 8);
     L.newinfo = o;
     o = (o + 15u) & ~15u;
     L.bars = o;  // as make_layout's, then one per stage for its scales
@@ -269,6 +280,18 @@ struct Producer8 {
     }
 };
 
+// 2^n, for n of -149 .. 127.
+__device__ __forceinline__ float pow2(int n)
+{
+    return __uint_as_float(n >= -126 ? (uint32_t)(n + 127) << 23 : 1u << (n + 149));
+}
+
+// e of a scale 2^e f with 1/2 < f <= 1, as a float: -inf for 0, at least -126 otherwise.
+__device__ __forceinline__ float scale_exponent(float x)
+{
+    return x == 0.f ? -INFINITY : (float)((int)((__float_as_uint(x) + 0x7fffffu) >> 23) - 127);
+}
+
 // ---------------------------------------------------------------------------
 // Scale warp: walks the same items as the producer and brings each stage's scales into
 // shared memory by plain loads.  (A 16-byte bulk copy of them behind every block's tiles
@@ -306,6 +329,19 @@ struct ScaleWarp {
         return __ldcg(reinterpret_cast<const float2 *>(q8.scales + (size_t)id * q8.block_bytes) + it.kvh);
     }
 
+    // Largest and smallest e of the V scales (scale_exponent) of the lane's stage, whose
+    // blocks are kBPS consecutive lanes'.
+    static __device__ float2 range_of(float vs)
+    {
+        float2 e = make_float2(scale_exponent(vs), vs == 0.f ? INFINITY : scale_exponent(vs));
+#pragma unroll
+        for (int o = 1; o < C::kBPS; o <<= 1) {
+            e.x = fmaxf(e.x, __shfl_xor_sync(0xffffffffu, e.x, o));
+            e.y = fminf(e.y, __shfl_xor_sync(0xffffffffu, e.y, o));
+        }
+        return e;
+    }
+
     __device__ bool emit(const Item &it)
     {
         const int32_t *row = p.block_tables + (size_t)it.tseq * p.max_blocks;
@@ -325,6 +361,7 @@ struct ScaleWarp {
             const float2 next_s = scales_of(it, next_id);
             next_id = block_id(it, row, jb + 64 + lane);
             const int cnt = min(32, it.j1 - jb);
+            const float2 range = range_of(s.y);
             for (int i = 0; i < cnt; i += C::kBPS, ++g) {
                 const uint32_t st = g % C::kStages;
                 int ok = 1;
@@ -337,8 +374,12 @@ struct ScaleWarp {
                         raise_error(p, c.abort, PA_DEVERR_TIMEOUT_EMPTY);
                     return false;
                 }
+                // (blocks past the item: zeros)
+                float2 *const dst = reinterpret_cast<float2 *>(c.newrow) + st * (C::kBPS + 1);
                 if (lane >= i && lane < i + C::kBPS)
-                    reinterpret_cast<float2 *>(c.newrow)[st * C::kBPS + lane - i] = s;
+                    dst[lane - i] = s;
+                if (lane == i)
+                    dst[C::kBPS] = range;
                 __syncwarp();
                 if (lane == 0)
                     dev::mbar_arrive(dev::smem_addr(&sfull[st]));
@@ -367,6 +408,10 @@ __device__ __forceinline__ void load_row(float (&x)[N], const T *src)
             x[i * E + k] = to_float(e[k]);
     }
 }
+
+// k of a row whose references are m and w: at least -126, where p vs is below fp32's
+// normal range altogether (also without any w); at most 128, as w <= m + 128.
+__device__ __forceinline__ float shift_of(float w, float m) { return fmaxf(ceilf(w - m), -126.f); }
 
 // Four consecutive outputs in the storage type.
 template <typename T>
@@ -421,7 +466,8 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
     constexpr int DM = D / 16;    // 16-dim tiles of O^T
     constexpr int SA = D + kAccPad;
     constexpr uint32_t kQSlotBytes = NT * 8 * D * sizeof(T);
-    constexpr float kUp = 16384.f;  // 2^14: p's factor in the products
+    constexpr int kUp = 14;         // products are held times 2^kUp
+    constexpr float kSpread = 6.f;  // binades over which all e lie, or rows take a k each
     const int q4 = lane & 3;       // fragment columns: query rows 8 nt + 2 q4, + 1
     const int r8 = lane >> 2;      // fragment row
     const int tok0 = 4 * (r8 >> 1) + (r8 & 1);  // this lane's tokens of a tile: tok0, tok0 + 2
@@ -487,8 +533,13 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
         for (int i = 0; i < DM; ++i)
             o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
     }
-    float vref = FLT_MIN;  // largest vs so far (its inverse is finite, also for scales of 0)
-    float vinv = 1.f / FLT_MIN;
+    float mu = 0.f;                              // mantissa of the first vs that is not 0
+    float e_top = -INFINITY, e_low = INFINITY;   // largest and smallest e so far
+    float vinv = 0.f;                            // 2^-k / mu, or 1 / mu where rows have a k each
+    bool spread = false;                         // they have
+    // w and k of the rows then: at the start of the warp's own merge rows (16 floats a group
+    // of 8 rows; a merge row has 72 at least)
+    float2 *const wk = reinterpret_cast<float2 *>(c.macc + warp * rows_cap * SA) + 2 * q4;
     const int rot = it.rot();
     const int stages = (it.j1 - it.j0 + C::kBPS - 1) / C::kBPS;
     int i = (warp - rot) & (kConsumerWarps - 1);
@@ -514,15 +565,17 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
         const int valid = min(nbs * BS, it.len - j * BS);
         const bool partial = valid < TS;
         const uint32_t stage = ring + st * C::kStageBytes;
-        float kscale[C::kBPS], vscale[C::kBPS];
-        float vmax = vref;
+        float kscale[C::kBPS], vscale[C::kBPS];  // (blocks past the item: 0)
+        const uint32_t sc = scales + st * (C::kBPS + 1) * 8;
 #pragma unroll
         for (int b = 0; b < C::kBPS; ++b) {
-            const float2 s2 = dev::lds_f2(scales + (st * C::kBPS + b) * 8);
+            const float2 s2 = dev::lds_f2(sc + b * 8);
             kscale[b] = s2.x;
-            vscale[b] = b < nbs ? s2.y : 0.f;
-            vmax = fmaxf(vmax, vscale[b]);
+            vscale[b] = s2.y;
         }
+        const float2 range = dev::lds_f2(sc + C::kBPS * 8);
+        const float top = fmaxf(e_top, range.x);
+        e_low = fminf(e_low, range.y);
 
         // S^T = K Q^T, even and odd k-steps in accumulators of their own (shorter chains)
         float s[MT][NT][4];
@@ -562,7 +615,7 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
         // Scale and mask.  A lane compares its own scores with the reference: only where
         // one passes it by more than 1 do the lanes look for the maximum, and the warp
         // takes a new reference.
-        bool raise = vmax > vref;
+        bool raise = top > e_top;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -580,10 +633,104 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
                 }
             }
         }
-        if (__any_sync(0xffffffffu, raise)) {
-            const float cv = vref / vmax;
-            vref = vmax;
-            vinv = 1.f / vref;
+        // (rows of maxima: a lane's own tokens, then the lanes of the same rows)
+        auto row_max = [](float x) {
+#pragma unroll
+            for (int o_ = 4; o_ < 32; o_ <<= 1)
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o_));
+            return x;
+        };
+        auto rescale = [&](int nt, float ca, float cb) {
+#pragma unroll
+            for (int i = 0; i < DM; ++i) {
+                o[nt][i][0] *= ca;
+                o[nt][i][1] *= cb;
+                o[nt][i][2] *= ca;
+                o[nt][i][3] *= cb;
+            }
+        };
+        float counted = 1.f;
+        auto find_mu = [&] {
+#pragma unroll
+            for (int b = 0; b < C::kBPS; ++b)
+                if (mu == 0.f && vscale[b] > 0.f)
+                    mu = vscale[b] < FLT_MIN
+                             ? 1.f
+                             : __uint_as_float((__float_as_uint(vscale[b]) & 0x7fffffu) | 0x3f800000u);
+        };
+        if (__builtin_expect(top - e_low > kSpread, 0)) {
+            if (!spread) {  // from here on: what the rows hold so far is within 2^m 2^e_top
+                spread = true;
+                find_mu();
+                vinv = 1.f / mu;
+                if (r8 == 0) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        wk[nt * 8] = make_float2(ma[nt] + e_top, fmaxf(e_top, -126.f));
+                        wk[nt * 8 + 1] = make_float2(mb[nt] + e_top, fmaxf(e_top, -126.f));
+                    }
+                }
+                __syncwarp();
+            }
+            float vexp[C::kBPS];
+#pragma unroll
+            for (int b = 0; b < C::kBPS; ++b)
+                vexp[b] = scale_exponent(vscale[b]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float2 old_a = wk[nt * 8], old_b = wk[nt * 8 + 1];
+                float na = ma[nt], nb = mb[nt], va = old_a.x, vb = old_b.x;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    const float xa = fmaxf(s[mt][nt][0], s[mt][nt][2]), xb = fmaxf(s[mt][nt][1], s[mt][nt][3]);
+                    na = fmaxf(na, xa);
+                    nb = fmaxf(nb, xb);
+                    va = fmaxf(va, xa + vexp[mt * 16 / BS]);
+                    vb = fmaxf(vb, xb + vexp[mt * 16 / BS]);
+                }
+                na = row_max(na);
+                nb = row_max(nb);
+                va = row_max(va);
+                vb = row_max(vb);
+                const float ka = shift_of(va, na), kb = shift_of(vb, nb);
+                // (one power for both: it is at most about 2, its factors may not be finite)
+                const bool fresh_a = ma[nt] == -INFINITY, fresh_b = mb[nt] == -INFINITY;
+                const float da = ma[nt] - na, db = mb[nt] - nb;
+                rescale(nt, fresh_a ? 0.f : exp2f(da + (old_a.y - ka)), fresh_b ? 0.f : exp2f(db + (old_b.y - kb)));
+                la[nt] *= fresh_a ? 0.f : exp2f(da);
+                lb[nt] *= fresh_b ? 0.f : exp2f(db);
+                ma[nt] = na;
+                mb[nt] = nb;
+                __syncwarp();
+                if (r8 == 0) {
+                    wk[nt * 8] = make_float2(va, ka);
+                    wk[nt * 8 + 1] = make_float2(vb, kb);
+                }
+                // p is counted here, and the scores move by e - k for the products
+                na = na == -INFINITY ? 0.f : na;
+                nb = nb == -INFINITY ? 0.f : nb;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float &xa = s[mt][nt][2 * h], &xb = s[mt][nt][2 * h + 1];
+                        la[nt] += dev::ex2(xa - na);
+                        lb[nt] += dev::ex2(xb - nb);
+                        xa += vexp[mt * 16 / BS] - ka;
+                        xb += vexp[mt * 16 / BS] - kb;
+                    }
+            }
+            e_top = top;  // (the difference never shrinks)
+            counted = 0.f;
+#pragma unroll
+            for (int b = 0; b < C::kBPS; ++b)  // f
+                vscale[b] = vscale[b] == 0.f ? 0.f : vscale[b] * pow2(-(int)vexp[b]);
+        } else if (__any_sync(0xffffffffu, raise)) {
+            // (e_top grows by kSpread at most, or from -inf, when there is nothing yet)
+            const float cv = e_top == top || e_top == -INFINITY ? 1.f : pow2((int)(e_top - top));
+            find_mu();
+            vinv = mu == 0.f ? 0.f : pow2(-(int)top) / mu;
+            e_top = top;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float na = ma[nt], nb = mb[nt];
@@ -592,11 +739,8 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
                     na = fmaxf(na, fmaxf(s[mt][nt][0], s[mt][nt][2]));
                     nb = fmaxf(nb, fmaxf(s[mt][nt][1], s[mt][nt][3]));
                 }
-#pragma unroll
-                for (int o_ = 4; o_ < 32; o_ <<= 1) {
-                    na = fmaxf(na, __shfl_xor_sync(0xffffffffu, na, o_));
-                    nb = fmaxf(nb, __shfl_xor_sync(0xffffffffu, nb, o_));
-                }
+                na = row_max(na);
+                nb = row_max(nb);
                 // (no finite score yet: nothing to rescale)
                 const float ca = ma[nt] == -INFINITY ? 0.f : exp2f(ma[nt] - na);
                 const float cb = mb[nt] == -INFINITY ? 0.f : exp2f(mb[nt] - nb);
@@ -604,29 +748,23 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
                 mb[nt] = nb;
                 la[nt] *= ca;
                 lb[nt] *= cb;
-#pragma unroll
-                for (int i = 0; i < DM; ++i) {
-                    o[nt][i][0] *= ca * cv;
-                    o[nt][i][1] *= cb * cv;
-                    o[nt][i][2] *= ca * cv;
-                    o[nt][i][3] *= cb * cv;
-                }
+                rescale(nt, ca * cv, cb * cv);
             }
         }
 
-        // P^T as the B operand: exp2, times 2^14 vs / vref, rounded, transposed
+        // P^T as the B operand: 2^kUp p vs 2^-k / mu, rounded, transposed
         uint32_t pb[MT][NT][QT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const float na = ma[nt] == -INFINITY ? 0.f : ma[nt], nb = mb[nt] == -INFINITY ? 0.f : mb[nt];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-                const float vs = vscale[mt * 16 / BS] * vinv * kUp;
+                const float vs = vscale[mt * 16 / BS] * vinv * (float)(1 << kUp);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const float ea = dev::ex2(s[mt][nt][2 * h] - na), eb = dev::ex2(s[mt][nt][2 * h + 1] - nb);
-                    la[nt] += ea;
-                    lb[nt] += eb;
+                    la[nt] = fmaf(ea, counted, la[nt]);
+                    lb[nt] = fmaf(eb, counted, lb[nt]);
                     const float ya = ea * vs, yb = eb * vs;
                     const uint32_t hi = dev::Mma<__half>::pack(ya, yb);
                     pb[mt][nt][0][h] = dev::movmatrix_trans(hi);
@@ -696,8 +834,21 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
 
     g += stages;
 
-    // partial rows of this warp
+    // Partial rows of this warp: back from 2^kUp p vs 2^-k / mu in two steps (2^(k - kUp) alone
+    // is exact also where it is below the normal range).
     float *mine = c.macc + warp * rows_cap * SA;
+    float ua[NT], ub[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+        ua[nt] = ub[nt] = pow2((int)fmaxf(e_top, -126.f) - kUp);
+    if (spread) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            ua[nt] = pow2((int)wk[nt * 8].y - kUp);
+            ub[nt] = pow2((int)wk[nt * 8 + 1].y - kUp);
+        }
+        __syncwarp();  // the rows take their place
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         float sa = la[nt], sb = lb[nt];
@@ -710,15 +861,15 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
         if (ra < it.rows) {
 #pragma unroll
             for (int dm = 0; dm < DM; ++dm) {
-                mine[ra * SA + dm * 16 + r8] = o[nt][dm][0] * (1.f / kUp) * vref;
-                mine[ra * SA + dm * 16 + r8 + 8] = o[nt][dm][2] * (1.f / kUp) * vref;
+                mine[ra * SA + dm * 16 + r8] = o[nt][dm][0] * mu * ua[nt];
+                mine[ra * SA + dm * 16 + r8 + 8] = o[nt][dm][2] * mu * ua[nt];
             }
         }
         if (rb < it.rows) {
 #pragma unroll
             for (int dm = 0; dm < DM; ++dm) {
-                mine[rb * SA + dm * 16 + r8] = o[nt][dm][1] * (1.f / kUp) * vref;
-                mine[rb * SA + dm * 16 + r8 + 8] = o[nt][dm][3] * (1.f / kUp) * vref;
+                mine[rb * SA + dm * 16 + r8] = o[nt][dm][1] * mu * ub[nt];
+                mine[rb * SA + dm * 16 + r8 + 8] = o[nt][dm][3] * mu * ub[nt];
             }
         }
         if (NT == 1 && alone) {
@@ -757,6 +908,10 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
     return true;
 }
 
+// The square root of a merge's weight 2^x.  Rows are multiplied by it twice: with V scales
+// far apart a weight may be below fp32's range although its row counts.
+__device__ __forceinline__ float root_weight(float x) { return exp2f(0.5f * x); }
+
 // One part of a split unit joins its row's merge: M the largest log2-sum-exp of the parts
 // at hand (a part without any weight, -inf, adds nothing).  A unit cut once is merged by
 // finalize8 or by merge_few, as its parts happen to end; both add them in slot order with
@@ -764,12 +919,12 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
 __device__ __forceinline__ void add_part(float (&o)[4], float &W, float M, float lse, const float4 &v)
 {
     if (lse != -INFINITY) {
-        const float w = exp2f(lse - M);
-        W = __fadd_rn(W, w);
-        o[0] = __fmaf_rn(w, v.x, o[0]);
-        o[1] = __fmaf_rn(w, v.y, o[1]);
-        o[2] = __fmaf_rn(w, v.z, o[2]);
-        o[3] = __fmaf_rn(w, v.w, o[3]);
+        const float h = root_weight(lse - M);
+        W = __fmaf_rn(h, h, W);
+        o[0] = __fmaf_rn(h, __fmul_rn(h, v.x), o[0]);
+        o[1] = __fmaf_rn(h, __fmul_rn(h, v.y), o[1]);
+        o[2] = __fmaf_rn(h, __fmul_rn(h, v.z), o[2]);
+        o[3] = __fmaf_rn(h, __fmul_rn(h, v.w), o[3]);
     }
 }
 
@@ -808,12 +963,12 @@ __device__ __forceinline__ void finalize8(const DecodeParams &p, const Item &it,
 #pragma unroll
         for (int c = 0; c < kConsumerWarps; ++c) {
             if (mc[c] != -INFINITY) {  // (a warp without stages left no rows)
-                const float w = exp2f(mc[c] - M);
-                L += w * lc[c];
-                o[0] += w * v[c].x;
-                o[1] += w * v[c].y;
-                o[2] += w * v[c].z;
-                o[3] += w * v[c].w;
+                const float h = root_weight(mc[c] - M);
+                L += h * h * lc[c];
+                o[0] += h * (h * v[c].x);
+                o[1] += h * (h * v[c].y);
+                o[2] += h * (h * v[c].z);
+                o[3] += h * (h * v[c].w);
             }
         }
 #pragma unroll
@@ -884,13 +1039,14 @@ __device__ __forceinline__ bool merge8(const DecodeParams &p, const Item &it, co
             M = fmaxf(M, room[r * n + i]);
         M = dev::warp_max(M);
         for (int i = lane; i < n; i += 32) {
-            const float w = M == -INFINITY ? 0.f : exp2f(room[r * n + i] - M);
-            room[r * n + i] = w;
-            W += w;
+            const float h = M == -INFINITY ? 0.f : root_weight(room[r * n + i] - M);
+            room[r * n + i] = h;
+            W += h * h;
         }
         W = dev::warp_sum(W);
+        const float root = sqrtf(W);  // (at least 1, or 0 without any weight)
         for (int i = lane; i < n; i += 32)
-            room[r * n + i] = W > 0.f ? room[r * n + i] / W : 0.f;
+            room[r * n + i] = W > 0.f ? room[r * n + i] / root : 0.f;
     }
     if (!consumer_sync(p, c, sph))
         return false;
@@ -915,14 +1071,14 @@ __device__ __forceinline__ bool merge8(const DecodeParams &p, const Item &it, co
                 const int k = k0 + u * ways;
                 const float w0 = k < n ? room[r * n + k] : 0.f, w1 = k < n ? room[r2 * n + k] : 0.f;
                 if (k < n) {
-                    o[0][0] = fmaf(w0, v[0][u].x, o[0][0]);
-                    o[0][1] = fmaf(w0, v[0][u].y, o[0][1]);
-                    o[0][2] = fmaf(w0, v[0][u].z, o[0][2]);
-                    o[0][3] = fmaf(w0, v[0][u].w, o[0][3]);
-                    o[1][0] = fmaf(w1, v[1][u].x, o[1][0]);
-                    o[1][1] = fmaf(w1, v[1][u].y, o[1][1]);
-                    o[1][2] = fmaf(w1, v[1][u].z, o[1][2]);
-                    o[1][3] = fmaf(w1, v[1][u].w, o[1][3]);
+                    o[0][0] = fmaf(w0, w0 * v[0][u].x, o[0][0]);
+                    o[0][1] = fmaf(w0, w0 * v[0][u].y, o[0][1]);
+                    o[0][2] = fmaf(w0, w0 * v[0][u].z, o[0][2]);
+                    o[0][3] = fmaf(w0, w0 * v[0][u].w, o[0][3]);
+                    o[1][0] = fmaf(w1, w1 * v[1][u].x, o[1][0]);
+                    o[1][1] = fmaf(w1, w1 * v[1][u].y, o[1][1]);
+                    o[1][2] = fmaf(w1, w1 * v[1][u].z, o[1][2]);
+                    o[1][3] = fmaf(w1, w1 * v[1][u].w, o[1][3]);
                 }
             }
         }
@@ -979,12 +1135,12 @@ __device__ __forceinline__ void merge_few(const DecodeParams &p, const Item &it,
 #pragma unroll
             for (int i = 0; i < kFlight; ++i)
                 m = fmaxf(m, lse[i]);
-            const float c = M == -INFINITY ? 0.f : exp2f(M - m);
+            const float h = M == -INFINITY ? 0.f : root_weight(M - m);
             M = m;
-            W *= c;
+            W *= h * h;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                o[e] *= c;
+                o[e] = h * (h * o[e]);
 #pragma unroll
             for (int i = 0; i < kFlight; ++i)
                 if (k0 + i < n)
