@@ -84,6 +84,12 @@ __device__ __forceinline__ int owner(const long long *incl, long long x)
     return lo;
 }
 
+// Blocks of B tokens that hold `tokens`, both below 2^31 (their sum may pass that).
+__device__ __forceinline__ int blocks_of(long long tokens, int B)
+{
+    return (int)(((unsigned int)tokens + (unsigned int)(B - 1)) / (unsigned int)B);
+}
+
 __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const __grid_constant__ TablesParams p)
 {
     namespace cg = cooperative_groups;
@@ -110,7 +116,7 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const __grid_
         want = s < p.num_seqs ? p.new_tokens[s] : 0;
         if (!__syncthreads_or(want < 0))
             continue;
-        long long gone = want < 0 ? (min((long long)len, cap) + B - 1) / B : 0, none = 0, total, zero;
+        long long gone = want < 0 ? blocks_of(min((long long)len, cap), B) : 0, none = 0, total, zero;
         scan2(gone, none, total, zero, part);
         blk_incl[tid] = gone;
         __syncthreads();
@@ -134,10 +140,10 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const __grid_
             want = s < p.num_seqs ? p.new_tokens[s] : 0;
             cluster.sync();  // read by every CTA before the writer goes on
         }
-        const int nb = (int)((min((long long)len, cap) + B - 1) / B);
+        const int nb = blocks_of(min((long long)len, cap), B);
         const bool fits = want <= 0 || (long long)len + want <= cap;
         const int n = fits && want > 0 ? want : 0;
-        const int need = n > 0 ? (int)(((long long)len + n + B - 1) / B) - nb : 0;
+        const int need = n > 0 ? blocks_of((long long)len + n, B) - nb : 0;
         long long ni = need, wi = n, nt, wt;
         scan2(ni, wi, nt, wt, part);
         const bool ok = want <= 0 || (fits && (need == 0 || need_before + ni <= have) &&
@@ -169,13 +175,13 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const __grid_
         for (long long i = first; i < bt; i += stride) {
             const int o = owner(blk_incl, i);
             const long long k = i - (o > 0 ? blk_incl[o - 1] : 0);
-            const int nb_o = (s_len[o] + B - 1) / B;
+            const int nb_o = blocks_of(s_len[o], B);
             p.block_tables[(size_t)(s0 + o) * W + nb_o + k] = popped(o, k);
         }
         for (long long i = first; i < tt && !p.slots_apart; i += stride) {
             const int o = owner(tok_incl, i);
             const int pos = s_len[o] + (int)(i - (o > 0 ? tok_incl[o - 1] : 0));
-            const int j = pos / B, nb_o = (s_len[o] + B - 1) / B;
+            const int j = pos / B, nb_o = blocks_of(s_len[o], B);
             const int id = j < nb_o ? p.block_tables[(size_t)(s0 + o) * W + j] : popped(o, j - nb_o);
             p.slots[tok_before + i] = id >= 0 ? (int64_t)id * B + pos % B : -1;
         }
