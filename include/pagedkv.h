@@ -485,7 +485,8 @@ size_t pa_q8_scales_offset(int num_kv_heads, int head_dim, int block_size);
  *                 non-decreasing from 0, or NULL
  * Errors: PA_ERR_INVALID (null or misaligned pointer, bad size, query_start NULL with
  *   num_tokens != num_seqs), PA_ERR_UNSUPPORTED (head_dim, block_size or dtype not
- *   built), PA_ERR_CUDA.  num_tokens = 0 or num_seqs = 0 is a no-op.
+ *   built, num_tokens or num_seqs above 2^31 - 1024), PA_ERR_CUDA.  num_tokens = 0 or
+ *   num_seqs = 0 is a no-op.
  */
 pa_status pa_q8_append(const void *k, const void *v, void *kv_cache, const int32_t *block_tables,
                        int max_blocks_per_seq, const int32_t *context_lens, const int32_t *query_start,
@@ -566,7 +567,8 @@ pa_status pa_q8_swap_blocks(const void *src_cache, void *dst_cache, const int32_
  *   free_list         device int32 [num_blocks]
  * Errors: PA_ERR_INVALID (null or misaligned pointer, negative num_seqs or num_slots,
  *   non-positive num_blocks, block_size or max_blocks_per_seq, num_blocks or
- *   max_blocks_per_seq * block_size >= 2^31), PA_ERR_CUDA.  num_seqs = 0 still pads the slot map.
+ *   max_blocks_per_seq * block_size >= 2^31), PA_ERR_UNSUPPORTED (num_seqs or num_slots
+ *   above 2^31 - 1024), PA_ERR_CUDA.  num_seqs = 0 still pads the slot map.
  */
 pa_status pa_build_tables(int32_t *block_tables, int max_blocks_per_seq, int32_t *context_lens_out,
                           const int32_t *context_lens, const int32_t *new_tokens, int num_seqs,

@@ -763,6 +763,11 @@ def q8_views(kv_cache, num_kv_heads: int, head_dim: int, block_size: int):
     return codes, scales
 
 
+def _check_counts(*counts) -> None:
+    # (ctypes would pass on the low 32 bits of a larger one)
+    _want(max(counts) < 2 ** 31, "tensors of 2^31 rows or columns and more are not taken")
+
+
 def _check_batch(kv_cache, block_tables, context_lens, num_kv_heads, head_dim, block_size):
     T = _torch()
     if block_tables.dtype != T.int32 or context_lens.dtype != T.int32:
@@ -773,6 +778,7 @@ def _check_batch(kv_cache, block_tables, context_lens, num_kv_heads, head_dim, b
         raise ValueError("block_tables must be [S, W] and context_lens [S]")
     if kv_cache.dim() != 2 or kv_cache.shape[1] != pa_q8_block_bytes(num_kv_heads, head_dim, block_size):
         raise ValueError("kv_cache must be [num_blocks, pa_q8_block_bytes(...)]")
+    _check_counts(*block_tables.shape, kv_cache.shape[0])
 
 
 _APPEND_NAMES = ("k", "v", "kv_cache", "block_tables", "context_lens", "query_start")
@@ -790,6 +796,7 @@ def pa_q8_append(k, v, kv_cache, block_tables, context_lens, block_size: int, qu
     if k.dtype != v.dtype:
         raise TypeError("k and v must have one dtype")
     n, hkv, d = k.shape
+    _check_counts(n)
     S, W = block_tables.shape
     _check_batch(kv_cache, block_tables, context_lens, hkv, d, block_size)
     tensors = (k, v, kv_cache, block_tables, context_lens)
@@ -904,6 +911,7 @@ def pa_build_tables(block_tables, context_lens, new_tokens, free_list, num_free,
     _want(query_start.shape == (S + 1,), "query_start must be [S + 1]")
     _want(num_free.numel() == 1 and num_free_out.numel() == 1, "num_free and num_free_out hold one number")
     _want(free_list.dim() == 1 and slot_mapping.dim() == 1, "free_list and slot_mapping must have one dimension")
+    _check_counts(S, W, free_list.shape[0], slot_mapping.shape[0])
     dev, device = _on_device(_TABLE_NAMES, tensors)
     _call("pa_build_tables", device, block_tables.data_ptr(), W, context_lens_out.data_ptr(),
           context_lens.data_ptr(), new_tokens.data_ptr(), S, free_list.data_ptr(), free_list.shape[0],

@@ -19,6 +19,10 @@ pa_status cuda_fail(cudaError_t e)
 
 bool dtype_ok(int d) { return d == PA_F32 || d == PA_F16 || d == PA_BF16; }
 
+// Sequences, tokens and slots at most: a kernel goes through them up to 1024 at a time, in
+// 32-bit numbers that must not pass 2^31 on the last round.
+constexpr int kMaxCount = 0x7fffffff - 1023;
+
 // Sizes every entry point of the cache shares.
 pa_status check_sizes(int num_blocks, int max_blocks, int num_kv_heads, int head_dim, int block_size,
                       int dtype)
@@ -89,6 +93,8 @@ pa_status pa_q8_append(const void *k, const void *v, void *kv_cache, const int32
         check_sizes(num_blocks, max_blocks_per_seq, num_kv_heads, head_dim, block_size, dtype);
     if (st != PA_OK)
         return st;
+    if (num_seqs > kMaxCount || num_tokens > kMaxCount)
+        return PA_ERR_UNSUPPORTED;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
@@ -256,6 +262,8 @@ pa_status pa_build_tables(int32_t *block_tables, int max_blocks_per_seq, int32_t
     if ((long long)num_blocks * block_size >= (1ll << 31) ||
         (long long)max_blocks_per_seq * block_size >= (1ll << 31))
         return PA_ERR_INVALID;
+    if (num_seqs > kMaxCount || num_slots > kMaxCount)
+        return PA_ERR_UNSUPPORTED;
     TablesParams p;
     p.block_tables = block_tables;
     p.context_lens_out = context_lens_out;

@@ -1,7 +1,9 @@
 """pa_build_tables at the ends of its ranges, against the one-request-at-a-time model."""
 import numpy as np
 import pytest
+import torch
 
+import paged_kv_cache_79_gb300 as P
 from tests.test_gpu_tables import check
 
 pytestmark = pytest.mark.gpu
@@ -26,3 +28,19 @@ def test_blocks_of_nearly_all_the_range(b, width, cl, new):
         want = check(bt, np.array(cl, dtype=np.int32), np.array(new), free, left, b, 40)
         if left:
             assert (want[4] == new).sum() >= 1
+
+
+def test_the_longest_slot_map():
+    """2^31 - 1024 slots, 17 GB: two requests' own, then padding to the very end."""
+    n, b = 2 ** 31 - 1024, 16
+    i32 = dict(dtype=torch.int32, device="cuda")
+    slots = torch.empty(n, dtype=torch.int64, device="cuda")
+    slots[:100], slots[-5000:] = 7, 7
+    bt, cl = torch.full((2, 4), -1, **i32), torch.zeros(2, **i32)
+    qs, granted, nfree = torch.zeros(3, **i32), torch.zeros(2, **i32), torch.tensor([6], **i32)
+    P.pa_build_tables(bt, cl, torch.tensor([20, 33], **i32), torch.arange(6, **i32), nfree, b, slots, qs, granted)
+    assert granted.tolist() == [20, 33] and qs.tolist() == [0, 20, 53] and nfree.item() == 1
+    own = [5 * b + i for i in range(16)] + [4 * b + i for i in range(4)] + \
+        [3 * b + i for i in range(16)] + [2 * b + i for i in range(16)] + [b]
+    assert slots[:53].tolist() == own and (slots[53:100] == -1).all() and (slots[-5000:] == -1).all()
+    assert (slots[n // 2 - 5:n // 2 + 70000] == -1).all()
