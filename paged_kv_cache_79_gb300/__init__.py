@@ -751,6 +751,8 @@ def q8_views(kv_cache, num_kv_heads: int, head_dim: int, block_size: int):
     [num_blocks, Hkv, 2, B, d] and float32 [num_blocks, Hkv, 2], index 0 of the pair K
     and 1 V; a code stands for code * scale."""
     import torch
+    if kv_cache.element_size() != 1:   # (the strides below count bytes)
+        raise TypeError("kv_cache must be uint8")
     nb, size = kv_cache.shape
     _want(size == pa_q8_block_bytes(num_kv_heads, head_dim, block_size) and kv_cache.is_contiguous(),
           "kv_cache must be a contiguous [num_blocks, pa_q8_block_bytes(...)]")

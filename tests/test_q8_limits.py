@@ -1,5 +1,5 @@
-"""Counts at the top of their 32 bits: refused before anything is launched (no GPU needed;
-the pointers are never looked at)."""
+"""Refusals of the 8-bit cache and the tables that need no GPU: counts at the top of their 32
+bits (before anything is launched; the pointers are never looked at), views of wrong types."""
 import pytest
 import torch
 
@@ -38,3 +38,13 @@ def test_the_binding_refuses_counts_past_32_bits():
                         ("slot_mapping", torch.zeros(1, dtype=torch.int64).expand(2 ** 32 + 7))):
         with pytest.raises(ValueError, match="2.31"):
             P.pa_build_tables(**{**args, name: value})
+
+
+def test_views_of_a_cache_that_is_not_bytes_are_refused():
+    size = P.pa_q8_block_bytes(2, 64, 16)
+    for dtype in (torch.float32, torch.bfloat16, torch.int32):
+        with pytest.raises(TypeError, match="uint8"):
+            P.q8_views(torch.zeros(3, size, dtype=dtype), 2, 64, 16)
+    cache = torch.zeros(3, size, dtype=torch.uint8)
+    for same in (cache, cache.view(torch.int8), cache.view(torch.float8_e4m3fn)):
+        assert P.q8_views(same, 2, 64, 16)[0].data_ptr() == cache.data_ptr()
