@@ -540,15 +540,19 @@ pa_status pa_q8_swap_blocks(const void *src_cache, void *dst_cache, const int32_
  *   new_tokens[s] < 0   released: its blocks, in table order, go to the end of the free
  *                       list; its length becomes 0.  All releases come before the
  *                       first grant, in request order.
- *   new_tokens[s] >= 0  granted when its row of the table can hold T + n tokens and,
+ *   new_tokens[s] > 0   (n) granted when its row of the table can hold T + n tokens and,
  *                       where it needs blocks, they and those wanted by the requests
- *                       before it fit the pool, and its rows and those wanted before it
- *                       fit num_slots: it takes the next blocks from the end of the free
- *                       list, its length grows by n.  Otherwise refused: nothing of it
- *                       changes.  (A request whose table row is too short counts
- *                       nothing toward the ones after it; one refused for want of
- *                       blocks or slots does: later requests are not served in its
- *                       place, unless they need no block.)
+ *                       before it fit the pool, and its n slots and those wanted by the
+ *                       requests before it fit num_slots: it takes the next blocks from
+ *                       the end of the free list, its length grows by n.  Otherwise
+ *                       refused: nothing of it changes.  A request whose table row is too
+ *                       short counts nothing toward the ones after it.  One refused for
+ *                       want of blocks or slots counts its blocks and its slots: later
+ *                       requests are not served in its place.  So behind one refused for
+ *                       want of blocks, a request that needs no block is served while
+ *                       the slots of all before it and its own fit; behind one refused
+ *                       for want of slots, none is.
+ *   new_tokens[s] = 0   granted 0, whatever T is: nothing of it changes
  * Outputs:
  *   block_tables      entries of the granted requests' new blocks written; others left
  *   context_lens_out  lengths after the step; may be context_lens

@@ -30,6 +30,31 @@ def test_blocks_of_nearly_all_the_range(b, width, cl, new):
             assert (want[4] == new).sum() >= 1
 
 
+def granted(cl, new, left, num_slots, b=16, width=8):
+    bt = np.full((len(cl), width), -1, dtype=np.int32)
+    at = 20
+    for s, t in enumerate(cl):
+        for j in range(min(-(-t // b), width)):
+            bt[s, j], at = at, at + 1
+    free = np.arange(64, dtype=np.int32)
+    return check(bt, np.array(cl, dtype=np.int32), np.array(new), free, left, b, num_slots)[4].tolist()
+
+
+def test_who_is_served_behind_a_refused_request():
+    # 40 slots: the prompt of 100 tokens has none, and nobody behind it; those before it have
+    assert granted([5, 0, 5, 5], [1, 100, 1, 0], 9, 40) == [1, -1, -1, 0]
+    # 2 blocks: the prompt of 50 needs 4; a step within its own block goes on, a new block not
+    assert granted([5, 0, 5, 16], [1, 50, 1, 1], 2, 400) == [1, -1, 1, -1]
+    # its slots count although it is refused
+    assert granted([5, 0, 5, 5], [1, 50, 1, 1], 2, 52) == [1, -1, 1, -1]
+    # a row that is too short counts nothing
+    assert granted([5, 0, 5, 16], [1, 200, 1, 1], 2, 40) == [1, -1, 1, 1]
+
+
+def test_no_new_tokens_are_granted_whatever_the_length():
+    assert granted([0, 128, 129, 10 ** 9], [0, 0, 0, 0], 0, 0) == [0, 0, 0, 0]
+
+
 def test_the_longest_slot_map():
     """2^31 - 1024 slots, 17 GB: two requests' own, then padding to the very end."""
     n, b = 2 ** 31 - 1024, 16
