@@ -193,15 +193,6 @@ __device__ __forceinline__ void ldsm_b8_x2_trans(uint32_t addr, uint32_t &r0, ui
                  : "r"(addr));
 }
 
-// Two e4m3 codes (the low 16 bits of x) as two fp16 values: exact.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x)
-{
-    uint32_t d;
-    const unsigned short h = (unsigned short)x;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(h));
-    return d;
-}
-
 // 16 and 8 bytes of shared memory.
 __device__ __forceinline__ void lds128(uint32_t *x, uint32_t addr)
 {
@@ -216,7 +207,7 @@ __device__ __forceinline__ float2 lds_f2(uint32_t addr)
     return x;
 }
 
-// Four e4m3 codes as two fp16 pairs (codes 0, 1 and 2, 3).
+// Four e4m3 codes as two fp16 pairs (codes 0, 1 and 2, 3): exact.
 __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t x, uint32_t &lo, uint32_t &hi)
 {
     asm("{\n\t.reg .b16 a, b;\n\t"
