@@ -27,18 +27,7 @@ __device__ unsigned int g_device_errors;  // PA_DEVERR_* flags raised by kernels
 
 thread_local int t_last_cuda_error = 0;
 
-pa_status cuda_fail(cudaError_t e)
-{
-    t_last_cuda_error = (int)e;
-    cudaGetLastError();  // clear the sticky launch error of this thread
-    return PA_ERR_CUDA;
-}
-
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 int elem_size(pa_dtype d) { return d == PA_F32 ? 4 : 2; }
-
-bool dtype_ok(int d) { return d == PA_F32 || d == PA_F16 || d == PA_BF16; }
 
 std::mutex g_mu;
 
@@ -178,7 +167,12 @@ unsigned int next_epoch()
     return e;
 }
 
-void note_cuda_error(cudaError_t e) { cuda_fail(e); }
+pa_status cuda_fail(cudaError_t e)
+{
+    t_last_cuda_error = (int)e;
+    cudaGetLastError();  // clear the sticky launch error of this thread
+    return PA_ERR_CUDA;
+}
 
 unsigned long long wait_limit_ns() { return g_wait_limit_ns.load(); }
 

@@ -258,8 +258,12 @@ EncodeTiledFn encode_fn();
 bool device_accessible(const void *ptr);
 
 // Record `e` as this thread's last CUDA error (read by pa_last_cuda_error) and
-// clear the runtime's sticky launch error.
-void note_cuda_error(cudaError_t e);
+// clear the runtime's sticky launch error; PA_ERR_CUDA.
+pa_status cuda_fail(cudaError_t e);
+
+// Argument checks that the entry points share.
+inline bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+inline bool dtype_ok(int d) { return d == PA_F32 || d == PA_F16 || d == PA_BF16; }
 
 cudaError_t launch_reshape_and_cache(const void *k, const void *v, void *k_cache, void *v_cache,
                                      const int64_t *slots, int num_tokens, size_t row_bytes,

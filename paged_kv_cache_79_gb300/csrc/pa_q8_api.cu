@@ -9,16 +9,6 @@ using namespace pagedkv;
 
 namespace {
 
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-pa_status cuda_fail(cudaError_t e)
-{
-    note_cuda_error(e);
-    return PA_ERR_CUDA;
-}
-
-bool dtype_ok(int d) { return d == PA_F32 || d == PA_F16 || d == PA_BF16; }
-
 // Sequences, tokens and slots at most: a kernel goes through them up to 1024 at a time, in
 // 32-bit numbers that must not pass 2^31 on the last round.
 constexpr int kMaxCount = 0x7fffffff - 1023;
