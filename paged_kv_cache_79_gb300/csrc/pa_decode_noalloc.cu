@@ -64,10 +64,8 @@ extern "C" pa_status pa_decode_noalloc(void *out, const void *q, const void *k_c
     void *scratch = nullptr;
     if (e == cudaSuccess)
         e = scratch_address(dev, &scratch);
-    if (e != cudaSuccess) {
-        pagedkv::note_cuda_error(e);
-        return PA_ERR_CUDA;
-    }
+    if (e != cudaSuccess)
+        return pagedkv::cuda_fail(e);
     return pa_decode(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
                      num_seqs, num_blocks, scale, num_q_heads, num_kv_heads, head_dim, block_size,
                      dtype, partition_size, scratch, (size_t)PA_DECODE_NOALLOC_SCRATCH_BYTES, stream);
