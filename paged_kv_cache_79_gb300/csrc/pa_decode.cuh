@@ -490,7 +490,8 @@ __device__ __forceinline__ bool consumer_sync(const DecodeParams &p, const CtaSt
 template <typename T, int D, int BS, int kBPS, int kChunks, int kTileBytes, int kStages, int kCopy>
 struct Producer {
     static constexpr bool kCountParts = true;  // emit_unit looks for CTAs without positions
-    static constexpr int kLead = kUnitCost;    // a unit's charged positions lie before its stages
+    static constexpr int kUnit = kUnitCost;    // positions charged per unit,
+    static constexpr int kLead = kUnitCost;    // and how many of them lie before its stages
     const DecodeParams &p;
     const CUtensorMap *tk;
     const CUtensorMap *tv;
@@ -823,8 +824,8 @@ __device__ __forceinline__ long long warp_sum_ll(long long v)
 
 // Positions of the whole stream (every lane gets the value).  With kPrefix,
 // *prefix tells whether some sequence's units start after shared leading blocks
-// (the own blocks of a batch with shared prefixes).
-template <bool kShare, bool kPrefix>
+// (the own blocks of a batch with shared prefixes).  kUnit: positions charged per unit.
+template <bool kShare, bool kPrefix, int kUnit>
 __device__ __forceinline__ long long stream_total(const DecodeParams &p, int bs, int bps, int lane,
                                                   long long *units = nullptr,
                                                   bool *prefix = nullptr)
@@ -835,7 +836,7 @@ __device__ __forceinline__ long long stream_total(const DecodeParams &p, int bs,
         const int s = s0 + lane;
         if (s < p.num_seqs) {
             const SeqUnits u = seq_units<kShare>(p, s, bs, bps);
-            t += (long long)u.nunits * (kUnitCost + u.ns);
+            t += (long long)u.nunits * (kUnit + u.ns);
             n += u.nunits;
             if (kPrefix)
                 pre |= u.start > 0;
@@ -852,7 +853,7 @@ __device__ __forceinline__ long long stream_total(const DecodeParams &p, int bs,
 // num_seqs if x >= total.  *base_out gets the sequence's first position.  With
 // one_unit, each sequence counts the positions of one of its units (a row of the
 // (unit, sequence) order).  Warp-cooperative.
-template <bool kShare>
+template <bool kShare, int kUnit>
 __device__ __forceinline__ int find_seq_at(const DecodeParams &p, int bs, int bps, long long x,
                                            long long *base_out, int lane, bool one_unit = false)
 {
@@ -862,7 +863,7 @@ __device__ __forceinline__ int find_seq_at(const DecodeParams &p, int bs, int bp
         long long w = 0;
         if (s < p.num_seqs) {
             const SeqUnits u = seq_units<kShare>(p, s, bs, bps);
-            w = (one_unit ? 1ll : (long long)u.nunits) * (kUnitCost + u.ns);
+            w = (one_unit ? 1ll : (long long)u.nunits) * (kUnit + u.ns);
         }
         long long incl = w;
 #pragma unroll
@@ -903,9 +904,9 @@ __device__ __forceinline__ long long cta_of(long long x, long long total, long l
     return ((x + 1) * G - 1) / total;
 }
 
-// Emits unit u of sequence s (stream positions [a, a + kUnitCost + ns)) if its
-// real stages meet the CTA's range [s_c, e_c).  Returns false once the producer
-// aborted.
+// Emits unit u of sequence s (stream positions [a, a + Prod::kUnit + ns), the first
+// Prod::kLead of them charged) if its real stages meet the CTA's range [s_c, e_c).
+// Returns false once the producer aborted.
 template <bool kShare, class Prod>
 __device__ __forceinline__ bool emit_unit(const DecodeParams &p, Prod &pr, const SeqUnits &su,
                                           int s, long long u, long long a, long long s_c,
@@ -988,12 +989,12 @@ __device__ __forceinline__ bool walk_chunk(const DecodeParams &p, int bs, int bp
     if (s_c >= e_c)
         return true;
     long long base = 0;
-    int s = find_seq_at<kShare>(p, bs, bps, s_c, &base, lane);
+    int s = find_seq_at<kShare, Prod::kUnit>(p, bs, bps, s_c, &base, lane);
     for (; s < p.num_seqs && base < e_c && !*pr.c.abort; ++s) {
         const SeqUnits su = seq_units<kShare>(p, s, bs, bps);
         if (su.nunits == 0)
             continue;
-        const long long span = kUnitCost + su.ns;
+        const long long span = Prod::kUnit + su.ns;
         const long long u_lo = s_c > base ? (s_c - base) / span : 0;
         const long long u_hi = min((long long)su.nunits - 1, (e_c - 1 - base) / span);
         for (long long u = u_lo; u <= u_hi; ++u)
@@ -1024,14 +1025,14 @@ __device__ __forceinline__ bool walk_chunk_unit_major(const DecodeParams &p, int
     const long long W = total / U;  // positions of one unit of every sequence
     long long u = s_c / W;
     long long inner = 0;
-    int s = find_seq_at<true>(p, bs, bps, s_c - u * W, &inner, lane, true);
+    int s = find_seq_at<true, Prod::kUnit>(p, bs, bps, s_c - u * W, &inner, lane, true);
     long long base = u * W + inner;
     for (; u < U && base < e_c && !*pr.c.abort; ++u, s = 0) {
         for (; s < p.num_seqs && base < e_c; ++s) {
             const SeqUnits su = seq_units<true>(p, s, bs, bps);
             if (!emit_unit<true>(p, pr, su, s, u, base, s_c, e_c, total, G, cta, bps, div))
                 return false;
-            base += kUnitCost + su.ns;
+            base += Prod::kUnit + su.ns;
         }
     }
     return !*pr.c.abort;
@@ -1108,14 +1109,14 @@ __device__ __forceinline__ void walk_planned(const DecodeParams &p, int bs, int 
             for (; s < p.num_seqs && base < e_c; ++s) {
                 const SeqUnits su = first ? su0 : seq_units<true>(p, s, bs, bps);
                 first = false;
-                if (base + kUnitCost + su.ns > total) {
+                if (base + Prod::kUnit + su.ns > total) {
                     if (lane == 0)
                         atomicOr(p.errors, PA_DEVERR_PLAN);
                     return;
                 }
                 if (!emit_unit<true>(p, pr, su, s, u, base, s_c, e_c, total, G, cta, bps, div))
                     return;
-                base += kUnitCost + su.ns;
+                base += Prod::kUnit + su.ns;
             }
         }
         return;
@@ -1124,7 +1125,7 @@ __device__ __forceinline__ void walk_planned(const DecodeParams &p, int bs, int 
         const SeqUnits su = s == seq ? su0 : seq_units<kShare>(p, s, bs, bps);
         if (kShare && su.nunits == 0)
             continue;
-        const long long span = kUnitCost + su.ns;
+        const long long span = Prod::kUnit + su.ns;
         if (base + (long long)su.nunits * span > total) {
             if (lane == 0)
                 atomicOr(p.errors, PA_DEVERR_PLAN);
@@ -1151,7 +1152,7 @@ __device__ __forceinline__ void walk_balanced(const DecodeParams &p, int bs, int
     constexpr bool kOwn = kMode == kModeOwn;
     long long units = 0;
     bool prefix = false;
-    const long long total = stream_total<kShare, kOwn>(p, bs, bps, lane, &units, &prefix);
+    const long long total = stream_total<kShare, kOwn, Prod::kUnit>(p, bs, bps, lane, &units, &prefix);
     const int div = balanced_divisor(total, units);
     const long long G = balanced_grid(total, div);
     if ((long long)blockIdx.x >= G)

@@ -55,13 +55,6 @@
 // a movmatrix transpose per 8 x 8 half, as in the 16-bit kernel.
 #pragma once
 
-// Stream positions charged per unit for its fixed cost, in this kernel's ring stages
-// (8 KB, half of pa_decode's at 128 dims).  With 4, 6, 8, 10, 12 and 16: 64 ragged sequences
-// of 64 / 8 heads take 143, 140.4, 139.6, 139.4, 139.4 and 140.4 us, 8 of 40 / 40 heads 23.6,
-// 23.9, 23.7, 23.7, 24.2 and 24.9, 37 of 39 / 3 heads 19.5, 18.7, 18.4, 18.1, 18.0 and 18.3.
-#ifndef PA_UNIT_COST
-#define PA_UNIT_COST 10
-#endif
 #include "pa_decode.cuh"
 
 namespace pagedkv {
@@ -110,10 +103,15 @@ __device__ __forceinline__ uint32_t tile_unit(int tok, int u)
     return (uint32_t)(row * 128 + ((unit ^ (row & 7)) << 4));
 }
 
-// Half of a unit's charged positions lie before its stages and half behind: both parts of
-// a unit cut in the middle store, count and merge.  (152 units of 26 stages on 304 CTAs,
-// each cut once: 15.8 us with all of the charge before the stages, 13.8 with half.)
-constexpr int kLead8 = kUnitCost / 2;
+// Stream positions charged per unit for its fixed cost, in this kernel's ring stages
+// (8 KB, half of pa_decode's at 128 dims).  With 4, 6, 8, 10, 12 and 16: 64 ragged sequences
+// of 64 / 8 heads take 143, 140.4, 139.6, 139.4, 139.4 and 140.4 us, 8 of 40 / 40 heads 23.6,
+// 23.9, 23.7, 23.7, 24.2 and 24.9, 37 of 39 / 3 heads 19.5, 18.7, 18.4, 18.1, 18.0 and 18.3.
+constexpr int kUnitCost8 = 10;
+// Half of them lie before the unit's stages and half behind: both parts of a unit cut in
+// the middle store, count and merge.  (152 units of 26 stages on 304 CTAs, each cut once:
+// 15.8 us with all of the charge before the stages, 13.8 with half.)
+constexpr int kLead8 = kUnitCost8 / 2;
 
 constexpr int kThreads8 = kThreads + 32;  // one warp more than pa_decode: the scales'
 
@@ -161,6 +159,7 @@ struct Producer8 {
     // G = ceil(total / divisor) <= total: none is without (a division for each part, 38 of
     // them, kept the first copy of a single sequence's one head back by 5 us)
     static constexpr bool kCountParts = false;
+    static constexpr int kUnit = kUnitCost8;
     static constexpr int kLead = kLead8;
     using C = Cfg8<T, D, BS, NT>;
     const DecodeParams &p;
@@ -303,6 +302,7 @@ __device__ __forceinline__ float scale_exponent(float x)
 template <typename T, int D, int BS, int NT>
 struct ScaleWarp {
     static constexpr bool kCountParts = false;
+    static constexpr int kUnit = kUnitCost8;
     static constexpr int kLead = kLead8;
     using C = Cfg8<T, D, BS, NT>;
     const DecodeParams &p;

@@ -48,3 +48,15 @@ def test_views_of_a_cache_that_is_not_bytes_are_refused():
     cache = torch.zeros(3, size, dtype=torch.uint8)
     for same in (cache, cache.view(torch.int8), cache.view(torch.float8_e4m3fn)):
         assert P.q8_views(same, 2, 64, 16)[0].data_ptr() == cache.data_ptr()
+
+
+def test_schedule_constants_have_one_value_in_every_file():
+    """Device templates of pa_decode.cuh are instantiated in several files: a macro that one
+    of them set otherwise would give one name two meanings."""
+    import glob
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(P.__file__), "csrc")
+    files = {os.path.basename(f): open(f).read() for f in glob.glob(os.path.join(csrc, "*"))}
+    for macro in ("PA_UNIT_COST", "PA_MIN_POSITIONS", "PA_STAGE_TOKENS"):
+        assert [f for f, s in files.items() if re.search(rf"#define\s+{macro}\b", s)] == ["pa_internal.h"]
