@@ -473,10 +473,11 @@ size_t pa_q8_scales_offset(int num_kv_heads, int head_dim, int block_size);
  * they were.
  *
  * No block may be written for two sequences in one call (apply the step's copy-on-write
- * pairs first, pa_q8_copy_blocks), nor stand twice among the entries that one writes.  Rows at negative positions, past the table's
- * max_blocks_per_seq * block_size, of blocks outside [0, num_blocks), and rows of k and
- * v from query_start[num_seqs] on (padding) are skipped; nothing is accessed outside the
- * arguments.  Results do not depend on the order in which tokens arrive within a call.
+ * pairs first, pa_q8_copy_blocks), nor stand twice among the entries that one writes.
+ * Rows at negative positions, past the table's max_blocks_per_seq * block_size, of blocks
+ * outside [0, num_blocks), and rows of k and v from query_start[num_seqs] on (padding) are
+ * skipped; nothing is accessed outside the arguments.  Results do not depend on the order
+ * in which tokens arrive within a call.
  *
  *   k, v          device [num_tokens][num_kv_heads][head_dim], dtype `dtype`
  *   kv_cache      device, 16-byte aligned, written

@@ -696,7 +696,8 @@ __device__ __forceinline__ bool consume_item8(const DecodeParams &p, const CtaSt
                 // (one power for both: it is at most about 2, its factors may not be finite)
                 const bool fresh_a = ma[nt] == -INFINITY, fresh_b = mb[nt] == -INFINITY;
                 const float da = ma[nt] - na, db = mb[nt] - nb;
-                rescale(nt, fresh_a ? 0.f : exp2f(da + (old_a.y - ka)), fresh_b ? 0.f : exp2f(db + (old_b.y - kb)));
+                rescale(nt, fresh_a ? 0.f : exp2f(da + (old_a.y - ka)),
+                        fresh_b ? 0.f : exp2f(db + (old_b.y - kb)));
                 la[nt] *= fresh_a ? 0.f : exp2f(da);
                 lb[nt] *= fresh_b ? 0.f : exp2f(db);
                 ma[nt] = na;
@@ -1006,10 +1007,10 @@ __device__ __forceinline__ int merge_room(int rows_cap, int D)
 }
 
 // Merge the partials of a split unit into its output rows by the log-sum-exp rule, all
-// consumer warps together, where they are many: every (row, part)'s log2-sum-exp in one round of loads, a row's
-// weights by one warp, then the weighted rows, D / 4 threads per row with two rows and
-// eight parts of each in flight; with fewer rows than such groups of threads, several
-// groups share a row's parts.  `room`: the merge rows, free by now.  False on a timeout.
+// consumer warps together, where they are many: every (row, part)'s log2-sum-exp in one
+// round of loads, a row's weights by one warp, then the weighted rows, D / 4 threads per row
+// with two rows and eight parts of each in flight; with fewer rows than such groups of
+// threads, several groups share a row's parts.  `room`: the merge rows, free by now.  False on a timeout.
 template <typename T, int D>
 __device__ __forceinline__ bool merge8(const DecodeParams &p, const Item &it, const CtaState &c, uint32_t &sph,
                                        int warp, int lane, float *room)
@@ -1154,9 +1155,17 @@ __device__ __forceinline__ void merge_few(const DecodeParams &p, const Item &it,
 }
 
 // Whether merge_few's rounds take less than merge8's two exchanges: up to 16 parts, or 40
-// where the rows fill the groups of threads once.  (4 rows of 128 dims, 38 parts, one
-// sequence of 32 / 8 heads: 19.4 us against 20.6; 8 rows, 38 parts: 16.4 against 14.6; 1
-// row, 38 parts: 12.6 against 11.3.)
+// where the rows fill the groups of threads once.  Whole calls, one unit of so many parts,
+// bf16, us with merge_few / merge8:
+//     parts                  6          10          16          20          32          40
+//     128 dims,  1 row   8.5/10.0    8.5/10.0    9.3/10.2   10.5/10.5   10.9/10.4   12.7/11.4
+//                4 rows  8.5/9.9     8.6/10.0    9.5/10.9   10.7/11.8   11.2/12.5   12.8/13.6
+//                8 rows  9.8/10.8   10.0/11.0   11.6/12.0   13.4/12.8   14.6/13.6   16.9/14.8
+//               16 rows 14.3/15.2   15.0/15.8   18.2/17.5   21.3/19.3   24.1/21.2   28.0/24.1
+//      64 dims,  1 row   8.9/10.2    8.7/9.9     9.8/10.3   10.5/10.5   11.4/10.7   12.8/10.8
+//                8 rows  8.5/10.2    9.1/10.7    9.8/11.6   10.4/12.0   11.5/13.2   12.4/14.1
+//               16 rows 10.9/12.7   11.4/13.1   13.1/14.1   14.4/14.8   16.2/16.0   17.6/17.6
+// (The full groups, 4 rows of 128 dims and 8 of 64, keep a lead of 1.5 us at 64 parts.)
 template <int D>
 __device__ __forceinline__ bool few_rounds(const Item &it)
 {
