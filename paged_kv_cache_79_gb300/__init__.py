@@ -765,9 +765,9 @@ def q8_views(kv_cache, num_kv_heads: int, head_dim: int, block_size: int):
     return codes, scales
 
 
-def _check_counts(*counts) -> None:
-    # (ctypes would pass on the low 32 bits of a larger one)
-    _want(max(counts) < 2 ** 31, "tensors of 2^31 rows or columns and more are not taken")
+def _check_counts(bits: int) -> None:
+    """`bits`: sizes or-ed together (ctypes would pass on the low 32 bits of a larger one)."""
+    _want(not bits >> 31, "tensors of 2^31 rows or columns and more are not taken")
 
 
 def _check_batch(kv_cache, block_tables, context_lens, num_kv_heads, head_dim, block_size):
@@ -780,7 +780,6 @@ def _check_batch(kv_cache, block_tables, context_lens, num_kv_heads, head_dim, b
         raise ValueError("block_tables must be [S, W] and context_lens [S]")
     if kv_cache.dim() != 2 or kv_cache.shape[1] != pa_q8_block_bytes(num_kv_heads, head_dim, block_size):
         raise ValueError("kv_cache must be [num_blocks, pa_q8_block_bytes(...)]")
-    _check_counts(*block_tables.shape, kv_cache.shape[0])
 
 
 _APPEND_NAMES = ("k", "v", "kv_cache", "block_tables", "context_lens", "query_start")
@@ -798,9 +797,10 @@ def pa_q8_append(k, v, kv_cache, block_tables, context_lens, block_size: int, qu
     if k.dtype != v.dtype:
         raise TypeError("k and v must have one dtype")
     n, hkv, d = k.shape
-    _check_counts(n)
     S, W = block_tables.shape
     _check_batch(kv_cache, block_tables, context_lens, hkv, d, block_size)
+    blocks = kv_cache.shape[0]
+    _check_counts(n | S | W | blocks)
     tensors = (k, v, kv_cache, block_tables, context_lens)
     qs_ptr = None
     if query_start is not None:
@@ -811,7 +811,7 @@ def pa_q8_append(k, v, kv_cache, block_tables, context_lens, block_size: int, qu
         qs_ptr = query_start.data_ptr()
     dev, device = _on_device(_APPEND_NAMES, tensors)
     _call("pa_q8_append", device, k.data_ptr(), v.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(), W,
-          context_lens.data_ptr(), qs_ptr, S, n, kv_cache.shape[0], hkv, d, block_size, _code(k),
+          context_lens.data_ptr(), qs_ptr, S, n, blocks, hkv, d, block_size, _code(k),
           _raw_stream(stream, dev))
 
 
@@ -830,6 +830,8 @@ def pa_q8_decode(out, q, kv_cache, block_tables, context_lens, scale: float, num
     include/pagedkv.h); workspace: uint8 CUDA tensor or None (allocated here)."""
     S, W = block_tables.shape
     _check_batch(kv_cache, block_tables, context_lens, num_kv_heads, head_dim, block_size)
+    blocks = kv_cache.shape[0]
+    _check_counts(S | W | blocks)
     _want(q.shape == (S, num_q_heads, head_dim) and out.shape == q.shape, "q and out must be [S, Hq, d]")
     if out.dtype != q.dtype:
         raise TypeError("q and out must have one dtype")
@@ -841,7 +843,7 @@ def pa_q8_decode(out, q, kv_cache, block_tables, context_lens, scale: float, num
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous and on the device of q")
     _call("pa_q8_decode", device, out.data_ptr(), q.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(), W,
-          context_lens.data_ptr(), S, kv_cache.shape[0], float(scale), num_q_heads, num_kv_heads, head_dim,
+          context_lens.data_ptr(), S, blocks, float(scale), num_q_heads, num_kv_heads, head_dim,
           block_size, _code(q), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
           _raw_stream(stream, dev))
     return out
@@ -913,12 +915,13 @@ def pa_build_tables(block_tables, context_lens, new_tokens, free_list, num_free,
     _want(query_start.shape == (S + 1,), "query_start must be [S + 1]")
     _want(num_free.numel() == 1 and num_free_out.numel() == 1, "num_free and num_free_out hold one number")
     _want(free_list.dim() == 1 and slot_mapping.dim() == 1, "free_list and slot_mapping must have one dimension")
-    _check_counts(S, W, free_list.shape[0], slot_mapping.shape[0])
+    blocks, slots = free_list.shape[0], slot_mapping.shape[0]
+    _check_counts(S | W | blocks | slots)
     dev, device = _on_device(_TABLE_NAMES, tensors)
     _call("pa_build_tables", device, block_tables.data_ptr(), W, context_lens_out.data_ptr(),
-          context_lens.data_ptr(), new_tokens.data_ptr(), S, free_list.data_ptr(), free_list.shape[0],
+          context_lens.data_ptr(), new_tokens.data_ptr(), S, free_list.data_ptr(), blocks,
           num_free_out.data_ptr(), num_free.data_ptr(), block_size, granted.data_ptr(), query_start.data_ptr(),
-          slot_mapping.data_ptr(), slot_mapping.shape[0], _raw_stream(stream, dev))
+          slot_mapping.data_ptr(), slots, _raw_stream(stream, dev))
 
 
 def pa_kv_transfer_worthwhile(reusable_tokens: int, threshold_tokens: int = 64) -> bool:

@@ -164,6 +164,32 @@ def test_scales_over_the_whole_range(dtype):
         check(run_decode(c, q, bt, cl, scale, 4), c, q, bt, cl, scale, dtype)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d,group,lens", [(64, 1, [30000, 40]), (128, 4, [20000]), (64, 12, [9000, 12000]),
+                                          (128, 12, [30001])])
+def test_far_scales_in_units_of_many_parts(dtype, d, group, lens):
+    """As above in units that are merged from up to 38 parts and more: all blocks add alike
+    (first head), so no part's weight may be lost."""
+    hkv, b = 1, 16
+    rng = np.random.default_rng(30 + d + group)
+    nbs = [-(-t // b) for t in lens]
+    bt, _ = W.random_tables(rng, lens, b, sum(nbs), pad=1)
+    c = M.Cache(np.zeros((sum(nbs), M.block_bytes(hkv, b, d)), dtype=np.uint8), hkv, b, d)
+    c.codes[...] = M.encode(rng.uniform(32, 448, size=c.codes.shape) * rng.choice([-1.0, 1.0], size=c.codes.shape))
+    signs = rng.choice([-1.0, 1.0], size=(len(lens), d))
+    a = np.array([1.0, 1.25, 0.5, 2.0, 1.125, 0.75, 1.5, 1.0, 0.875, 1.0, 1.25, 3.0])[:group]
+    q = torch.from_numpy(signs[:, None] * a[None, :, None]).to(TD[dtype])
+    c.scales[..., 0] = 2.0 ** -5
+    for s, nb in enumerate(nbs):
+        e = np.sort(rng.integers(-12, 13, size=nb))           # parts far apart from each other
+        for j in range(nb):
+            c.codes[bt[s, j], 0, 0] = M.encode(signs[s] * float(-e[j]))
+            c.scales[bt[s, j], 0, 1] = rng.uniform(1, 2) * 2.0 ** (8 * int(e[j]))
+    scale = float(np.float32(8 * math.log(2) / (d * 2.0 ** -5)))
+    cl = np.array(lens, dtype=np.int32)
+    check(run_decode(c, q, bt, cl, scale, group), c, q, bt, cl, scale, dtype)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("scale", [0.37, 1.9999998, 3.1e-3, 1.1754944e-38])
 def test_one_token_of_any_scale_returns_its_value(dtype, scale):
