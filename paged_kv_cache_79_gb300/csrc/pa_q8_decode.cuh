@@ -11,8 +11,8 @@
 // What bounds it: the bytes of the codes, half of a 16-bit cache's; at G = 8 heads per
 // kv head that is 8 multiply-adds per byte, far below the tensor pipes' rate.  Of 6682 GB/s
 // (the measured copy) a batch of 2.0 GB (32 sequences, 32 / 8 heads) reaches 101%, one of
-// 0.86 GB (64 ragged sequences, 64 / 8 heads) 93%, back to back.  Small batches are bound
-// by their chain of latencies: 5.5 us for 50 tokens of one sequence, most of it the launch,
+// 0.86 GB (64 ragged sequences, 64 / 8 heads) 92%, back to back.  Small batches are bound
+// by their chain of latencies: 5.6 us for 50 tokens of one sequence, most of it the launch,
 // lengths, table entry and first tile one after another, and 2 to 3 us more where units are
 // cut, for the parts' stores, counts and merge.
 //
