@@ -501,9 +501,11 @@ pa_status pa_q8_append(const void *k, const void *v, void *kv_cache, const int32
  * kv head.  q and out are `dtype`; scores, softmax statistics and sums are fp32.  The
  * codes enter the products exactly; queries, and probabilities times V's scale, enter them in
  * fp16 (fp32 queries and outputs: two fp16 terms, about 22 bits).  Scales may be any finite,
- * non-negative values, powers of two or not, and as far apart as they like: no block's scale
- * takes precision from the blocks that carry the weight (V scales more than 2^6 apart cost up
- * to a sixth of the time).  Sums of probability times |code * scale| have to stay within
+ * non-negative values, powers of two or not, and as far apart as they like: a product of
+ * probability and scale is held to 2^-11 of itself (fp32: 2^-22), or to 2^-31 of its row's
+ * largest such product where that is more, so that a block of large scale takes precision
+ * from others only as its probability counts.  (V scales more than 2^6 apart cost up to a
+ * sixth of the time.)  Sums of probability times |code * scale| have to stay within
  * fp32's range.  T = 0 yields a zero row, and so does a row whose scores are all -inf; rows
  * past T are never counted, whatever they hold; a table entry outside [0, num_blocks) reads
  * zeros; a NaN among a sequence's codes makes the outputs that it enters NaN.  num_q_heads /

@@ -32,18 +32,19 @@
 // accumulation truncates.
 //
 // Scales.  ks multiplies the fp32 scores.  vs = 2^e f, 1/2 < f <= 1, multiplies p before its
-// rounding, over 2^k mu.  mu is the mantissa (1 <= mu < 2) of the first vs that is not 0, so that
-// scales that are alike but for powers of two round nothing.  k is the largest e the warp
-// has met in the item, as long as the e lie within kSpread of each other: then each row's
-// largest product is within that of the reference.  Scales that are further apart take a
-// slower path from there on, as a block whose vs is large while its p is nothing must
-// not push the blocks that count out of fp16's range: each row has a second reference
-// beside the scores' maximum m, w = the largest s + e, and a k of its own, ceil(w - m); the
+// rounding, over 2^k mu.  mu is the mantissa (1 <= mu < 2) of the first vs that is not 0,
+// so that scales that are alike but for powers of two round nothing.  k is the largest e
+// the warp has met in the item, as long as the e lie within kSpread of each other: then
+// each row's largest product is within that of the reference.  Scales that are further
+// apart, or 0 beside others (the scores' maximum may be a token that adds nothing), take a
+// slower path from there on, as a block whose vs is large while its p is nothing must not
+// push the blocks that count out of fp16's range: each row has a second reference beside
+// the scores' maximum m, w = the largest s + e, and a k of its own, ceil(w - m); the
 // products are 2^(s - m + e - k) f / mu, the power taken as a whole (p alone may be below
 // fp32's range although the product counts), and the accumulator follows new references by
-// 2^(m - m' + k - k').  (16 sequences of 2000 tokens, 104 / 8 heads, fp16: 32.3 us, with scales
-// 10 binades apart 35.3; 64 sequences, 64 / 8 heads, bf16: 140.0 and 145.1.  Rows' own k
-// throughout took 35.5 of the former.)
+// 2^(m - m' + k - k').  (16 sequences of 2000 tokens, 104 / 8 heads, fp16: 32.3 us, with
+// scales 10 binades apart 35.3; 64 sequences, 64 / 8 heads, bf16: 140.0 and 145.1.  Rows'
+// own k throughout took 35.5 of the former.)
 //
 // Layout of the products (16 tokens at a time).  S^T[token x row] = K Q^T: row r of the
 // A tile is token 4 (r / 2) + r % 2 for r < 8 and that plus 2 for r >= 8, and the k order
@@ -329,11 +330,11 @@ struct ScaleWarp {
         return __ldcg(reinterpret_cast<const float2 *>(q8.scales + (size_t)id * q8.block_bytes) + it.kvh);
     }
 
-    // Largest and smallest e of the V scales (scale_exponent) of the lane's stage, whose
-    // blocks are kBPS consecutive lanes'.
-    static __device__ float2 range_of(float vs)
+    // Largest and smallest e of the V scales (scale_exponent; a block past the item is
+    // neither) of the lane's stage, whose blocks are kBPS consecutive lanes'.
+    static __device__ float2 range_of(float vs, bool past)
     {
-        float2 e = make_float2(scale_exponent(vs), vs == 0.f ? INFINITY : scale_exponent(vs));
+        float2 e = make_float2(scale_exponent(vs), past ? INFINITY : scale_exponent(vs));
 #pragma unroll
         for (int o = 1; o < C::kBPS; o <<= 1) {
             e.x = fmaxf(e.x, __shfl_xor_sync(0xffffffffu, e.x, o));
@@ -361,7 +362,7 @@ struct ScaleWarp {
             const float2 next_s = scales_of(it, next_id);
             next_id = block_id(it, row, jb + 64 + lane);
             const int cnt = min(32, it.j1 - jb);
-            const float2 range = range_of(s.y);
+            const float2 range = range_of(s.y, lane >= cnt);
             for (int i = 0; i < cnt; i += C::kBPS, ++g) {
                 const uint32_t st = g % C::kStages;
                 int ok = 1;

@@ -127,6 +127,25 @@ def test_scales_of_zero_among_others(dtype):
         assert not out[6].any()
 
 
+@pytest.mark.parametrize("above", [1, 20, 60, 100])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("d,group,outside", [(128, 3, False), (64, 12, False), (128, 3, True)])
+def test_blocks_of_zeros_that_score_highest(d, group, outside, dtype, above):
+    """Scales of 0, or table entries outside the pool, `above` binades over scales that are all
+    alike: what the others add is small, and all there is."""
+    c, q, bt, cl, _ = two_level_case(13, dtype, d, 16, group, 10, False)
+    c.scales[..., 1] = 2.0 ** -6
+    for s, js in enumerate([[0], [1], [0, 43], list(range(0, 44, 3)), [20], [81], [0, 1, 2], [4]]):
+        sign = np.sign(q[s].double().numpy())[::group, None]
+        c.codes[bt[s], :, 0] = M.encode((-8.0 if outside else 0.0) * sign)
+        c.codes[bt[s, js], :, 0] = M.encode((0.0 if outside else 8.0) * sign)
+        c.scales[bt[s, js], :, 1] = 0.0
+        if outside:
+            bt[s, js] = len(c.raw) + 5
+    scale = float(np.float32(above * math.log(2) / (8 * d * 2.0 ** -5)))
+    check(run_decode(c, q, bt, cl, scale, 2 * group), c, q, bt, cl, scale, dtype)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("group", [3, 12])
 def test_scores_that_overflow_before_others_that_do_not(dtype, group):
