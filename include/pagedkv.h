@@ -433,6 +433,71 @@ pa_status pa_scatter_blocks(const void *staging_k, const void *staging_v, void *
                             size_t block_bytes, void *stream);
 
 /* ------------------------------------------------------------------------- *
+ * Rotary positions.  The pages have no counterpart: what a model does to its  *
+ * queries and keys before they reach the cache and the attention.             *
+ * ------------------------------------------------------------------------- */
+
+/*
+ * pa_rope_append / pa_rope -- turn queries and keys by their positions; pa_rope_append also
+ * writes the turned keys and the values through the slot map into the paged cache, as
+ * pa_reshape_and_cache does.
+ *
+ * For every token t and pair i < rotary_dim / 2 of each head, elements (a, b) = (i, i +
+ * rotary_dim / 2), or with `interleaved` (2i, 2i + 1), become
+ *     amplitude * (a cos w - b sin w, b cos w + a sin w),   w = 2 pi freqs[i] positions[t] / 2^64
+ * in fp32, rounded once to `dtype`; elements from rotary_dim on are copied.  freqs[i] is the
+ * pair's turns of a full circle per position in units of 2^-64 (pa_rope_frequencies makes
+ * them): the product with a position is taken modulo a turn exactly, so far positions are as
+ * precise as near ones (angles to 2^-24 of half a turn).  Positions may be negative.
+ *
+ *   q, q_out        device rows of [Hq][d]; strides in elements from one token's row to the
+ *                   next, multiples of 16 bytes and at least a row (so q may be part of a
+ *                   fused projection's rows).  q_out may be q, with the same stride; it must
+ *                   not overlap it otherwise.
+ *   k, v            device rows of [Hkv][d], likewise with strides
+ *   k_out           (pa_rope) rows of [Hkv][d]; may be k with the same stride
+ *   k_cache, v_cache, slot_mapping  (pa_rope_append) as pa_reshape_and_cache's; a slot outside
+ *                   [0, num_blocks * block_size) skips the cache, the token's queries are
+ *                   turned all the same.  Two tokens with one slot: either's row may land.
+ *   positions       device int32 [num_tokens];  freqs device int64 [rotary_dim / 2]
+ *   rotary_dim      a multiple of 16, at most head_dim;  head_dim 64 or 128
+ * Errors: PA_ERR_INVALID (null or misaligned pointer, bad size or stride, amplitude not
+ *   finite), PA_ERR_UNSUPPORTED (head_dim, rotary_dim or dtype not built, more than 2^24
+ *   elements a token), PA_ERR_CUDA.  num_tokens = 0 is a no-op.
+ */
+pa_status pa_rope_append(void *q_out, long long q_out_stride, const void *q, long long q_stride,
+                         const void *k, long long k_stride, const void *v, long long v_stride,
+                         void *k_cache, void *v_cache, const int32_t *positions,
+                         const int64_t *slot_mapping, const int64_t *freqs, int num_tokens,
+                         int num_q_heads, int num_kv_heads, int head_dim, int rotary_dim, int interleaved,
+                         float amplitude, int block_size, int num_blocks, pa_dtype dtype, void *stream);
+pa_status pa_rope(void *q_out, long long q_out_stride, const void *q, long long q_stride, void *k_out,
+                  long long k_out_stride, const void *k, long long k_stride, const int32_t *positions,
+                  const int64_t *freqs, int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                  int rotary_dim, int interleaved, float amplitude, pa_dtype dtype, void *stream);
+
+/*
+ * pa_rope_frequencies -- freqs (host int64 [rotary_dim / 2]) and amplitude of the usual
+ * angles base^(-2i / rotary_dim) per position, scaled for contexts `factor` times as long as
+ * original_len, the length that the model was trained on:
+ *   PA_ROPE_NONE    unscaled (factor, original_len, low and high are not read)
+ *   PA_ROPE_LINEAR  angles divided by factor
+ *   PA_ROPE_NTK     base * factor^(rotary_dim / (rotary_dim - 2)) in base's place
+ *   PA_ROPE_BANDS   between divided and unscaled, by a ramp over the pair's turns within
+ *                   original_len: divided up to `low` turns, unscaled from `high` turns
+ *   PA_ROPE_YARN    the same between the pair of `high` turns and that of `low` turns, by a
+ *                   ramp over the pair's index (whole indices outwards), and amplitude
+ *                   0.1 ln(factor) + 1
+ * amplitude is 1 otherwise.  Host only.  Errors: PA_ERR_INVALID (null pointer, odd or
+ * non-positive rotary_dim, base not above 1, factor below 1, original_len <= 0, not
+ * 0 < low < high), PA_ERR_UNSUPPORTED (unknown scaling).
+ */
+typedef enum { PA_ROPE_NONE = 0, PA_ROPE_LINEAR = 1, PA_ROPE_NTK = 2, PA_ROPE_BANDS = 3, PA_ROPE_YARN = 4 } pa_rope_scaling;
+pa_status pa_rope_frequencies(int64_t *freqs, float *amplitude, int rotary_dim, double base,
+                              pa_rope_scaling scaling, double factor, double original_len, double low,
+                              double high);
+
+/* ------------------------------------------------------------------------- *
  * The 8-bit cache.  The pages have no counterpart: the same paged cache, half *
  * the bytes of a 16-bit one, so half the bytes a decode has to read.          *
  * ------------------------------------------------------------------------- */
@@ -582,6 +647,55 @@ pa_status pa_build_tables(int32_t *block_tables, int max_blocks_per_seq, int32_t
                           int32_t *free_list, int num_blocks, int32_t *num_free_out,
                           const int32_t *num_free, int block_size, int32_t *granted,
                           int32_t *query_start, int64_t *slot_mapping, int num_slots, void *stream);
+
+/*
+ * pa_fork_tables -- the next step's batch from rows of this one's, on the GPU: samples of a
+ * prompt, beams that go on or end, finished requests.
+ *
+ * The device counterpart of pa_alloc_fork, the copy-on-write of pa_alloc_append and
+ * pa_alloc_free_seq ([T] §5.1, [S] "Memory sharing"), for batches whose blocks are shared.
+ * extra_refs[b] counts block b's references beyond the first: 0 for a block that one row
+ * holds (so a block that pa_build_tables grants needs no entry) and for a free one.  New
+ * row i goes on from old row parents[i], or is empty when parents[i] is outside
+ * [0, num_rows); old rows that no new one goes on from are released.  With T =
+ * context_lens[parents[i]] tokens in ceil(T / B) blocks:
+ *   full blocks       shared: new row i holds its parent's
+ *   half-filled last  (T % B != 0) stays with the first new row of that parent; every later
+ *                     one gets a block of its own from the end of the free list, in the order
+ *                     of the rows, and copy_pairs[i] = (parent's block, its own): the copies
+ *                     to run (pa_copy_blocks, pa_q8_copy_blocks) before the next append
+ *   references        each old row drops one of every block it held, each new row takes one
+ *                     of every block it holds; a block without any left goes to the end of
+ *                     the free list, such blocks in ascending order, before any is handed out
+ * A row that finds the free list empty is refused: it becomes an empty row and holds nothing
+ * (the first new row of a parent never is).
+ * So no block that can still be written is shared, and pa_build_tables grows the new batch; it
+ * must not release rows that share blocks (new_tokens < 0): release them here.
+ *
+ *   block_tables_out  int32 [num_children][max_blocks_per_seq], written whole: -1 behind the
+ *                     row's blocks; must not overlap block_tables
+ *   context_lens_out  int32 [num_children]: T, 0 for empty and refused rows; must not overlap
+ *                     context_lens
+ *   extra_refs        int32 [num_blocks], updated; no entry below 0 (such a block would be
+ *                     taken for one that has lost its last reference)
+ *   free_list, num_free, num_free_out  as pa_build_tables's (num_free_out may be num_free)
+ *   copy_pairs        int32 [num_children][2]: (-1, -1) where nothing is copied
+ *   granted           int32 [num_children]: 1 goes on, 0 empty, -1 refused
+ * Deterministic.  Lengths are clamped to [0, max_blocks_per_seq * block_size], *num_free to
+ * [0, num_blocks]; table entries outside [0, num_blocks) are copied and counted nowhere; a
+ * free-list entry outside is handed out as it is; pushes past num_blocks are dropped.  Nothing
+ * is accessed outside the arguments.
+ * Errors: PA_ERR_INVALID (null or misaligned pointer, negative count, non-positive size,
+ *   block_tables_out = block_tables, context_lens_out = context_lens, num_blocks or
+ *   max_blocks_per_seq * block_size >= 2^31), PA_ERR_UNSUPPORTED (more than 65536 rows or
+ *   children, max_blocks_per_seq above 65535 * 1024, num_blocks above 2^31 - 1024), PA_ERR_CUDA.
+ */
+pa_status pa_fork_tables(int32_t *block_tables_out, const int32_t *block_tables, int max_blocks_per_seq,
+                         int32_t *context_lens_out, const int32_t *context_lens, int num_rows,
+                         const int32_t *parents, int num_children, int32_t *extra_refs,
+                         int32_t *free_list, int num_blocks, int32_t *num_free_out,
+                         const int32_t *num_free, int block_size, int32_t *copy_pairs, int32_t *granted,
+                         void *stream);
 
 /*
  * Host predicate of [K] "KV recompute threshold": fetching another engine's KV for

@@ -18,6 +18,10 @@ calls on tensors that are not CUDA tensors raise.
     pa_q8_append /          the same cache in 8 bits (e4m3 codes, a scale per block and
       pa_q8_decode            kv head): quantising append, and decode attention over it
     pa_build_tables         block tables, lengths and slot maps grown and released on the GPU
+    pa_fork_tables          the next batch's tables from rows of this one's, on the GPU (samples,
+                              beams), with reference counts and copies of half-filled blocks
+    pa_rope /               rotary positions of queries and keys, and the same with the append
+      pa_rope_append          of keys and values
     BlockAllocator          host ref-counted block allocator (pa_alloc_*)
 """
 from __future__ import annotations
@@ -924,6 +928,132 @@ def pa_build_tables(block_tables, context_lens, new_tokens, free_list, num_free,
           slot_mapping.data_ptr(), slots, _raw_stream(stream, dev))
 
 
+_FORK_NAMES = ("block_tables", "context_lens", "parents", "extra_refs", "free_list", "num_free", "copy_pairs",
+               "granted", "block_tables_out", "context_lens_out", "num_free_out")
+
+
+def pa_fork_tables(block_tables_out, context_lens_out, block_tables, context_lens, parents, extra_refs, free_list,
+                   num_free, block_size: int, copy_pairs, granted, num_free_out=None, stream=None):
+    """New rows [C, W] that go on from old ones ([S, W]; parents int32 [C], outside [0, S):
+    empty), sharing full blocks by extra_refs (int32 [num_blocks], references beyond the
+    first), with copies for half-filled last blocks (copy_pairs int32 [C, 2]: run
+    pa_copy_blocks) and the blocks that nobody holds any more back on the free list (see
+    pa_fork_tables in include/pagedkv.h).  num_free_out defaults to num_free, in place."""
+    if num_free_out is None:
+        num_free_out = num_free
+    tensors = (block_tables, context_lens, parents, extra_refs, free_list, num_free, copy_pairs, granted,
+               block_tables_out, context_lens_out, num_free_out)
+    int32 = _torch().int32
+    for name, t in zip(_FORK_NAMES, tensors):
+        if t.dtype != int32:
+            raise TypeError(f"{name} must be int32")
+    _want(block_tables.dim() == 2 and block_tables_out.dim() == 2, "block_tables must be [S, W]")
+    S, W = block_tables.shape
+    C = block_tables_out.shape[0]
+    _want(block_tables_out.shape[1] == W, "block_tables_out must be [C, W]")
+    _want(context_lens.shape == (S,) and context_lens_out.shape == (C,) and parents.shape == (C,) and
+          granted.shape == (C,), "context_lens must be [S]; context_lens_out, parents and granted [C]")
+    _want(copy_pairs.shape == (C, 2), "copy_pairs must be [C, 2]")
+    _want(num_free.numel() == 1 and num_free_out.numel() == 1, "num_free and num_free_out hold one number")
+    _want(free_list.dim() == 1 and extra_refs.shape == free_list.shape, "free_list and extra_refs must be [num_blocks]")
+    blocks = free_list.shape[0]
+    _check_counts(S | W | C | blocks)
+    dev, device = _on_device(_FORK_NAMES, tensors)
+    _call("pa_fork_tables", device, block_tables_out.data_ptr(), block_tables.data_ptr(), W,
+          context_lens_out.data_ptr(), context_lens.data_ptr(), S, parents.data_ptr(), C, extra_refs.data_ptr(),
+          free_list.data_ptr(), blocks, num_free_out.data_ptr(), num_free.data_ptr(), block_size,
+          copy_pairs.data_ptr(), granted.data_ptr(), _raw_stream(stream, dev))
+
+
+# ----------------------------------------------------------------------------
+# rotary positions
+# ----------------------------------------------------------------------------
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     original_len: float = 0.0, low: float = 1.0, high: float = 32.0):
+    """(freqs int64 [rotary_dim / 2] on the host, amplitude) of pa_rope and pa_rope_append:
+    turns per position in units of 2^-64, unscaled or scaled for long contexts ("linear",
+    "ntk", "bands", "yarn"; see pa_rope_frequencies in include/pagedkv.h).  A program copies
+    freqs to the device once."""
+    import torch
+    _want(scaling in ROPE_SCALINGS, f"scaling must be one of {sorted(ROPE_SCALINGS)}")
+    _want(0 < rotary_dim <= 1 << 20 and rotary_dim % 2 == 0, "rotary_dim must be even and positive")
+    freqs = torch.empty(rotary_dim // 2, dtype=torch.int64)
+    amplitude = ctypes.c_float()
+    _check(_load().pa_rope_frequencies(freqs.data_ptr(), ctypes.byref(amplitude), rotary_dim, base,
+                                       ROPE_SCALINGS[scaling], factor, original_len, low, high),
+           "pa_rope_frequencies")
+    return freqs, amplitude.value
+
+
+def _rows(t, name: str, n: int, d: int):
+    """Stride between the rows of a [N, H, d] tensor whose rows are dense (in elements)."""
+    if t.dim() != 3 or t.shape[0] != n or t.shape[2] != d or not t.shape[1]:
+        raise ValueError(f"{name} must be [{n}, heads, {d}]")
+    h = t.shape[1]
+    row, head, one = t.stride()
+    if one != 1 or (head != d and h > 1):
+        raise ValueError(f"{name} must have dense [heads, head_dim] rows")
+    return row if n > 1 else h * d
+
+
+def _rope_args(dense, rows, positions, freqs):
+    """Checks that pa_rope and pa_rope_append share: (device index, device context, n, d, strides)."""
+    T = _torch()
+    names, tensors = tuple(rows), tuple(rows.values())
+    q = rows["q"]
+    n, _, d = q.shape if q.dim() == 3 else (0, 0, 0)
+    strides = tuple(_rows(t, name, n, d) for name, t in rows.items())
+    for name, t in {**rows, **dense}.items():
+        if t.dtype != q.dtype:
+            raise TypeError(f"{name} and q must have one dtype")
+    if positions.dtype != T.int32 or freqs.dtype != T.int64:
+        raise TypeError("positions must be int32 and freqs int64")
+    _want(positions.shape == (n,) and freqs.dim() == 1, "positions must be [N] and freqs [rotary_dim / 2]")
+    _check_counts(n)
+    dev, device = _on_device(tuple(dense) + ("positions", "freqs"), tuple(dense.values()) + (positions, freqs))
+    for name, t in zip(names, tensors):
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be a CUDA tensor on the device of positions")
+    return dev, device, n, d, strides
+
+
+def pa_rope(q_out, q, k_out, k, positions, freqs, interleaved: bool = False, amplitude: float = 1.0, stream=None):
+    """q_out, k_out [N, H, d] <- q, k turned by their positions (see pa_rope in
+    include/pagedkv.h).  Rows may be strided (parts of a fused projection); q_out may be q
+    and k_out k.  freqs int64 [rotary_dim / 2]: rope_frequencies's, on the device."""
+    dev, device, n, d, (qos, qs, kos, ks) = _rope_args(
+        {}, {"q_out": q_out, "q": q, "k_out": k_out, "k": k}, positions, freqs)
+    _want(q_out.shape == q.shape and k_out.shape == k.shape, "q_out must be as q and k_out as k")
+    _call("pa_rope", device, q_out.data_ptr(), qos, q.data_ptr(), qs, k_out.data_ptr(), kos, k.data_ptr(), ks,
+          positions.data_ptr(), freqs.data_ptr(), n, q.shape[1], k.shape[1], d, 2 * freqs.shape[0],
+          int(interleaved), float(amplitude), _code(q), _raw_stream(stream, dev))
+
+
+def pa_rope_append(q_out, q, k, v, k_cache, v_cache, positions, slot_mapping, freqs, interleaved: bool = False,
+                   amplitude: float = 1.0, stream=None):
+    """q_out [N, Hq, d] <- q turned by its positions; k turned likewise and v go through
+    slot_mapping (int64 [N], negative: skipped) into the caches [num_blocks, B, Hkv, d] (see
+    pa_rope_append in include/pagedkv.h).  q, k and v may be strided rows of one fused
+    projection; q_out may be q."""
+    dev, device, n, d, (qos, qs, ks, vs) = _rope_args(
+        {"k_cache": k_cache, "v_cache": v_cache, }, {"q_out": q_out, "q": q, "k": k, "v": v}, positions, freqs)
+    if slot_mapping.dtype != _torch().int64:
+        raise TypeError("slot_mapping must be int64")
+    _want(q_out.shape == q.shape and v.shape == k.shape, "q_out must be as q and v as k")
+    _want(k_cache.dim() == 4 and k_cache.shape == v_cache.shape and k_cache.shape[2:] == k.shape[1:],
+          "the caches must be [num_blocks, B, Hkv, d]")
+    _want(slot_mapping.shape == (n,), "slot_mapping must be [N]")
+    _on_device(("positions", "slot_mapping"), (positions, slot_mapping))
+    _check_counts(k_cache.shape[0] | k_cache.shape[1])
+    _call("pa_rope_append", device, q_out.data_ptr(), qos, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+          k_cache.data_ptr(), v_cache.data_ptr(), positions.data_ptr(), slot_mapping.data_ptr(), freqs.data_ptr(), n,
+          q.shape[1], k.shape[1], d, 2 * freqs.shape[0], int(interleaved), float(amplitude), k_cache.shape[1],
+          k_cache.shape[0], _code(q), _raw_stream(stream, dev))
+
+
 def pa_kv_transfer_worthwhile(reusable_tokens: int, threshold_tokens: int = 64) -> bool:
     """Fetch another engine's KV for a prefix (True) or recompute it (False)."""
     return bool(_load().pa_kv_transfer_worthwhile(int(reusable_tokens), int(threshold_tokens)))
@@ -938,6 +1068,7 @@ __all__ = ["pa_decode", "pa_decode_append", "pa_decode_plan_bytes", "pa_decode_p
            "pa_reshape_and_cache", "pa_copy_blocks", "pa_swap_blocks", "pa_gather_blocks",
            "pa_scatter_blocks", "pa_q8_block_bytes", "alloc_q8_cache", "q8_views", "pa_q8_append", "pa_q8_decode",
            "pa_q8_decode_workspace_size", "pa_q8_copy_blocks", "pa_q8_swap_blocks", "pa_build_tables",
+           "pa_fork_tables", "rope_frequencies", "ROPE_SCALINGS", "pa_rope", "pa_rope_append",
            "pa_kv_transfer_worthwhile", "pa_device_errors", "pa_set_wait_limit_ns",
            "PA_DEVERR_TIMEOUT_FULL", "PA_DEVERR_TIMEOUT_EMPTY", "PA_DEVERR_SHARE", "PA_WAIT_LIMIT_DEFAULT_NS", "pa_status_string",
            "BlockAllocator", "PagedKVError", "OutOfBlocks", "library_path"]

@@ -211,6 +211,83 @@ struct TablesParams {
 };
 cudaError_t launch_build_tables(TablesParams p, cudaStream_t stream);
 
+// Sequences, tokens, slots and blocks at most where a kernel goes through them up to 1024 at
+// a time, in 32-bit numbers that must not pass 2^31 on the last round.
+constexpr int kMaxCount = 0x7fffffff - 1023;
+
+// ---- rotary positions ------------------------------------------------------------
+struct RopeParams {
+    void *q_out;                      // rows of [Hq][d], strides in elements
+    const void *q;
+    void *k_out;                      // rows of [Hkv][d]: the cache's slots, or plain rows
+    const void *k;
+    void *v_out;                      // with slots
+    const void *v;                    // null: keys and queries alone
+    long long q_out_stride, q_stride, k_out_stride, k_stride, v_stride;
+    const int32_t *positions;
+    const int64_t *slots;             // null: row t of k goes to row t of k_out
+    const unsigned long long *freqs;  // [half] turns per position, in units of 2^-64
+    long long num_slots;
+    int num_tokens, num_q_heads, num_kv_heads, head_dim;
+    int half;                         // pairs that turn
+    int interleaved;
+    int units_per_token;              // set by the launcher
+    float amplitude;
+};
+
+// ---- attention of several query tokens -------------------------------------------
+// What the merge kernel has to know about the item that a CTA's start cuts.
+struct AttendCut {
+    int parts;   // 0: the start cuts no item, or not as the first cut of one
+    int token0;  // the item's first query token (row of q), and its tokens
+    int tokens;
+    int head0;   // its first query head, and its heads
+    int heads;
+    int unused[3];
+};
+struct AttendParams {
+    void *out;                    // [N][Hq][D]
+    float *lse;                   // [N][Hq] or null
+    const void *q;                // rows of [Hq][D], q_stride elements apart
+    const void *k_cache, *v_cache;
+    const int32_t *block_tables, *context_lens, *query_start;
+    AttendCut *cuts;              // workspace: [CTAs]
+    float2 *part_ml;              // [CTAs][2][part_rows] maximum (log2 units), sum
+    float *part_o;                // [CTAs][2][part_rows][D]
+    unsigned int *errors;
+    unsigned long long wait_ns;
+    long long q_stride;
+    float scale_log2;
+    int num_seqs, num_rows, max_blocks, num_blocks, block_size;
+    int num_q_heads, num_kv_heads, group;
+    int heads_per_item, head_chunks, units;  // units: kv heads * chunks of their groups
+    int tokens_per_item;
+    int part_rows;
+    int causal;
+};
+struct AttendLaunch {
+    AttendParams p;
+    CUtensorMap map_q, map_k, map_v;
+    int head_dim, sms, ctas;      // ctas: the grid
+};
+
+// ---- forked tables ---------------------------------------------------------------
+constexpr int kForkMaxRows = 1 << 16;
+struct ForkParams {
+    int32_t *tables_out;
+    const int32_t *tables_in;
+    int32_t *context_lens_out;
+    const int32_t *context_lens;
+    const int32_t *parents;
+    int32_t *extra;
+    int32_t *free_list;
+    int32_t *num_free_out;
+    const int32_t *num_free;
+    int32_t *pairs;
+    int32_t *granted;
+    int max_blocks, rows, children, num_blocks, block_size;
+};
+
 // Persistent grid (CTAs) of a balanced-split launch of the plain decode with a
 // plan; 0 if the configuration cannot launch.
 int plan_grid_f32(const DecodeLaunch &L);

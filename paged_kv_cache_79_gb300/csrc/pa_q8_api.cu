@@ -9,10 +9,6 @@ using namespace pagedkv;
 
 namespace {
 
-// Sequences, tokens and slots at most: a kernel goes through them up to 1024 at a time, in
-// 32-bit numbers that must not pass 2^31 on the last round.
-constexpr int kMaxCount = 0x7fffffff - 1023;
-
 // Sizes every entry point of the cache shares.
 pa_status check_sizes(int num_blocks, int max_blocks, int num_kv_heads, int head_dim, int block_size,
                       int dtype)
