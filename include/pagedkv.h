@@ -347,6 +347,58 @@ pa_status pa_decode_noalloc(void *out, const void *q, const void *k_cache, const
                             int block_size, pa_dtype dtype, int partition_size, void *stream);
 
 /* ------------------------------------------------------------------------- *
+ * Attention of several query tokens per sequence.                             *
+ * ------------------------------------------------------------------------- */
+
+/*
+ * pa_attend -- attention of a ragged batch of query tokens over the paged cache: cross
+ * attention to an encoder's states of another length, chunks of prompts behind a cached
+ * context, a few drafted tokens a sequence, or a mixture of them.
+ *
+ * [S]'s block-wise attention equation, as pa_decode, for n_s = query_start[s + 1] -
+ * query_start[s] query tokens of sequence s, rows query_start[s] .. of q.  With T =
+ * context_lens[s], query token i of the sequence sees the keys
+ *     causal = 0    t < T: all of them (cross attention)
+ *     causal = 1    t <= T - n_s + i: the query tokens are the sequence's last n_s, their own
+ *                   keys in the cache already (pa_reshape_and_cache, pa_rope_append)
+ * and   out[r][h] = sum_t exp(s_t - max) V_t / sum_t exp(s_t - max),   s_t = scale q[r][h] . K_t
+ *       lse[r][h] = log sum_t exp(s_t)          (natural logarithm; to merge with other keys)
+ * A row that sees no key (T = 0, or n_s > T with causal) yields zeros and lse -inf.  Scores,
+ * statistics and sums are fp32; probabilities enter the second product in `dtype` (fp16 and
+ * bf16: rounded to 2^-12 and 2^-9 of themselves; fp32: two tf32 terms, about 21 bits).  Keys
+ * past T are never counted, whatever their rows hold; a table entry outside [0, num_blocks)
+ * reads zeros.  A NaN or infinity among the values of a sequence's context can make NaN also
+ * of its query tokens that do not see it.  One query token of every sequence is
+ * pa_decode's case, which takes half the time; here it may stand among longer ones.
+ *
+ *   out            device [num_tokens][Hq][d]; rows of q and out from query_start[num_seqs] on
+ *                  are padding: not read, and left as they were
+ *   lse            device fp32 [num_tokens][Hq], or NULL
+ *   q              device rows of [Hq][d], q_stride elements from one token's to the next (a
+ *                  multiple of 16 bytes, at least Hq * d: q may be part of a fused projection)
+ *   query_start    device int32 [num_seqs + 1], non-decreasing from 0 to at most num_tokens
+ *   others         as pa_decode's; num_q_heads / num_kv_heads may be any size
+ *   workspace      device, 16-byte aligned, pa_attend_workspace_size bytes; no initialisation.
+ *                  Calls that may overlap need one each.
+ * Results do not depend on the order in which CTAs run.  Waits are bounded and reported as
+ * pa_decode's are (pa_device_errors).
+ * Errors: PA_ERR_INVALID (null or misaligned pointer, bad size or stride, workspace too small,
+ *   num_blocks or max_blocks_per_seq times block_size >= 2^31), PA_ERR_UNSUPPORTED (head_dim,
+ *   block_size or dtype not built, more than 65535 query heads, num_seqs or num_tokens above
+ *   2^31 - 1024, q_stride of 2^36 and more), PA_ERR_CUDA.  num_seqs = 0 or num_tokens = 0 is a
+ *   no-op.
+ */
+pa_status pa_attend(void *out, float *lse, const void *q, long long q_stride, const void *k_cache,
+                    const void *v_cache, const int32_t *block_tables, int max_blocks_per_seq,
+                    const int32_t *context_lens, const int32_t *query_start, int num_seqs, int num_tokens,
+                    int num_blocks, float scale, int causal, int num_q_heads, int num_kv_heads, int head_dim,
+                    int block_size, pa_dtype dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace pa_attend needs on the current device, whatever the lengths: two slots of
+ * partial rows per SM.  (size_t)-1 for invalid arguments. */
+size_t pa_attend_workspace_size(int num_q_heads, int num_kv_heads, int head_dim);
+
+/* ------------------------------------------------------------------------- *
  * Cache writes.                                                              *
  * ------------------------------------------------------------------------- */
 

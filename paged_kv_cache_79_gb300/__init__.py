@@ -10,6 +10,7 @@ calls on tensors that are not CUDA tensors raise.
     pa_decode_plan /        the balanced split's CTA starts computed on the host, and
       pa_decode_planned       the decode (and append) that starts from them
     pa_decode_shared        decode reading each shared prefix block once per group
+    pa_attend               several query tokens a sequence: prompts' chunks, cross attention
     pa_reshape_and_cache    write new tokens' K/V rows through a slot mapping
     pa_copy_blocks          copy-on-write block copies
     pa_swap_blocks          block moves between the device pool and pinned host memory
@@ -683,7 +684,7 @@ class _Torch:
 
     def __init__(self):
         import torch
-        self.int32, self.int64, self.uint8 = torch.int32, torch.int64, torch.uint8
+        self.int32, self.int64, self.uint8, self.float32 = torch.int32, torch.int64, torch.uint8, torch.float32
         self.codes = {torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16}
         self.device = torch.cuda.device
         self.current_device = torch._C._cuda_getDevice
@@ -966,6 +967,65 @@ def pa_fork_tables(block_tables_out, context_lens_out, block_tables, context_len
 
 
 # ----------------------------------------------------------------------------
+# attention of several query tokens per sequence
+# ----------------------------------------------------------------------------
+def pa_attend_workspace_size(num_q_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    """Bytes of workspace pa_attend needs on the current device, whatever the lengths."""
+    n = _load().pa_attend_workspace_size(num_q_heads, num_kv_heads, head_dim)
+    if n == ctypes.c_size_t(-1).value:
+        raise PagedKVError(PA_ERR_INVALID, "pa_attend_workspace_size")
+    return n
+
+
+_ATTEND_NAMES = ("out", "k_cache", "v_cache", "block_tables", "context_lens", "query_start", "lse")
+
+
+def pa_attend(out, q, k_cache, v_cache, block_tables, context_lens, query_start, scale: float, num_q_heads: int,
+              num_kv_heads: int, head_dim: int, block_size: int, causal: bool = False, lse=None, workspace=None,
+              stream=None):
+    """out[N, Hq, d] <- attention of sequence s's query tokens, rows query_start[s] .. of q
+    (query_start int32 [S + 1]), over its paged keys: all of them, or with `causal` those up
+    to the token's own, the query tokens being the last of the context (see pa_attend in
+    include/pagedkv.h).  q's rows may be strided; lse: float32 [N, Hq] for the rows'
+    log-sum-exp, or None; workspace: uint8 CUDA tensor or None (allocated here)."""
+    T = _torch()
+    n = q.shape[0]
+    q_stride = _rows(q, "q", n, head_dim)
+    _want(q.shape[1] == num_q_heads and out.shape == q.shape, "q and out must be [N, Hq, d]")
+    _want(k_cache.dim() == 4 and k_cache.shape == v_cache.shape and
+          k_cache.shape[1:] == (block_size, num_kv_heads, head_dim), "the caches must be [num_blocks, B, Hkv, d]")
+    if not out.dtype == q.dtype == k_cache.dtype == v_cache.dtype:
+        raise TypeError("out, q, k_cache and v_cache must have one dtype")
+    if not block_tables.dtype == context_lens.dtype == query_start.dtype == T.int32:
+        raise TypeError("block_tables, context_lens and query_start must be int32")
+    _want(block_tables.dim() == 2, "block_tables must be [S, W]")
+    S, W = block_tables.shape
+    _want(context_lens.shape == (S,) and query_start.shape == (S + 1,),
+          "context_lens must be [S] and query_start [S + 1]")
+    _check_counts(n | S | W | k_cache.shape[0])
+    tensors = (out, k_cache, v_cache, block_tables, context_lens, query_start)
+    if lse is not None:
+        if lse.dtype != T.float32:
+            raise TypeError("lse must be float32")
+        _want(lse.shape == (n, num_q_heads), "lse must be [N, Hq]")
+        tensors += (lse,)
+    dev, device = _on_device(_ATTEND_NAMES, tensors)
+    _want(q.get_device() == dev, "q must be on the device of out")
+    if workspace is None:
+        with device or contextlib.nullcontext():
+            workspace = _launch_scratch(pa_attend_workspace_size(num_q_heads, num_kv_heads, head_dim), q.device,
+                                        stream)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on the device of q")
+    _call("pa_attend", device, out.data_ptr(), None if lse is None else lse.data_ptr(), q.data_ptr(), q_stride,
+          k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), W, context_lens.data_ptr(),
+          query_start.data_ptr(), S, n, k_cache.shape[0], float(scale), int(causal), num_q_heads, num_kv_heads,
+          head_dim, block_size, _code(q), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+          _raw_stream(stream, dev))
+    return out
+
+
+# ----------------------------------------------------------------------------
 # rotary positions
 # ----------------------------------------------------------------------------
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
@@ -1068,7 +1128,7 @@ __all__ = ["pa_decode", "pa_decode_append", "pa_decode_plan_bytes", "pa_decode_p
            "pa_reshape_and_cache", "pa_copy_blocks", "pa_swap_blocks", "pa_gather_blocks",
            "pa_scatter_blocks", "pa_q8_block_bytes", "alloc_q8_cache", "q8_views", "pa_q8_append", "pa_q8_decode",
            "pa_q8_decode_workspace_size", "pa_q8_copy_blocks", "pa_q8_swap_blocks", "pa_build_tables",
-           "pa_fork_tables", "rope_frequencies", "ROPE_SCALINGS", "pa_rope", "pa_rope_append",
+           "pa_attend", "pa_attend_workspace_size", "pa_fork_tables", "rope_frequencies", "ROPE_SCALINGS", "pa_rope", "pa_rope_append",
            "pa_kv_transfer_worthwhile", "pa_device_errors", "pa_set_wait_limit_ns",
            "PA_DEVERR_TIMEOUT_FULL", "PA_DEVERR_TIMEOUT_EMPTY", "PA_DEVERR_SHARE", "PA_WAIT_LIMIT_DEFAULT_NS", "pa_status_string",
            "BlockAllocator", "PagedKVError", "OutOfBlocks", "library_path"]

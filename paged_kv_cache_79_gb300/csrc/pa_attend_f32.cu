@@ -1,0 +1,380 @@
+// pa_attend for fp32: mma.sync with each operand in two tf32 terms.
+//
+// Tensor cores take fp32 operands as tf32 (11 significant bits).  x = hi + lo with hi its first
+// 11 bits and lo the rest leaves a product as hi hi' + hi lo' + lo hi', off by 2^-21 of itself
+// at most, accumulated in fp32: three instructions per product, and the result as good as
+// fp32 sums of that length are.  (tcgen05 takes both operands from shared memory or TMEM as
+// they are, so the split would have to be written there first, four tiles for each one.)
+//
+// A CTA's four warps hold 16 rows each of a tile of 64 rows, and step through tiles of 32 keys
+// in two buffers, the next one's copies in flight while this one is multiplied.  Scores
+// stay in registers: the fragment that Q K^T leaves becomes P's when a step of 8 keys is taken
+// in the order 0 2 4 6 1 3 5 7, which only means reading V's rows in that order.
+#include "pa_attend.cuh"
+
+namespace pagedkv {
+
+namespace {
+
+constexpr int kF32Threads = 128;
+constexpr int kF32Rows = kF32TileRows;
+constexpr int kF32Keys = 32;
+
+__device__ __forceinline__ void split(float x, uint32_t &hi, uint32_t &lo)
+{
+    hi = __float_as_uint(x) & 0xffffe000u;
+    const float d = x - __uint_as_float(hi);
+    // (infinities and NaN have no rest)
+    lo = (hi & 0x7f800000u) == 0x7f800000u ? 0u : __float_as_uint(d);
+    if ((hi & 0x7f800000u) == 0x7f800000u)
+        hi = __float_as_uint(x);
+}
+
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
+        " {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_3(float (&c)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4], float b0,
+                                      float b1)
+{
+    uint32_t h0, l0, h1, l1;
+    split(b0, h0, l0);
+    split(b1, h1, l1);
+    mma_tf32(c, al, h0, h1);
+    mma_tf32(c, ah, l0, l1);
+    mma_tf32(c, ah, h0, h1);
+}
+
+// 16 bytes to shared memory, or zeros where the source is not there (src_bytes 0).
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0)
+                 : "memory");
+}
+
+template <int D>
+struct SmemF32 {
+    static constexpr int kStride = D + 4;  // floats; rows 4 banks apart
+    float q[kF32Rows * kStride];
+    float k[2][kF32Keys * kStride];
+    float v[2][kF32Keys * kStride];
+    long long scratch[kF32Threads / 32 + 4];
+};
+
+// Four elements as fp32 into shared memory: an asynchronous copy, or with a conversion.
+template <typename T>
+__device__ __forceinline__ void load4(float *dst, const T *src, bool there)
+{
+    if constexpr (sizeof(T) == 4) {
+        cp_async16_or_zero(dev::smem_addr(dst), src, there);
+    } else {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (there) {
+            const uint2 w = *reinterpret_cast<const uint2 *>(src);
+            const T *t = reinterpret_cast<const T *>(&w);
+            x = make_float4((float)t[0], (float)t[1], (float)t[2], (float)t[3]);
+        }
+        *reinterpret_cast<float4 *>(dst) = x;
+    }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kF32Threads) attend_f32_kernel(const __grid_constant__ AttendParams p)
+{
+    using Walk = AttendWalk<kF32Keys>;
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    SmemF32<D> &sm = *reinterpret_cast<SmemF32<D> *>(smem_raw);
+    constexpr int kStride = SmemF32<D>::kStride;
+    constexpr int kVecs = D / 4;
+    dev::grid_dependency_wait();
+    dev::grid_launch_dependents();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, c4 = lane & 3;
+    Walk walk(p);
+    if (!walk.begin<kF32Threads>(sm.scratch))
+        return;
+    do {
+        int a, b;
+        if (!walk.part(a, b))
+            continue;
+        const AttendItem &it = walk.it;
+        const auto rows = Walk::rows_of(p, it);
+        const int num = rows.tokens * p.heads_per_item;
+        const int32_t *table = p.block_tables + (size_t)it.s * p.max_blocks;
+
+        auto load_kv = [&](int tile, int buf) {
+            for (int i = tid; i < kF32Keys * kVecs; i += kF32Threads) {
+                const int r = i / kVecs, x = i % kVecs;
+                const int key = tile * kF32Keys + r;
+                const int id = key < it.seen ? table[key / p.block_size] : -1;
+                const bool there = id >= 0 && id < p.num_blocks;
+                const size_t at =
+                    there ? (((size_t)id * p.block_size + key % p.block_size) * p.num_kv_heads + rows.kv) * D + x * 4 : 0;
+                load4(&sm.k[buf][r * kStride + x * 4], static_cast<const T *>(p.k_cache) + at, there);
+                load4(&sm.v[buf][r * kStride + x * 4], static_cast<const T *>(p.v_cache) + at, there);
+            }
+        };
+        __syncthreads();  // the previous item's tiles have been read
+        for (int i = tid; i < kF32Rows * kVecs; i += kF32Threads) {
+            const int r = i / kVecs, x = i % kVecs;
+            const int tok = r / p.heads_per_item, head = r - tok * p.heads_per_item;
+            const bool there = r < num && head < rows.heads;
+            const T *src = static_cast<const T *>(p.q) +
+                           (there ? (rows.token0 + tok) * p.q_stride + (size_t)(rows.head0 + head) * D + x * 4 : 0);
+            load4(&sm.q[r * kStride + x * 4], src, there);
+        }
+        if (b > a)
+            load_kv(a, 0);
+        dev::cp_async_commit();
+
+        // this thread's rows: r0 = 16 warp + g, and r0 + 8
+        int limit[2];  // keys that the row sees
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int tok = (16 * warp + g + 8 * h) / p.heads_per_item;
+            const long long last = (long long)it.T - it.n + it.j * (long long)p.tokens_per_item + tok + 1;
+            limit[h] = p.causal ? (int)min(max(last, 0ll), (long long)it.T) : it.T;
+        }
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        float o[D / 8][4] = {};
+        for (int tile = a; tile < b; ++tile) {
+            const int buf = (tile - a) & 1;
+            dev::cp_async_wait_all();
+            __syncthreads();  // this tile's copies are there, the other buffer has been read
+            if (tile + 1 < b)
+                load_kv(tile + 1, buf ^ 1);
+            dev::cp_async_commit();
+            float s[kF32Keys / 8][4] = {};
+#pragma unroll
+            for (int k0 = 0; k0 < D; k0 += 8) {
+                uint32_t ah[4], al[4];
+                const float *qr = &sm.q[(16 * warp + g) * kStride + k0 + c4];
+                split(qr[0], ah[0], al[0]);
+                split(qr[8 * kStride], ah[1], al[1]);
+                split(qr[4], ah[2], al[2]);
+                split(qr[8 * kStride + 4], ah[3], al[3]);
+#pragma unroll
+                for (int n = 0; n < kF32Keys / 8; ++n) {
+                    const float *kr = &sm.k[buf][(8 * n + g) * kStride + k0 + c4];
+                    mma_3(s[n], ah, al, kr[0], kr[4]);
+                }
+            }
+            const int key0 = tile * kF32Keys + 2 * c4;
+            float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int n = 0; n < kF32Keys / 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const bool seen = key0 + 8 * n + (e & 1) < limit[e >> 1];
+                    s[n][e] = seen ? s[n][e] * p.scale_log2 : -INFINITY;
+                    // (fmaxf passes a NaN over; the sum does not)
+                    top[e >> 1] = fmaxf(top[e >> 1], s[n][e]);
+                }
+            float scale[2], base[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
+                top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
+                const float now = fmaxf(m[h], top[h]);
+                base[h] = now == -INFINITY ? 0.f : now;
+                scale[h] = exp2f(m[h] - base[h]);
+                m[h] = now;
+                l[h] *= scale[h];
+            }
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    o[n][e] *= scale[e >> 1];
+#pragma unroll
+            for (int n = 0; n < kF32Keys / 8; ++n) {
+                float e[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    e[i] = exp2f(s[n][i] - base[i >> 1]);
+                    l[i >> 1] += e[i];
+                }
+                // keys 2 c4 and 2 c4 + 1 of the step stand at its places c4 and c4 + 4
+                uint32_t ah[4], al[4];
+                split(e[0], ah[0], al[0]);
+                split(e[2], ah[1], al[1]);
+                split(e[1], ah[2], al[2]);
+                split(e[3], ah[3], al[3]);
+                const float *vr = &sm.v[buf][(8 * n + 2 * c4) * kStride + g];
+#pragma unroll
+                for (int d = 0; d < D / 8; ++d)
+                    mma_3(o[d], ah, al, vr[8 * d], vr[8 * d + kStride]);
+            }
+        }
+        dev::cp_async_wait_all();
+        const bool whole = a == 0 && b == it.tiles;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+            const int r = 16 * warp + g + 8 * h;
+            const int tok = r / p.heads_per_item, head = r - tok * p.heads_per_item;
+            if (r >= num || head >= rows.heads)
+                continue;
+            if (whole) {
+                const size_t row = (size_t)(rows.token0 + tok) * p.num_q_heads + rows.head0 + head;
+                const float inv = l[h] == 0.f ? 0.f : 1.f / l[h];
+                T *dst = static_cast<T *>(p.out) + row * D + 2 * c4;
+#pragma unroll
+                for (int d = 0; d < D / 8; ++d) {
+                    dst[8 * d] = dev::from_float<T>(o[d][2 * h] * inv);
+                    dst[8 * d + 1] = dev::from_float<T>(o[d][2 * h + 1] * inv);
+                }
+                if (p.lse && c4 == 0)
+                    p.lse[row] = l[h] == 0.f ? -INFINITY : (m[h] + log2f(l[h])) * 0.6931471805599453f;
+            } else {
+                const size_t row = attend_part_row(p, blockIdx.x, a > 0 ? 0 : 1) + r;
+                if (c4 == 0)
+                    p.part_ml[row] = make_float2(m[h], l[h]);
+                float *dst = p.part_o + row * D + 2 * c4;
+#pragma unroll
+                for (int d = 0; d < D / 8; ++d)
+                    *reinterpret_cast<float2 *>(dst + 8 * d) = make_float2(o[d][2 * h], o[d][2 * h + 1]);
+            }
+        }
+    } while (walk.next() && walk.inside());
+}
+
+template <typename T, int D>
+cudaError_t launch_d(const AttendLaunch &L, cudaStream_t stream)
+{
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess)
+        return e;
+    const size_t smem = sizeof(SmemF32<D>);
+    if (cached_occupancy(reinterpret_cast<void *>(attend_f32_kernel<T, D>), device, smem, smem, kF32Threads) <= 0)
+        return cudaErrorInvalidConfiguration;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)L.ctas);
+    cfg.blockDim = dim3(kF32Threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, attend_f32_kernel<T, D>, L.p);
+    return e;
+}
+
+// ---- the merge of cut items --------------------------------------------------------
+constexpr int kMergeWarps = 4;
+constexpr int kMergeRows = 16;  // rows per CTA
+
+// CTA (c, y): rows [y kMergeRows, ..) of the item that CTA c + 1 of the attention cut first.
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kMergeWarps) attend_merge_kernel(const __grid_constant__ AttendParams p)
+{
+    constexpr int kE = D / 32;
+    dev::grid_dependency_wait();
+    dev::grid_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int cta = blockIdx.x + 1;
+    const AttendCut c = p.cuts[cta];
+    const int num = c.parts > 0 ? c.tokens * p.heads_per_item : 0;
+    for (int r = blockIdx.y * kMergeRows + warp; r < min(num, (int)(blockIdx.y + 1) * kMergeRows); r += kMergeWarps) {
+        const int tok = r / p.heads_per_item, head = r - tok * p.heads_per_item;
+        if (head >= c.heads)
+            continue;
+        // part 0 is the second slot of the CTA before, the others the first slots from `cta` on
+        auto row_of = [&](int part) {
+            return part == 0 ? attend_part_row(p, cta - 1, 1) + r : attend_part_row(p, cta + part - 1, 0) + r;
+        };
+        float m = -INFINITY;
+        for (int i = lane; i < c.parts; i += 32)
+            m = fmaxf(m, p.part_ml[row_of(i)].x);
+        m = dev::warp_max(m);
+        const float base = m == -INFINITY ? 0.f : m;
+        float l = 0.f, o[kE] = {};
+#pragma unroll 4
+        for (int i = 0; i < c.parts; ++i) {
+            const size_t row = row_of(i);
+            const float2 ml = p.part_ml[row];
+            const float w = exp2f(ml.x - base);
+            l += w * ml.y;
+            const float *src = p.part_o + row * D + lane * kE;
+            if constexpr (kE == 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(src);
+                o[0] += w * x.x;
+                o[1] += w * x.y;
+                o[2] += w * x.z;
+                o[3] += w * x.w;
+            } else {
+                const float2 x = *reinterpret_cast<const float2 *>(src);
+                o[0] += w * x.x;
+                o[1] += w * x.y;
+            }
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const size_t row = (size_t)(c.token0 + tok) * p.num_q_heads + c.head0 + head;
+        T *dst = static_cast<T *>(p.out) + row * D + lane * kE;
+        T x[kE];
+#pragma unroll
+        for (int e = 0; e < kE; ++e)
+            x[e] = dev::from_float<T>(o[e] * inv);
+        if constexpr (sizeof(x) == 16)
+            *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<const uint4 *>(x);
+        else if constexpr (sizeof(x) == 8)
+            *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<const uint2 *>(x);
+        else
+            *reinterpret_cast<uint32_t *>(dst) = *reinterpret_cast<const uint32_t *>(x);
+        if (p.lse && lane == 0)
+            p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    }
+}
+
+template <typename T, int D>
+cudaError_t launch_merge_d(const AttendLaunch &L, cudaStream_t stream)
+{
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(L.ctas - 1), (unsigned)((L.p.part_rows + kMergeRows - 1) / kMergeRows));
+    cfg.blockDim = dim3(32 * kMergeWarps);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attend_merge_kernel<T, D>, L.p);
+}
+
+}  // namespace
+
+cudaError_t launch_attend_f32(const AttendLaunch &L, cudaStream_t stream)
+{
+    return L.head_dim == 64 ? launch_d<float, 64>(L, stream) : launch_d<float, 128>(L, stream);
+}
+cudaError_t launch_attend_f16(const AttendLaunch &L, cudaStream_t stream)
+{
+    return L.head_dim == 64 ? launch_d<__half, 64>(L, stream) : launch_d<__half, 128>(L, stream);
+}
+cudaError_t launch_attend_bf16(const AttendLaunch &L, cudaStream_t stream)
+{
+    return L.head_dim == 64 ? launch_d<__nv_bfloat16, 64>(L, stream) : launch_d<__nv_bfloat16, 128>(L, stream);
+}
+
+cudaError_t launch_attend_merge(const AttendLaunch &L, int dtype, cudaStream_t stream)
+{
+    if (L.ctas < 2)
+        return cudaSuccess;
+    const bool narrow = L.head_dim == 64;
+    if (dtype == PA_F32)
+        return narrow ? launch_merge_d<float, 64>(L, stream) : launch_merge_d<float, 128>(L, stream);
+    if (dtype == PA_F16)
+        return narrow ? launch_merge_d<__half, 64>(L, stream) : launch_merge_d<__half, 128>(L, stream);
+    return narrow ? launch_merge_d<__nv_bfloat16, 64>(L, stream) : launch_merge_d<__nv_bfloat16, 128>(L, stream);
+}
+
+}  // namespace pagedkv
