@@ -29,6 +29,45 @@ Workspace workspace_of(int ctas, int part_rows, int head_dim)
     return w;
 }
 
+CUtensorMapDataType type_of(int dtype)
+{
+    return dtype == PA_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+}
+
+// A 16-bit cache [num_blocks][B][Hkv][d] as (64 elements, token slot, column of 64, kv head); a
+// box is one column of a block's rows of one kv head: B rows of 128 bytes, 128-byte swizzle.
+// (A box of both columns would put them B rows apart; a tile of keys wants them 128 rows apart.)
+bool make_blocks_map(CUtensorMap *map, const void *cache, int num_blocks, int B, int Hkv, int D, int dtype)
+{
+    const EncodeTiledFn enc = encode_fn();
+    if (!enc)
+        return false;
+    const cuuint64_t dims[4] = {64, (cuuint64_t)num_blocks * B, (cuuint64_t)D / 64, (cuuint64_t)Hkv};
+    const cuuint64_t strides[3] = {(cuuint64_t)Hkv * D * 2, 128, (cuuint64_t)D * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)B, 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(map, type_of(dtype), 4, const_cast<void *>(cache), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows of queries as (64 elements, head, token, column of 64); a box is one column of `heads`
+// heads of `tokens` tokens: a row tile's rows in their order.
+bool make_rows_map(CUtensorMap *map, const void *q, long long stride, int num_tokens, int Hq, int D, int heads,
+                   int tokens, int dtype)
+{
+    const EncodeTiledFn enc = encode_fn();
+    if (!enc)
+        return false;
+    const cuuint64_t dims[4] = {64, (cuuint64_t)Hq, (cuuint64_t)num_tokens, (cuuint64_t)D / 64};
+    const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2, 128};
+    const cuuint32_t box[4] = {64, (cuuint32_t)heads, (cuuint32_t)tokens, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(map, type_of(dtype), 4, const_cast<void *>(q), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 
 extern "C" {
@@ -111,14 +150,22 @@ pa_status pa_attend(void *out, float *lse, const void *q, long long q_stride, co
     p.wait_ns = wait_limit_ns();
     L.head_dim = head_dim;
     L.sms = sms;
-    // a tile of kF32TileRows rows, two CTAs per SM: half the rows of the workspace's slots
-    const int tile = kF32TileRows;
+    // fp32: items of kF32TileRows rows, two CTAs per SM; fp16 and bf16: two tiles of 128 rows, one
+    // CTA per SM.  Either way at most two slots of kAttendRows rows per SM.
+    const bool f32 = dtype == PA_F32;
+    const int tile = f32 ? kF32TileRows : kAttendRows / 2;
     p.heads_per_item = p.group < tile ? p.group : tile;
     p.head_chunks = (p.group + p.heads_per_item - 1) / p.heads_per_item;
     p.units = num_kv_heads * p.head_chunks;
-    p.tokens_per_item = tile / p.heads_per_item;
-    p.part_rows = tile;
-    L.ctas = 2 * sms;
+    p.tokens_per_item = tile / p.heads_per_item * (f32 ? 1 : 2);
+    p.part_rows = f32 ? kF32TileRows : kAttendRows;
+    L.ctas = f32 ? 2 * sms : sms;
+    if (!f32 &&
+        (!make_rows_map(&L.map_q, q, p.q_stride, num_tokens, num_q_heads, head_dim, p.heads_per_item,
+                        p.tokens_per_item / 2, dtype) ||
+         !make_blocks_map(&L.map_k, k_cache, num_blocks, block_size, num_kv_heads, head_dim, dtype) ||
+         !make_blocks_map(&L.map_v, v_cache, num_blocks, block_size, num_kv_heads, head_dim, dtype)))
+        return cuda_fail(cudaErrorInvalidValue);
     const Workspace w = workspace_of(L.ctas, p.part_rows, head_dim);
     char *const ws = static_cast<char *>(workspace);
     p.cuts = reinterpret_cast<AttendCut *>(ws);

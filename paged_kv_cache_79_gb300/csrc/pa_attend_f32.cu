@@ -1,9 +1,8 @@
 // pa_attend for fp32: mma.sync with each operand in two tf32 terms.
 //
-// Tensor cores take fp32 operands as tf32 (11 significant bits).  x = hi + lo with hi its first
-// 11 bits and lo the rest leaves a product as hi hi' + hi lo' + lo hi', off by 2^-21 of itself
-// at most, accumulated in fp32: three instructions per product, and the result as good as
-// fp32 sums of that length are.  (tcgen05 takes both operands from shared memory or TMEM as
+// Tensor cores take fp32 operands as tf32 (11 significant bits).  x = hi + lo, both rounded to
+// that, leaves a product as hi hi' + hi lo' + lo hi', off by 2^-22 of itself at most,
+// accumulated in fp32: three instructions per product.  (tcgen05 takes both operands from shared memory or TMEM as
 // they are, so the split would have to be written there first, four tiles for each one.)
 //
 // A CTA's four warps hold 16 rows each of a tile of 64 rows, and step through tiles of 32 keys
@@ -22,12 +21,15 @@ constexpr int kF32Keys = 32;
 
 __device__ __forceinline__ void split(float x, uint32_t &hi, uint32_t &lo)
 {
-    hi = __float_as_uint(x) & 0xffffe000u;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
     const float d = x - __uint_as_float(hi);
-    // (infinities and NaN have no rest)
-    lo = (hi & 0x7f800000u) == 0x7f800000u ? 0u : __float_as_uint(d);
-    if ((hi & 0x7f800000u) == 0x7f800000u)
+    // (infinities and NaN have no rest, and values at the type's end may round to infinity)
+    if ((hi & 0x7f800000u) == 0x7f800000u) {
         hi = __float_as_uint(x);
+        lo = 0u;
+    } else {
+        asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(d));
+    }
 }
 
 __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
@@ -66,24 +68,7 @@ struct SmemF32 {
     long long scratch[kF32Threads / 32 + 4];
 };
 
-// Four elements as fp32 into shared memory: an asynchronous copy, or with a conversion.
-template <typename T>
-__device__ __forceinline__ void load4(float *dst, const T *src, bool there)
-{
-    if constexpr (sizeof(T) == 4) {
-        cp_async16_or_zero(dev::smem_addr(dst), src, there);
-    } else {
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (there) {
-            const uint2 w = *reinterpret_cast<const uint2 *>(src);
-            const T *t = reinterpret_cast<const T *>(&w);
-            x = make_float4((float)t[0], (float)t[1], (float)t[2], (float)t[3]);
-        }
-        *reinterpret_cast<float4 *>(dst) = x;
-    }
-}
-
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kF32Threads) attend_f32_kernel(const __grid_constant__ AttendParams p)
 {
     using Walk = AttendWalk<kF32Keys>;
@@ -115,8 +100,10 @@ __global__ void __launch_bounds__(kF32Threads) attend_f32_kernel(const __grid_co
                 const bool there = id >= 0 && id < p.num_blocks;
                 const size_t at =
                     there ? (((size_t)id * p.block_size + key % p.block_size) * p.num_kv_heads + rows.kv) * D + x * 4 : 0;
-                load4(&sm.k[buf][r * kStride + x * 4], static_cast<const T *>(p.k_cache) + at, there);
-                load4(&sm.v[buf][r * kStride + x * 4], static_cast<const T *>(p.v_cache) + at, there);
+                cp_async16_or_zero(dev::smem_addr(&sm.k[buf][r * kStride + x * 4]),
+                                   static_cast<const float *>(p.k_cache) + at, there);
+                cp_async16_or_zero(dev::smem_addr(&sm.v[buf][r * kStride + x * 4]),
+                                   static_cast<const float *>(p.v_cache) + at, there);
             }
         };
         __syncthreads();  // the previous item's tiles have been read
@@ -124,9 +111,9 @@ __global__ void __launch_bounds__(kF32Threads) attend_f32_kernel(const __grid_co
             const int r = i / kVecs, x = i % kVecs;
             const int tok = r / p.heads_per_item, head = r - tok * p.heads_per_item;
             const bool there = r < num && head < rows.heads;
-            const T *src = static_cast<const T *>(p.q) +
-                           (there ? (rows.token0 + tok) * p.q_stride + (size_t)(rows.head0 + head) * D + x * 4 : 0);
-            load4(&sm.q[r * kStride + x * 4], src, there);
+            const float *src = static_cast<const float *>(p.q) +
+                               (there ? (rows.token0 + tok) * p.q_stride + (size_t)(rows.head0 + head) * D + x * 4 : 0);
+            cp_async16_or_zero(dev::smem_addr(&sm.q[r * kStride + x * 4]), src, there);
         }
         if (b > a)
             load_kv(a, 0);
@@ -186,11 +173,7 @@ __global__ void __launch_bounds__(kF32Threads) attend_f32_kernel(const __grid_co
                 m[h] = now;
                 l[h] *= scale[h];
             }
-#pragma unroll
-            for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    o[n][e] *= scale[e >> 1];
+            uint32_t ah[kF32Keys / 8][4], al[kF32Keys / 8][4];
 #pragma unroll
             for (int n = 0; n < kF32Keys / 8; ++n) {
                 float e[4];
@@ -200,15 +183,24 @@ __global__ void __launch_bounds__(kF32Threads) attend_f32_kernel(const __grid_co
                     l[i >> 1] += e[i];
                 }
                 // keys 2 c4 and 2 c4 + 1 of the step stand at its places c4 and c4 + 4
-                uint32_t ah[4], al[4];
-                split(e[0], ah[0], al[0]);
-                split(e[2], ah[1], al[1]);
-                split(e[1], ah[2], al[2]);
-                split(e[3], ah[3], al[3]);
-                const float *vr = &sm.v[buf][(8 * n + 2 * c4) * kStride + g];
+                split(e[0], ah[n][0], al[n][0]);
+                split(e[2], ah[n][1], al[n][1]);
+                split(e[1], ah[n][2], al[n][2]);
+                split(e[3], ah[n][3], al[n][3]);
+            }
+            // The tile's share of the output is summed by itself: the tensor core's additions cut
+            // low bits off, which over a long context leans one way; the addition here rounds.
 #pragma unroll
-                for (int d = 0; d < D / 8; ++d)
-                    mma_3(o[d], ah, al, vr[8 * d], vr[8 * d + kStride]);
+            for (int d = 0; d < D / 8; ++d) {
+                float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int n = 0; n < kF32Keys / 8; ++n) {
+                    const float *vr = &sm.v[buf][(8 * n + 2 * c4) * kStride + 8 * d + g];
+                    mma_3(c, ah[n], al[n], vr[0], vr[kStride]);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    o[d][e] = fmaf(o[d][e], scale[e >> 1], c[e]);
             }
         }
         dev::cp_async_wait_all();
@@ -224,12 +216,10 @@ __global__ void __launch_bounds__(kF32Threads) attend_f32_kernel(const __grid_co
             if (whole) {
                 const size_t row = (size_t)(rows.token0 + tok) * p.num_q_heads + rows.head0 + head;
                 const float inv = l[h] == 0.f ? 0.f : 1.f / l[h];
-                T *dst = static_cast<T *>(p.out) + row * D + 2 * c4;
+                float *dst = static_cast<float *>(p.out) + row * D + 2 * c4;
 #pragma unroll
-                for (int d = 0; d < D / 8; ++d) {
-                    dst[8 * d] = dev::from_float<T>(o[d][2 * h] * inv);
-                    dst[8 * d + 1] = dev::from_float<T>(o[d][2 * h + 1] * inv);
-                }
+                for (int d = 0; d < D / 8; ++d)
+                    *reinterpret_cast<float2 *>(dst + 8 * d) = make_float2(o[d][2 * h] * inv, o[d][2 * h + 1] * inv);
                 if (p.lse && c4 == 0)
                     p.lse[row] = l[h] == 0.f ? -INFINITY : (m[h] + log2f(l[h])) * 0.6931471805599453f;
             } else {
@@ -245,7 +235,7 @@ __global__ void __launch_bounds__(kF32Threads) attend_f32_kernel(const __grid_co
     } while (walk.next() && walk.inside());
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch_d(const AttendLaunch &L, cudaStream_t stream)
 {
     int device = 0;
@@ -253,7 +243,7 @@ cudaError_t launch_d(const AttendLaunch &L, cudaStream_t stream)
     if (e != cudaSuccess)
         return e;
     const size_t smem = sizeof(SmemF32<D>);
-    if (cached_occupancy(reinterpret_cast<void *>(attend_f32_kernel<T, D>), device, smem, smem, kF32Threads) <= 0)
+    if (cached_occupancy(reinterpret_cast<void *>(attend_f32_kernel<D>), device, smem, smem, kF32Threads) <= 0)
         return cudaErrorInvalidConfiguration;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -265,7 +255,7 @@ cudaError_t launch_d(const AttendLaunch &L, cudaStream_t stream)
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, attend_f32_kernel<T, D>, L.p);
+    e = cudaLaunchKernelEx(&cfg, attend_f32_kernel<D>, L.p);
     return e;
 }
 
@@ -354,17 +344,8 @@ cudaError_t launch_merge_d(const AttendLaunch &L, cudaStream_t stream)
 
 cudaError_t launch_attend_f32(const AttendLaunch &L, cudaStream_t stream)
 {
-    return L.head_dim == 64 ? launch_d<float, 64>(L, stream) : launch_d<float, 128>(L, stream);
+    return L.head_dim == 64 ? launch_d<64>(L, stream) : launch_d<128>(L, stream);
 }
-cudaError_t launch_attend_f16(const AttendLaunch &L, cudaStream_t stream)
-{
-    return L.head_dim == 64 ? launch_d<__half, 64>(L, stream) : launch_d<__half, 128>(L, stream);
-}
-cudaError_t launch_attend_bf16(const AttendLaunch &L, cudaStream_t stream)
-{
-    return L.head_dim == 64 ? launch_d<__nv_bfloat16, 64>(L, stream) : launch_d<__nv_bfloat16, 128>(L, stream);
-}
-
 cudaError_t launch_attend_merge(const AttendLaunch &L, int dtype, cudaStream_t stream)
 {
     if (L.ctas < 2)

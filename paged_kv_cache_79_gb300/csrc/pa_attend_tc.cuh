@@ -1,0 +1,551 @@
+// pa_attend for fp16 and bf16: tcgen05 with accumulators in TMEM.
+//
+// An item has two tiles of 128 rows (rows: query tokens times heads of a group) that step
+// through the same keys, 128 at a time.  Per CTA, one per SM:
+//   warp 8       loader: per tile of keys one TMA copy for each cache block and 128-byte
+//                column of K, then of V, into a ring; Q's rows with TMA too.  The rows
+//                behind the last key that an item sees are zeros in V (a weight of 0 times what
+//                a stale row holds would be NaN where that is NaN);
+//   warp 9       products, issued by one thread: S = Q K^T into TMEM (operands in shared
+//                memory), O += P V with P read from TMEM;
+//   (warps 10 and 11 only fill up their warpgroup, which hands its registers on)
+//   warps 0..3   softmax of the first row tile, warps 4..7 of the second: a thread has a row.
+//                It reads its 128 scores from TMEM, writes its probabilities over them as
+//                fp16/bf16, and keeps the row's maximum and sum.
+// While one row tile's scores are in its softmax, the tensor cores work on the other's.
+//
+// The running maximum need not be the true one: any base with exponents that stay in range
+// gives the same quotient.  So O (in TMEM) is only rescaled when a row's maximum has grown by
+// more than 2^8 over the base in use; the probabilities stay below 2^8, far from fp16's end.
+#pragma once
+
+#include <type_traits>
+
+#include "pa_attend.cuh"
+
+namespace pagedkv {
+namespace tc {
+
+constexpr int kThreads = 384;
+constexpr int kLoaderWarp = 8;
+constexpr int kMmaWarp = 9;
+constexpr int kTileRows = 128;
+constexpr int kKeys = 128;
+constexpr int kChunkBytes = kKeys * 128;   // 128 rows of 128 bytes: one column of a tile
+constexpr float kRescale = 8.0f;           // growth of a maximum (log2) that the base may lag by
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColO = 256;            // O of the row tiles, behind their S (128 columns each)
+
+template <int D>
+struct Smem {
+    static constexpr int kChunks = D / 64;
+    static constexpr int kTileBytes = kChunks * kChunkBytes;  // 128 rows of Q, K or V
+    static constexpr int kStages = D == 128 ? 5 : 10;
+    static constexpr int kRing = 2 * kTileBytes;              // behind the two tiles of Q
+    static constexpr int kBars = kRing + kStages * kTileBytes;
+    static constexpr int kFull = kBars, kEmpty = kFull + 8 * kStages, kQFull = kEmpty + 8 * kStages,
+                         kQEmpty = kQFull + 16, kSFull = kQEmpty + 16, kPFull = kSFull + 16, kODone = kPFull + 16,
+                         kDrain = kODone + 16, kTmem = kDrain + 8, kAbort = kTmem + 4, kScratch = kAbort + 4,
+                         kEnd = kScratch + 8 * (kThreads / 32 + 4);
+    static constexpr int kBytes = kEnd + 1024;                // slack to align the base
+    static_assert(kBytes <= 232448, "one CTA's shared memory");
+};
+
+// ---- tcgen05 -------------------------------------------------------------------------
+__device__ __forceinline__ void tmem_alloc(uint32_t slot)
+{
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc(uint32_t base)
+{
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(kTmemCols) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// `bar` is arrived at when every product issued so far by this thread has completed.
+__device__ __forceinline__ void commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// D (+)= A B, operands in shared memory; and with A in TMEM.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+// 32 columns of this warp's 32 rows, a row per lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t addr)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14,"
+        " %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14,"
+        " %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14,"
+        " %15, %16};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// Shared-memory operand: 128-byte swizzle.  Rows of 128 bytes along K (Q and K: K-major):
+// groups of 8 rows `sbo` apart.  Rows of 128 bytes along N (V): groups of 8 keys `sbo` apart,
+// the next 64 columns `lbo` on.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lbo, uint32_t sbo)
+{
+    return (uint64_t)((addr >> 4) & 0x3fff) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(sbo >> 4) << 32 | 1ull << 46 |
+           2ull << 61;
+}
+// fp32 accumulators, 16-bit operands (format 0: fp16, 1: bf16), 128 rows, n columns.
+__host__ __device__ constexpr uint32_t instruction(uint32_t format, uint32_t n, bool b_along_n)
+{
+    return 1u << 4 | format << 7 | format << 10 | (b_along_n ? 1u << 16 : 0u) | (n >> 3) << 17 |
+           (uint32_t)(kTileRows >> 4) << 24;
+}
+
+__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+template <typename T, int D, int B>
+__global__ void __launch_bounds__(kThreads, 1)
+    attend_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ CUtensorMap map_q,
+                  const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v)
+{
+    using S = Smem<D>;
+    using Walk = AttendWalk<kKeys>;
+    constexpr int kChunks = S::kChunks;
+    constexpr int kBlocks = kKeys / B;  // cache blocks per tile of keys
+    constexpr uint32_t kFormat = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t smem = (dev::smem_addr(smem_raw) + 1023u) & ~1023u;
+    unsigned char *const smem_ptr = smem_raw + (smem - dev::smem_addr(smem_raw));
+    volatile int *const abort = reinterpret_cast<volatile int *>(smem_ptr + S::kAbort);
+    auto &scratch = *reinterpret_cast<long long(*)[kThreads / 32 + 4]>(smem_ptr + S::kScratch);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    if (tid == 0) {
+        for (int i = 0; i < S::kStages; ++i) {
+            dev::mbar_init(smem + S::kFull + 8 * i, 1);
+            dev::mbar_init(smem + S::kEmpty + 8 * i, 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            dev::mbar_init(smem + S::kQFull + 8 * t, 1);
+            dev::mbar_init(smem + S::kQEmpty + 8 * t, 1);
+            dev::mbar_init(smem + S::kSFull + 8 * t, 1);
+            dev::mbar_init(smem + S::kPFull + 8 * t, kTileRows);
+            dev::mbar_init(smem + S::kODone + 8 * t, 1);
+        }
+        dev::mbar_init(smem + S::kDrain, 1);
+        *abort = 0;
+        dev::fence_mbar_init();
+    }
+    dev::grid_dependency_wait();
+    dev::grid_launch_dependents();
+    Walk walk(p);
+    if (!walk.template begin<kThreads>(scratch))
+        return;
+    if (warp == kMmaWarp)
+        tmem_alloc(smem + S::kTmem);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem_ptr + S::kTmem);
+    const int half_tokens = p.tokens_per_item / 2;  // of a row tile
+
+    // A bounded wait; false: this CTA gives up.
+    auto wait = [&](uint32_t bar, uint32_t parity, unsigned int flag) {
+        const int r = dev::mbar_wait_abortable(bar, parity, p.wait_ns, abort);
+        if (r == 0) {
+            atomicOr(p.errors, flag);
+            *abort = 1;
+        }
+        return r > 0;
+    };
+    // The same by a whole warp, all of whose lanes go on or none.
+    auto wait_all = [&](uint32_t bar, uint32_t parity, unsigned int flag) {
+        return __all_sync(0xffffffffu, wait(bar, parity, flag)) != 0;
+    };
+
+    // The softmax warps hold 128 scores a thread: 168 registers each at launch (three warps per
+    // scheduler) become 2 x 208 and 88.
+    if (warp >= kLoaderWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == kLoaderWarp) {
+            uint32_t fills = 0, q_fills[2] = {0, 0};
+            bool ok = true;
+            const uint32_t q_bytes = (uint32_t)(half_tokens * p.heads_per_item) * 128u * kChunks;
+            do {
+                int a, b;
+                if (!walk.part(a, b) || b == a)
+                    continue;
+                const AttendItem &it = walk.it;
+                const auto rows = Walk::rows_of(p, it);
+                const int tiles_q = rows.tokens > half_tokens ? 2 : 1;
+                for (int t = 0; t < tiles_q && ok; ++t) {
+                    ok = wait_all(smem + S::kQEmpty + 8 * t, (q_fills[t] & 1) ^ 1, PA_DEVERR_TIMEOUT_EMPTY);
+                    if (ok && lane == 0) {
+                        const uint32_t bar = smem + S::kQFull + 8 * t;
+                        dev::mbar_arrive_expect_tx(bar, q_bytes);
+                        for (int c = 0; c < kChunks; ++c)
+                            dev::tma_load_4d(smem + t * S::kTileBytes + c * kChunkBytes, &map_q, 0, rows.head0,
+                                             rows.token0 + t * half_tokens, c, bar);
+                    }
+                    q_fills[t] += ok;
+                }
+                const int32_t *table = p.block_tables + (size_t)it.s * p.max_blocks;
+                const int blk = lane % kBlocks, chunk = lane / kBlocks;  // this lane's copy of a tile
+                const int used = (it.seen + B - 1) / B;                  // blocks with a key that is seen
+                auto id_of = [&](int tile) {
+                    const int j = tile * kBlocks + blk;
+                    const int id = tile < b && j < used ? table[j] : -1;
+                    return id >= 0 && id < p.num_blocks ? id : p.num_blocks;  // (past the end: zeros)
+                };
+                int id = id_of(a);
+                for (int tile = a; tile < b && ok; ++tile) {
+                    const int here = id;
+                    id = id_of(tile + 1);
+                    const int full = min(max(used - tile * kBlocks, 0), kBlocks);  // blocks of this tile
+                    for (int kv = 0; kv < 2 && ok; ++kv) {
+                        const int stage = fills % S::kStages;
+                        ok = wait_all(smem + S::kEmpty + 8 * stage, ((fills / S::kStages) & 1) ^ 1, PA_DEVERR_TIMEOUT_EMPTY);
+                        if (!ok)
+                            break;
+                        ++fills;
+                        const uint32_t at = smem + S::kRing + stage * S::kTileBytes, bar = smem + S::kFull + 8 * stage;
+                        // V's rows behind the last key: the block that holds it by plain copies, zeros after it
+                        int copies = full;
+                        const int rest = it.seen - tile * kKeys;  // keys of this tile
+                        if (kv == 1 && rest < kKeys) {
+                            copies = rest / B;
+                            const int last = __shfl_sync(0xffffffffu, here, copies % 32);
+                            const int first = copies * B;
+                            for (int i = lane; i < (kKeys - first) * (D / 8); i += 32) {
+                                const int r = first + i / (D / 8), x = i % (D / 8);
+                                uint4 val = make_uint4(0, 0, 0, 0);
+                                if (r < rest && last < p.num_blocks)
+                                    val = *reinterpret_cast<const uint4 *>(
+                                        static_cast<const T *>(p.v_cache) +
+                                        (((size_t)last * B + (r - first)) * p.num_kv_heads + rows.kv) * D + x * 8);
+                                *reinterpret_cast<uint4 *>(smem_ptr + (at - smem) + (x / 8) * kChunkBytes + r * 128 +
+                                                           (((x % 8) ^ (r & 7)) << 4)) = val;
+                            }
+                            fence_async_proxy();
+                            __syncwarp();
+                        }
+                        if (lane == 0)
+                            dev::mbar_arrive_expect_tx(bar, (uint32_t)(copies * B) * 128u * kChunks);
+                        __syncwarp();
+                        if (chunk < kChunks && blk < copies)
+                            dev::tma_load_4d(at + chunk * kChunkBytes + blk * B * 128, kv == 0 ? &map_k : &map_v, 0,
+                                             here * B, chunk, rows.kv, bar);
+                        __syncwarp();
+                    }
+                }
+            } while (ok && walk.next() && walk.inside());
+            // what is in flight lands before the CTA ends
+            if (*abort) {
+                for (uint32_t i = 0; i < S::kStages && i < fills; ++i) {
+                    const uint32_t f = fills - 1 - i;
+                    dev::mbar_wait(smem + S::kFull + 8 * (f % S::kStages), (f / S::kStages) & 1, kWaitTimeoutNs);
+                }
+                for (int t = 0; t < 2; ++t)
+                    if (q_fills[t])
+                        dev::mbar_wait(smem + S::kQFull + 8 * t, (q_fills[t] - 1) & 1, kWaitTimeoutNs);
+            }
+        } else if (warp == kMmaWarp) {
+            if (lane == 0) {
+                constexpr uint32_t kScores = instruction(kFormat, kKeys, false);
+                constexpr uint32_t kOutput = instruction(kFormat, D, true);
+                uint32_t fills = 0, q_fills[2] = {0, 0}, steps[2] = {0, 0};
+                bool ok = true;
+                auto stage_at = [&](uint32_t f) { return smem + S::kRing + (f % S::kStages) * S::kTileBytes; };
+                auto full = [&](uint32_t f) {
+                    return wait(smem + S::kFull + 8 * (f % S::kStages), (f / S::kStages) & 1, PA_DEVERR_TIMEOUT_FULL);
+                };
+                auto release = [&](uint32_t f) { commit(smem + S::kEmpty + 8 * (f % S::kStages)); };
+                auto scores = [&](int t, uint32_t f) {
+    #pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t off = (k / 4) * kChunkBytes + (k % 4) * 32;
+                        mma_ss(tmem + t * kKeys, operand(smem + t * S::kTileBytes + off, 16, 1024),
+                               operand(stage_at(f) + off, 16, 1024), kScores, k > 0);
+                    }
+                    commit(smem + S::kSFull + 8 * t);
+                };
+                do {
+                    int a, b;
+                    if (!walk.part(a, b) || b == a)
+                        continue;
+                    const auto rows = Walk::rows_of(p, walk.it);
+                    const int tiles_q = rows.tokens > half_tokens ? 2 : 1;
+                    const int n = b - a;
+                    for (int j = -1; j < n && ok; ++j) {
+                        const uint32_t fv = fills + 2 * j + 1, fk = fv + 1;  // V of tile j, K of tile j + 1
+                        for (int t = 0; t < tiles_q && ok; ++t) {
+                            if (j >= 0) {
+                                ok = wait(smem + S::kPFull + 8 * t, steps[t] & 1, PA_DEVERR_TIMEOUT_FULL) &&
+                                     (t > 0 || full(fv));
+                                if (!ok)
+                                    break;
+                                ++steps[t];
+                                fence_after();
+    #pragma unroll
+                                for (int k = 0; k < kKeys / 16; ++k)
+                                    mma_ts(tmem + kColO + t * D, tmem + t * kKeys + 8 * k,
+                                           operand(stage_at(fv) + k * 2048, kChunkBytes, 1024), kOutput, j > 0 || k > 0);
+                                if (j == n - 1)
+                                    commit(smem + S::kODone + 8 * t);
+                                if (t == tiles_q - 1)
+                                    release(fv);
+                            }
+                            if (j + 1 < n) {
+                                if (j < 0) {
+                                    ok = wait(smem + S::kQFull + 8 * t, q_fills[t] & 1, PA_DEVERR_TIMEOUT_FULL);
+                                    ++q_fills[t];
+                                }
+                                ok = ok && (t > 0 || full(fk));
+                                if (!ok)
+                                    break;
+                                scores(t, fk);
+                                if (j + 2 == n)
+                                    commit(smem + S::kQEmpty + 8 * t);
+                                if (t == tiles_q - 1)
+                                    release(fk);
+                            }
+                        }
+                    }
+                    fills += 2 * n;
+                } while (ok && walk.next() && walk.inside());
+                // every product has completed before the CTA gives its memory back
+                commit(smem + S::kDrain);
+                dev::mbar_wait(smem + S::kDrain, 0, kWaitTimeoutNs);
+            }
+            __syncwarp();
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        const int t = warp >> 2;              // row tile
+        const int r = tid & (kTileRows - 1);  // row of it: this thread's
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+        const uint32_t s_at = tmem + lanes + t * kKeys, o_at = tmem + lanes + kColO + t * D;
+        uint32_t steps = 0, parts = 0;
+        bool ok = true;
+        const int tok = r / p.heads_per_item, head = r - tok * p.heads_per_item;
+        const bool positive = p.scale_log2 >= 0.f;
+        do {
+            int a, b;
+            if (!walk.part(a, b))
+                continue;
+            const AttendItem &it = walk.it;
+            const auto rows = Walk::rows_of(p, it);
+            if (t * half_tokens >= rows.tokens)
+                continue;
+            const int my_tok = t * half_tokens + tok;  // of the item
+            const bool mine = tok < half_tokens && my_tok < rows.tokens && head < rows.heads;
+            const size_t row = (size_t)(rows.token0 + my_tok) * p.num_q_heads + rows.head0 + head;
+            // keys that this row sees, and that every row of the tile sees
+            int limit = it.T, common = it.T;
+            if (p.causal) {
+                const long long own = (long long)it.T - it.n + it.j * (long long)p.tokens_per_item + 1;
+                limit = (int)min(max(own + my_tok, 0ll), (long long)it.T);
+                common = (int)min(max(own + t * half_tokens, 0ll), (long long)it.T);
+            }
+            float m = -INFINITY, l = 0.f;  // the base in use, the sum
+            for (int tile = a; tile < b; ++tile) {
+                ok = wait_all(smem + S::kSFull + 8 * t, steps & 1, PA_DEVERR_TIMEOUT_FULL);
+                if (!ok)
+                    break;
+                ++steps;
+                fence_after();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    tmem_ld32(s[i], s_at + 32 * i);
+                wait_ld();
+                const int key0 = tile * kKeys;
+                if (key0 + kKeys > common) {
+                    const float hidden = positive ? -INFINITY : INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 128; ++i)
+                        if (key0 + i >= limit)
+                            s[i / 32][i % 32] = __float_as_uint(hidden);
+                }
+                float top[4];
+                if (positive) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        top[i] = __uint_as_float(s[i][0]);
+#pragma unroll
+                        for (int k = 1; k < 32; ++k)
+                            top[i] = fmaxf(top[i], __uint_as_float(s[i][k]));
+                    }
+                    top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        top[i] = __uint_as_float(s[i][0]);
+#pragma unroll
+                        for (int k = 1; k < 32; ++k)
+                            top[i] = fminf(top[i], __uint_as_float(s[i][k]));
+                    }
+                    top[0] = fminf(fminf(top[0], top[1]), fminf(top[2], top[3]));
+                }
+                const bool none = top[0] == (positive ? -INFINITY : INFINITY);
+                const float now = none ? -INFINITY : top[0] * p.scale_log2;
+                if (tile == a) {
+                    m = now;
+                } else if (__any_sync(0xffffffffu, now > m + kRescale)) {
+                    // O is at rest: the scores of this tile came after the product before it
+                    const float grown = fmaxf(m, now);
+                    const float f = grown == -INFINITY ? 1.f : exp2f(m - grown);
+                    m = grown;
+                    l *= f;
+#pragma unroll
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(o, o_at + c);
+                        wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                        tmem_st32(o_at + c, o);
+                    }
+                }
+                const float base = m == -INFINITY ? 0.f : m;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float x = dev::ex2(fmaf(__uint_as_float(s[h][2 * i]), p.scale_log2, -base));
+                        const float y = dev::ex2(fmaf(__uint_as_float(s[h][2 * i + 1]), p.scale_log2, -base));
+                        sum[2 * (i & 1)] += x;
+                        sum[2 * (i & 1) + 1] += y;
+                        w[i] = dev::Mma<T>::pack(x, y);
+                    }
+                    tmem_st16(s_at + 16 * h, w);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                wait_st();
+                fence_before();
+                dev::mbar_arrive(smem + S::kPFull + 8 * t);
+            }
+            if (!ok)
+                break;
+            const bool whole = a == 0 && b == it.tiles;
+            if (b > a) {
+                ok = wait_all(smem + S::kODone + 8 * t, parts & 1, PA_DEVERR_TIMEOUT_FULL);
+                if (!ok)
+                    break;
+                ++parts;
+                fence_after();
+            }
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const size_t part = attend_part_row(p, blockIdx.x, a > 0 ? 0 : 1) + my_tok * p.heads_per_item + head;
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                if (b > a) {
+                    tmem_ld32(o, o_at + c);
+                    wait_ld();
+                }
+                if (mine && whole) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + row * D + c);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = b > a ? dev::Mma<T>::pack(__uint_as_float(o[8 * k + 2 * e]) * inv,
+                                                             __uint_as_float(o[8 * k + 2 * e + 1]) * inv)
+                                         : 0u;
+                        dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                } else if (mine) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.part_o + part * D + c);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                }
+                __syncwarp();
+            }
+            fence_before();  // O has been read before the next item's first probabilities are announced
+            if (mine && whole && p.lse)
+                p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+            if (mine && !whole)
+                p.part_ml[part] = make_float2(m, l);
+        } while (walk.next() && walk.inside());
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == kMmaWarp)
+        tmem_dealloc(tmem);
+}
+
+template <typename T, int D, int B>
+cudaError_t launch(const AttendLaunch &L, cudaStream_t stream)
+{
+    int device = 0;
+    const cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess)
+        return e;
+    const size_t smem = Smem<D>::kBytes;
+    if (cached_occupancy(reinterpret_cast<void *>(attend_kernel<T, D, B>), device, smem, smem, kThreads) <= 0)
+        return cudaErrorInvalidConfiguration;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)L.ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attend_kernel<T, D, B>, L.p, L.map_q, L.map_k, L.map_v);
+}
+
+template <typename T>
+cudaError_t launch_type(const AttendLaunch &L, cudaStream_t stream)
+{
+    if (L.head_dim == 64)
+        return L.p.block_size == 16 ? launch<T, 64, 16>(L, stream) : launch<T, 64, 32>(L, stream);
+    return L.p.block_size == 16 ? launch<T, 128, 16>(L, stream) : launch<T, 128, 32>(L, stream);
+}
+
+}  // namespace tc
+}  // namespace pagedkv
