@@ -230,7 +230,7 @@ struct AttendWalk {
             const int a = cut(share_lo);
             if (a > 0 && a < it.tiles && cut(start_of(total, cta - 1, ctas)) == 0) {
                 int last = cta;
-                while (cut(start_of(total, last + 1, ctas)) < it.tiles)
+                while (last + 1 < ctas && cut(start_of(total, last + 1, ctas)) < it.tiles)
                     ++last;
                 const AttendRows rows = rows_of(p, it);
                 cutinfo.parts = last - cta + 2;

@@ -15,8 +15,10 @@
 // While one row tile's scores are in its softmax, the tensor cores work on the other's.
 //
 // The running maximum need not be the true one: any base with exponents that stay in range
-// gives the same quotient.  So O (in TMEM) is only rescaled when a row's maximum has grown by
-// more than 2^8 over the base in use; the probabilities stay below 2^8, far from fp16's end.
+// gives the same quotient.  So a tile's probabilities are taken by the base at hand while the
+// tile's maximum is still being found, and only where a row's maximum has grown by more than
+// 2^8 over its base, O (in TMEM) is rescaled and the tile's probabilities are taken again.
+// They stay below 2^8, far from fp16's end.
 #pragma once
 
 #include <type_traits>
@@ -33,6 +35,7 @@ constexpr int kTileRows = 128;
 constexpr int kKeys = 128;
 constexpr int kChunkBytes = kKeys * 128;   // 128 rows of 128 bytes: one column of a tile
 constexpr float kRescale = 8.0f;           // growth of a maximum (log2) that the base may lag by
+constexpr float kFar = 1048576.0f;         // bases (log2) from which on products are rounded first
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;            // O of the row tiles, behind their S (128 columns each)
 
@@ -64,7 +67,6 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t base)
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // `bar` is arrived at when every product issued so far by this thread has completed.
 __device__ __forceinline__ void commit(uint32_t bar)
@@ -111,14 +113,43 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16])
+// The loads so far have arrived, among them r (named so that no use of it moves ahead).
+__device__ __forceinline__ void wait_ld(uint32_t (&r)[32])
 {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14,"
-        " %15, %16};" ::"r"(addr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                   "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                   "+r"(r[30]), "+r"(r[31])::"memory");
+}
+
+// Two fp32 operations at a time, and the larger of three.
+__device__ __forceinline__ unsigned long long bits(float2 x)
+{
+    return (unsigned long long)__float_as_uint(x.y) << 32 | __float_as_uint(x.x);
+}
+__device__ __forceinline__ float2 pair(unsigned long long x)
+{
+    return make_float2(__uint_as_float((uint32_t)x), __uint_as_float((uint32_t)(x >> 32)));
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+    return pair(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    unsigned long long d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
+    return pair(d);
+}
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
 // Shared-memory operand: 128-byte swizzle.  Rows of 128 bytes along K (Q and K: K-major):
@@ -363,7 +394,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t steps = 0, parts = 0;
         bool ok = true;
         const int tok = r / p.heads_per_item, head = r - tok * p.heads_per_item;
-        const bool positive = p.scale_log2 >= 0.f;
         do {
             int a, b;
             if (!walk.part(a, b))
@@ -383,82 +413,112 @@ __global__ void __launch_bounds__(kThreads, 1)
                 common = (int)min(max(own + t * half_tokens, 0ll), (long long)it.T);
             }
             float m = -INFINITY, l = 0.f;  // the base in use, the sum
+            bool far = false;
             for (int tile = a; tile < b; ++tile) {
                 ok = wait_all(smem + S::kSFull + 8 * t, steps & 1, PA_DEVERR_TIMEOUT_FULL);
                 if (!ok)
                     break;
                 ++steps;
                 fence_after();
-                uint32_t s[4][32];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    tmem_ld32(s[i], s_at + 32 * i);
-                wait_ld();
                 const int key0 = tile * kKeys;
-                if (key0 + kKeys > common) {
-                    const float hidden = positive ? -INFINITY : INFINITY;
+                const bool masked = key0 + kKeys > common;
+                // Exponents of 32 columns: x = s * scale - base, -inf where the key is hidden; their
+                // maximum.  `far`: the product is rounded first.  Behind a large base the exact one
+                // would differ from it by the product's rounding error, which may be large itself.
+                auto exponents = [&](const uint32_t (&s)[32], int c, float base, bool far, float2 (&x)[16], float top) {
+                    if (far) {
 #pragma unroll
-                    for (int i = 0; i < 128; ++i)
-                        if (key0 + i >= limit)
-                            s[i / 32][i % 32] = __float_as_uint(hidden);
-                }
-                float top[4];
-                if (positive) {
+                        for (int i = 0; i < 16; ++i)
+                            x[i] = make_float2(__fadd_rn(__fmul_rn(__uint_as_float(s[2 * i]), p.scale_log2), -base),
+                                               __fadd_rn(__fmul_rn(__uint_as_float(s[2 * i + 1]), p.scale_log2), -base));
+                    } else {
+                        const float2 scale2 = make_float2(p.scale_log2, p.scale_log2), base2 = make_float2(-base, -base);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        top[i] = __uint_as_float(s[i][0]);
-#pragma unroll
-                        for (int k = 1; k < 32; ++k)
-                            top[i] = fmaxf(top[i], __uint_as_float(s[i][k]));
+                        for (int i = 0; i < 16; ++i)
+                            x[i] = fma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), scale2, base2);
                     }
-                    top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                } else {
+                    if (masked) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        top[i] = __uint_as_float(s[i][0]);
-#pragma unroll
-                        for (int k = 1; k < 32; ++k)
-                            top[i] = fminf(top[i], __uint_as_float(s[i][k]));
+                        for (int i = 0; i < 16; ++i) {
+                            x[i].x = key0 + 32 * c + 2 * i < limit ? x[i].x : -INFINITY;
+                            x[i].y = key0 + 32 * c + 2 * i + 1 < limit ? x[i].y : -INFINITY;
+                        }
                     }
-                    top[0] = fminf(fminf(top[0], top[1]), fminf(top[2], top[3]));
-                }
-                const bool none = top[0] == (positive ? -INFINITY : INFINITY);
-                const float now = none ? -INFINITY : top[0] * p.scale_log2;
-                if (tile == a) {
-                    m = now;
-                } else if (__any_sync(0xffffffffu, now > m + kRescale)) {
+                    float top2 = x[0].x;
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        top = max3(top, x[i].x, x[i].y);
+                        top2 = max3(top2, x[i + 1].x, x[i + 1].y);
+                    }
+                    return fmaxf(top, top2);
+                };
+                // The base becomes the row's maximum, this tile's included.
+                auto raise = [&]() {
+                    float top = m;
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t s[32];
+                        float2 x[16];
+                        tmem_ld32(s, s_at + 32 * c);
+                        wait_ld(s);
+                        top = exponents(s, c, 0.f, true, x, top);
+                    }
+                    const float f = top == -INFINITY ? 1.f : exp2f(m - top);
+                    m = top;
+                    far = __any_sync(0xffffffffu, fabsf(m) > kFar && m != -INFINITY);
+                    return f;
+                };
+                if (tile == a)
+                    raise();
+                // The probabilities by the base at hand; where that has fallen behind, once more.
+                uint32_t w[64];
+#pragma unroll 1
+                for (int pass = 0; pass < 2; ++pass) {
+                    const float base = m == -INFINITY ? 0.f : m;
+                    float top = -INFINITY;
+                    float2 sum = make_float2(0.f, 0.f), sum2 = sum;
+                    uint32_t s[2][32];
+                    tmem_ld32(s[0], s_at);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        wait_ld(s[c & 1]);
+                        if (c < 3)
+                            tmem_ld32(s[(c + 1) & 1], s_at + 32 * (c + 1));
+                        float2 x[16];
+                        top = exponents(s[c & 1], c, base, far, x, top);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            x[i].x = dev::ex2(x[i].x);
+                            x[i].y = dev::ex2(x[i].y);
+                            if (i & 1)
+                                sum2 = add2(sum2, x[i]);
+                            else
+                                sum = add2(sum, x[i]);
+                            w[16 * c + i] = dev::Mma<T>::pack(x[i].x, x[i].y);
+                        }
+                    }
+                    const float behind = m == -INFINITY ? -INFINITY : kRescale;  // (-inf: any score is news)
+                    if (pass == 1 || !__any_sync(0xffffffffu, top > behind)) {
+                        l += (sum.x + sum2.x) + (sum.y + sum2.y);
+                        break;
+                    }
                     // O is at rest: the scores of this tile came after the product before it
-                    const float grown = fmaxf(m, now);
-                    const float f = grown == -INFINITY ? 1.f : exp2f(m - grown);
-                    m = grown;
+                    const float f = raise();
                     l *= f;
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < D; c += 32) {
                         uint32_t o[32];
                         tmem_ld32(o, o_at + c);
-                        wait_ld();
+                        wait_ld(o);
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
                             o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
                         tmem_st32(o_at + c, o);
                     }
                 }
-                const float base = m == -INFINITY ? 0.f : m;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float x = dev::ex2(fmaf(__uint_as_float(s[h][2 * i]), p.scale_log2, -base));
-                        const float y = dev::ex2(fmaf(__uint_as_float(s[h][2 * i + 1]), p.scale_log2, -base));
-                        sum[2 * (i & 1)] += x;
-                        sum[2 * (i & 1) + 1] += y;
-                        w[i] = dev::Mma<T>::pack(x, y);
-                    }
-                    tmem_st16(s_at + 16 * h, w);
-                }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                for (int c = 0; c < 2; ++c)
+                    tmem_st32(s_at + 32 * c, *reinterpret_cast<const uint32_t(*)[32]>(w + 32 * c));
                 wait_st();
                 fence_before();
                 dev::mbar_arrive(smem + S::kPFull + 8 * t);
@@ -480,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t o[32];
                 if (b > a) {
                     tmem_ld32(o, o_at + c);
-                    wait_ld();
+                    wait_ld(o);
                 }
                 if (mine && whole) {
                     uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + row * D + c);

@@ -266,3 +266,44 @@ def test_nothing_to_do():
     c = Case([0, 0], [5, 0], 2, 2, 64, 16, "bf16", seed=14, pad=4)
     out, lse = c.run(True)
     assert (out == 7.0).all() and (lse == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("power", [5, 15])
+def test_scores_of_any_size(dtype, sign, power):
+    """Scores up to 2^40, far apart: each row is the value of its largest score (the others'
+    weights are 0), also where the scale is negative: to half a step of its one weight and half
+    a step of the output in fp16 and bf16, in fp32 to the 2^-22 that two tf32 terms leave."""
+    if dtype == "f16":
+        power = 5                                        # (2^5 * 255 is fp16's, 2^15 * 255 is not)
+    t = 250
+    c = Case([t], [t], 2, 1, 64, 16, dtype, seed=15)
+    c.scale = 0.125 * sign
+    c.q[...] = 2.0 ** power
+    rank = torch.randperm(t, device=DEV) + 1
+    slots = (c.bt[0, :16].long()[:, None] * 16 + torch.arange(16, device=DEV)).reshape(-1)[:t]
+    c.k.view(-1, 1, 64)[slots] = (rank * 2.0 ** power * sign)[:, None, None].to(c.dt)
+    out, lse = c.run(True)
+    best = torch.stack([rank[:i + 1].argmax() for i in range(t)])
+    want = c.v.view(-1, 64)[slots[best]]
+    for h in range(2):
+        assert ((out[:t, h] - want).abs().double() <= want.abs().double() * (2.0 ** -22 if dtype == "f32" else torch.finfo(c.dt).eps)).all()
+    top = rank[best].double() * 2.0 ** (2 * power + 3)   # 64 * 2^power * 2^power * rank / 8
+    assert ((lse[:t, 0].double() - top).abs() <= top * 2.0 ** -21).all()
+    assert P.pa_device_errors() == 0
+
+
+def test_waits_that_run_out():
+    """A limit shorter than a copy takes: the launch gives up, says so, and the next one is right."""
+    c = Case([300, 40], [900, 5000], 4, 2, 128, 16, "bf16", seed=16)
+    c.run(True)
+    assert P.pa_device_errors() == 0
+    P.pa_set_wait_limit_ns(1)
+    try:
+        c.run(True)
+        flags = P.pa_device_errors()
+    finally:
+        P.pa_set_wait_limit_ns(0)
+    assert flags & (P.PA_DEVERR_TIMEOUT_FULL | P.PA_DEVERR_TIMEOUT_EMPTY)
+    c.check(*c.run(True), True)
