@@ -152,6 +152,14 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return d;
 }
 
+// One lane of the warp (the same each time), in a form that leaves the code around it uniform.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+
 // Shared-memory operand: 128-byte swizzle.  Rows of 128 bytes along K (Q and K: K-major):
 // groups of 8 rows `sbo` apart.  Rows of 128 bytes along N (V): groups of 8 keys `sbo` apart,
 // the next 64 columns `lbo` on.
@@ -316,73 +324,80 @@ __global__ void __launch_bounds__(kThreads, 1)
                         dev::mbar_wait(smem + S::kQFull + 8 * t, (q_fills[t] - 1) & 1, kWaitTimeoutNs);
             }
         } else if (warp == kMmaWarp) {
-            if (lane == 0) {
-                constexpr uint32_t kScores = instruction(kFormat, kKeys, false);
-                constexpr uint32_t kOutput = instruction(kFormat, D, true);
-                uint32_t fills = 0, q_fills[2] = {0, 0}, steps[2] = {0, 0};
-                bool ok = true;
-                auto stage_at = [&](uint32_t f) { return smem + S::kRing + (f % S::kStages) * S::kTileBytes; };
-                auto full = [&](uint32_t f) {
-                    return wait(smem + S::kFull + 8 * (f % S::kStages), (f / S::kStages) & 1, PA_DEVERR_TIMEOUT_FULL);
-                };
-                auto release = [&](uint32_t f) { commit(smem + S::kEmpty + 8 * (f % S::kStages)); };
-                auto scores = [&](int t, uint32_t f) {
-    #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t off = (k / 4) * kChunkBytes + (k % 4) * 32;
-                        mma_ss(tmem + t * kKeys, operand(smem + t * S::kTileBytes + off, 16, 1024),
-                               operand(stage_at(f) + off, 16, 1024), kScores, k > 0);
-                    }
-                    commit(smem + S::kSFull + 8 * t);
-                };
-                do {
-                    int a, b;
-                    if (!walk.part(a, b) || b == a)
-                        continue;
-                    const auto rows = Walk::rows_of(p, walk.it);
-                    const int tiles_q = rows.tokens > half_tokens ? 2 : 1;
-                    const int n = b - a;
-                    for (int j = -1; j < n && ok; ++j) {
-                        const uint32_t fv = fills + 2 * j + 1, fk = fv + 1;  // V of tile j, K of tile j + 1
-                        for (int t = 0; t < tiles_q && ok; ++t) {
+            // The whole warp goes through the loop, so that addresses and descriptors stay in uniform
+            // registers; one lane issues.  (With one thread alone in the loop each product took 75
+            // cycles to issue, more than the 64 it takes to run.)
+            constexpr uint32_t kScores = instruction(kFormat, kKeys, false);
+            constexpr uint32_t kOutput = instruction(kFormat, D, true);
+            uint32_t fills = 0, q_fills[2] = {0, 0}, steps[2] = {0, 0};
+            bool ok = true;
+            const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
+            auto stage_at = [&](uint32_t f) { return smem + S::kRing + (f % S::kStages) * S::kTileBytes; };
+            auto full = [&](uint32_t f) {
+                return wait_all(smem + S::kFull + 8 * (f % S::kStages), (f / S::kStages) & 1, PA_DEVERR_TIMEOUT_FULL);
+            };
+            auto release = [&](uint32_t f) { return smem + S::kEmpty + 8 * (f % S::kStages); };
+            do {
+                int a, b;
+                if (!walk.part(a, b) || b == a)
+                    continue;
+                const auto rows = Walk::rows_of(p, walk.it);
+                const int tiles_q = __shfl_sync(0xffffffffu, rows.tokens > half_tokens ? 2 : 1, 0);
+                const int n = __shfl_sync(0xffffffffu, b - a, 0);
+                for (int j = -1; j < n && ok; ++j) {
+                    const uint32_t fv = fills + 2 * j + 1, fk = fv + 1;  // V of tile j, K of tile j + 1
+                    const bool more = j + 1 < n;
+                    ok = (j < 0 || full(fv)) && (!more || full(fk));
+                    for (int t = 0; t < tiles_q && ok; ++t) {
+                        const bool last = t == tiles_q - 1;
+                        if (j < 0) {
+                            ok = wait_all(smem + S::kQFull + 8 * t, q_fills[t] & 1, PA_DEVERR_TIMEOUT_FULL);
+                            ++q_fills[t];
+                        } else {
+                            ok = wait_all(smem + S::kPFull + 8 * t, steps[t] & 1, PA_DEVERR_TIMEOUT_FULL);
+                            ++steps[t];
+                        }
+                        if (!ok)
+                            break;
+                        fence_after();
+                        if (elect_one()) {
                             if (j >= 0) {
-                                ok = wait(smem + S::kPFull + 8 * t, steps[t] & 1, PA_DEVERR_TIMEOUT_FULL) &&
-                                     (t > 0 || full(fv));
-                                if (!ok)
-                                    break;
-                                ++steps[t];
-                                fence_after();
-    #pragma unroll
-                                for (int k = 0; k < kKeys / 16; ++k)
-                                    mma_ts(tmem + kColO + t * D, tmem + t * kKeys + 8 * k,
-                                           operand(stage_at(fv) + k * 2048, kChunkBytes, 1024), kOutput, j > 0 || k > 0);
-                                if (j == n - 1)
+                                const uint64_t v = operand(stage_at(fv), kChunkBytes, 1024);
+                                mma_ts(base + kColO + t * D, base + t * kKeys, v, kOutput, j > 0);
+#pragma unroll
+                                for (int k = 1; k < kKeys / 16; ++k)
+                                    mma_ts(base + kColO + t * D, base + t * kKeys + 8 * k, v + k * (2048 >> 4), kOutput,
+                                           true);
+                                if (!more)
                                     commit(smem + S::kODone + 8 * t);
-                                if (t == tiles_q - 1)
-                                    release(fv);
+                                if (last)
+                                    commit(release(fv));
                             }
-                            if (j + 1 < n) {
-                                if (j < 0) {
-                                    ok = wait(smem + S::kQFull + 8 * t, q_fills[t] & 1, PA_DEVERR_TIMEOUT_FULL);
-                                    ++q_fills[t];
+                            if (more) {
+                                const uint64_t q = operand(smem + t * S::kTileBytes, 16, 1024);
+                                const uint64_t k0 = operand(stage_at(fk), 16, 1024);
+#pragma unroll
+                                for (int k = 0; k < D / 16; ++k) {
+                                    const uint32_t off = ((k / 4) * kChunkBytes + (k % 4) * 32) >> 4;
+                                    mma_ss(base + t * kKeys, q + off, k0 + off, kScores, k > 0);
                                 }
-                                ok = ok && (t > 0 || full(fk));
-                                if (!ok)
-                                    break;
-                                scores(t, fk);
+                                commit(smem + S::kSFull + 8 * t);
                                 if (j + 2 == n)
                                     commit(smem + S::kQEmpty + 8 * t);
-                                if (t == tiles_q - 1)
-                                    release(fk);
+                                if (last)
+                                    commit(release(fk));
                             }
                         }
+                        __syncwarp();
                     }
-                    fills += 2 * n;
-                } while (ok && walk.next() && walk.inside());
-                // every product has completed before the CTA gives its memory back
+                }
+                fills += 2 * n;
+            } while (ok && walk.next() && walk.inside());
+            // every product has completed before the CTA gives its memory back
+            if (elect_one())
                 commit(smem + S::kDrain);
-                dev::mbar_wait(smem + S::kDrain, 0, kWaitTimeoutNs);
-            }
+            __syncwarp();
+            dev::mbar_wait(smem + S::kDrain, 0, kWaitTimeoutNs);
             __syncwarp();
         }
     } else {

@@ -294,16 +294,20 @@ def test_scores_of_any_size(dtype, sign, power):
     assert P.pa_device_errors() == 0
 
 
-def test_waits_that_run_out():
-    """A limit shorter than a copy takes: the launch gives up, says so, and the next one is right."""
-    c = Case([300, 40], [900, 5000], 4, 2, 128, 16, "bf16", seed=16)
-    c.run(True)
-    assert P.pa_device_errors() == 0
-    P.pa_set_wait_limit_ns(1)
-    try:
-        c.run(True)
-        flags = P.pa_device_errors()
-    finally:
-        P.pa_set_wait_limit_ns(0)
-    assert flags & (P.PA_DEVERR_TIMEOUT_FULL | P.PA_DEVERR_TIMEOUT_EMPTY)
-    c.check(*c.run(True), True)
+@pytest.mark.parametrize("dtype,new,lens", [("bf16", [300, 40], [900, 5000]), ("f16", [1], [60000]),
+                                            ("bf16", [2000], [9000]), ("f32", [20], [3000])])
+def test_waits_that_run_out(dtype, new, lens):
+    """With a limit shorter than a copy takes, waits may run out: the launch then gives up with its
+    copies in flight, returns and says so, and the next one is right."""
+    timeouts = P.PA_DEVERR_TIMEOUT_FULL | P.PA_DEVERR_TIMEOUT_EMPTY
+    c = Case(new, lens, 4, 2, 128, 16, dtype, seed=16)
+    for _ in range(3):
+        P.pa_set_wait_limit_ns(1)
+        try:
+            c.run(True)
+            flags = P.pa_device_errors()
+        finally:
+            P.pa_set_wait_limit_ns(0)
+        print(f"[waits] {dtype} {new} {lens}: flags {flags:#x}")
+        assert flags & ~timeouts == 0
+        c.check(*c.run(True), True)
