@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             dev::mbar_init(smem + S::kQFull + 8 * t, 1);
             dev::mbar_init(smem + S::kQEmpty + 8 * t, 1);
             dev::mbar_init(smem + S::kSFull + 8 * t, 1);
-            dev::mbar_init(smem + S::kPFull + 8 * t, kTileRows);
+            dev::mbar_init(smem + S::kPFull + 8 * t, kTileRows / 32);  // a warp each
             dev::mbar_init(smem + S::kODone + 8 * t, 1);
         }
         dev::mbar_init(smem + S::kDrain, 1);
@@ -440,8 +440,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Exponents of 32 columns: x = s * scale - base, -inf where the key is hidden; their
                 // maximum.  `far`: the product is rounded first.  Behind a large base the exact one
                 // would differ from it by the product's rounding error, which may be large itself.
-                auto exponents = [&](const uint32_t (&s)[32], int c, float base, bool far, float2 (&x)[16], float top) {
-                    if (far) {
+                // `plain`, known at compile time: neither hidden keys nor `far` (branches would part the
+                // code that the scheduler can interleave).
+                auto exponents = [&](auto plain, const uint32_t (&s)[32], int c, float base, bool far, float2 (&x)[16],
+                                     float top) {
+                    if (!plain && far) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             x[i] = make_float2(__fadd_rn(__fmul_rn(__uint_as_float(s[2 * i]), p.scale_log2), -base),
@@ -452,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int i = 0; i < 16; ++i)
                             x[i] = fma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), scale2, base2);
                     }
-                    if (masked) {
+                    if (!plain && masked) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             x[i].x = key0 + 32 * c + 2 * i < limit ? x[i].x : -INFINITY;
@@ -476,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float2 x[16];
                         tmem_ld32(s, s_at + 32 * c);
                         wait_ld(s);
-                        top = exponents(s, c, 0.f, true, x, top);
+                        top = exponents(std::false_type(), s, c, 0.f, true, x, top);
                     }
                     const float f = top == -INFINITY ? 1.f : exp2f(m - top);
                     m = top;
@@ -485,13 +488,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 if (tile == a)
                     raise();
-                // The probabilities by the base at hand; where that has fallen behind, once more.
+                // The probabilities by a base, their sum, and the largest exponent.
                 uint32_t w[64];
-#pragma unroll 1
-                for (int pass = 0; pass < 2; ++pass) {
+                float2 sum, sum2;
+                auto probabilities = [&](auto plain) {
                     const float base = m == -INFINITY ? 0.f : m;
                     float top = -INFINITY;
-                    float2 sum = make_float2(0.f, 0.f), sum2 = sum;
+                    sum = sum2 = make_float2(0.f, 0.f);
                     uint32_t s[2][32];
                     tmem_ld32(s[0], s_at);
 #pragma unroll
@@ -500,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (c < 3)
                             tmem_ld32(s[(c + 1) & 1], s_at + 32 * (c + 1));
                         float2 x[16];
-                        top = exponents(s[c & 1], c, base, far, x, top);
+                        top = exponents(plain, s[c & 1], c, base, far, x, top);
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             x[i].x = dev::ex2(x[i].x);
@@ -512,11 +515,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                             w[16 * c + i] = dev::Mma<T>::pack(x[i].x, x[i].y);
                         }
                     }
-                    const float behind = m == -INFINITY ? -INFINITY : kRescale;  // (-inf: any score is news)
-                    if (pass == 1 || !__any_sync(0xffffffffu, top > behind)) {
-                        l += (sum.x + sum2.x) + (sum.y + sum2.y);
-                        break;
-                    }
+                    return top;
+                };
+                // By the base at hand; where that has fallen behind, once more by the maximum.
+                const float top = masked || far ? probabilities(std::false_type()) : probabilities(std::true_type());
+                if (__any_sync(0xffffffffu, top > (m == -INFINITY ? -INFINITY : kRescale))) {
                     // O is at rest: the scores of this tile came after the product before it
                     const float f = raise();
                     l *= f;
@@ -530,13 +533,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                             o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
                         tmem_st32(o_at + c, o);
                     }
+                    probabilities(std::false_type());
                 }
+                l += (sum.x + sum2.x) + (sum.y + sum2.y);
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
                     tmem_st32(s_at + 32 * c, *reinterpret_cast<const uint32_t(*)[32]>(w + 32 * c));
                 wait_st();
                 fence_before();
-                dev::mbar_arrive(smem + S::kPFull + 8 * t);
+                __syncwarp();
+                if (lane == 0)
+                    dev::mbar_arrive(smem + S::kPFull + 8 * t);
             }
             if (!ok)
                 break;
