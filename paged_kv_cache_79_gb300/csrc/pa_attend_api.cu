@@ -35,16 +35,17 @@ CUtensorMapDataType type_of(int dtype)
 }
 
 // A 16-bit cache [num_blocks][B][Hkv][d] as (64 elements, token slot, column of 64, kv head); a
-// box is one column of a block's rows of one kv head: B rows of 128 bytes, 128-byte swizzle.
-// (A box of both columns would put them B rows apart; a tile of keys wants them 128 rows apart.)
-bool make_blocks_map(CUtensorMap *map, const void *cache, int num_blocks, int B, int Hkv, int D, int dtype)
+// box is `columns` columns of a block's rows of one kv head, each B rows of 128 bytes, 128-byte
+// swizzle.
+bool make_blocks_map(CUtensorMap *map, const void *cache, int num_blocks, int B, int Hkv, int D, int columns,
+                     int dtype)
 {
     const EncodeTiledFn enc = encode_fn();
     if (!enc)
         return false;
     const cuuint64_t dims[4] = {64, (cuuint64_t)num_blocks * B, (cuuint64_t)D / 64, (cuuint64_t)Hkv};
     const cuuint64_t strides[3] = {(cuuint64_t)Hkv * D * 2, 128, (cuuint64_t)D * 2};
-    const cuuint32_t box[4] = {64, (cuuint32_t)B, 1, 1};
+    const cuuint32_t box[4] = {64, (cuuint32_t)B, (cuuint32_t)columns, 1};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     return enc(map, type_of(dtype), 4, const_cast<void *>(cache), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -163,8 +164,8 @@ pa_status pa_attend(void *out, float *lse, const void *q, long long q_stride, co
     if (!f32 &&
         (!make_rows_map(&L.map_q, q, p.q_stride, num_tokens, num_q_heads, head_dim, p.heads_per_item,
                         p.tokens_per_item / 2, dtype) ||
-         !make_blocks_map(&L.map_k, k_cache, num_blocks, block_size, num_kv_heads, head_dim, dtype) ||
-         !make_blocks_map(&L.map_v, v_cache, num_blocks, block_size, num_kv_heads, head_dim, dtype)))
+         !make_blocks_map(&L.map_k, k_cache, num_blocks, block_size, num_kv_heads, head_dim, 1, dtype) ||
+         !make_blocks_map(&L.map_v, v_cache, num_blocks, block_size, num_kv_heads, head_dim, head_dim / 64, dtype)))
         return cuda_fail(cudaErrorInvalidValue);
     const Workspace w = workspace_of(L.ctas, p.part_rows, head_dim);
     char *const ws = static_cast<char *>(workspace);

@@ -3,7 +3,7 @@
 // An item has two tiles of 128 rows (rows: query tokens times heads of a group) that step
 // through the same keys, 128 at a time.  Per CTA, one per SM:
 //   warp 8       loader: per tile of keys one TMA copy for each cache block and 128-byte
-//                column of K, then of V, into a ring; Q's rows with TMA too.  The rows
+//                column of K, then one for each block of V, into a ring; Q's rows with TMA too.  The rows
 //                behind the last key that an item sees are zeros in V (a weight of 0 times what
 //                a stale row holds would be NaN where that is NaN);
 //   warp 9       products, issued by one thread: S = Q K^T into TMEM (operands in shared
@@ -162,7 +162,8 @@ __device__ __forceinline__ bool elect_one()
 
 // Shared-memory operand: 128-byte swizzle.  Rows of 128 bytes along K (Q and K: K-major):
 // groups of 8 rows `sbo` apart.  Rows of 128 bytes along N (V): groups of 8 keys `sbo` apart,
-// the next 64 columns `lbo` on.
+// the next 64 columns `lbo` on.  (A product takes all of K's rows, evenly spaced, so a block's
+// columns lie a whole tile apart; of V it takes 16 keys at a time, so blocks may stay whole.)
 __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lbo, uint32_t sbo)
 {
     return (uint64_t)((addr >> 4) & 0x3fff) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(sbo >> 4) << 32 | 1ull << 46 |
@@ -242,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp >= kLoaderWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == kLoaderWarp) {
-            uint32_t fills = 0, q_fills[2] = {0, 0};
+            uint32_t fills = 0, stage = 0, round = 0, q_round = 0, q_used = 0;  // (bits t: row tile t)
             bool ok = true;
             const uint32_t q_bytes = (uint32_t)(half_tokens * p.heads_per_item) * 128u * kChunks;
             do {
@@ -251,65 +252,92 @@ __global__ void __launch_bounds__(kThreads, 1)
                     continue;
                 const AttendItem &it = walk.it;
                 const auto rows = Walk::rows_of(p, it);
-                const int tiles_q = rows.tokens > half_tokens ? 2 : 1;
-                for (int t = 0; t < tiles_q && ok; ++t) {
-                    ok = wait_all(smem + S::kQEmpty + 8 * t, (q_fills[t] & 1) ^ 1, PA_DEVERR_TIMEOUT_EMPTY);
-                    if (ok && lane == 0) {
+                const bool two = rows.tokens > half_tokens;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (!ok || (t == 1 && !two))
+                        break;
+                    ok = wait_all(smem + S::kQEmpty + 8 * t, (q_round >> t & 1) ^ 1, PA_DEVERR_TIMEOUT_EMPTY);
+                    if (!ok)
+                        break;
+                    if (elect_one()) {
                         const uint32_t bar = smem + S::kQFull + 8 * t;
                         dev::mbar_arrive_expect_tx(bar, q_bytes);
+#pragma unroll
                         for (int c = 0; c < kChunks; ++c)
                             dev::tma_load_4d(smem + t * S::kTileBytes + c * kChunkBytes, &map_q, 0, rows.head0,
                                              rows.token0 + t * half_tokens, c, bar);
                     }
-                    q_fills[t] += ok;
+                    __syncwarp();
+                    q_round ^= 1u << t;
+                    q_used |= 1u << t;
                 }
                 const int32_t *table = p.block_tables + (size_t)it.s * p.max_blocks;
-                const int blk = lane % kBlocks, chunk = lane / kBlocks;  // this lane's copy of a tile
-                const int used = (it.seen + B - 1) / B;                  // blocks with a key that is seen
+                const int used = (it.seen + B - 1) / B;  // blocks with a key that is seen
+                // lane i: block i of a tile (past the last, or outside the pool: past the pool's end,
+                // where a copy brings zeros)
                 auto id_of = [&](int tile) {
-                    const int j = tile * kBlocks + blk;
-                    const int id = tile < b && j < used ? table[j] : -1;
-                    return id >= 0 && id < p.num_blocks ? id : p.num_blocks;  // (past the end: zeros)
+                    const int j = tile * kBlocks + lane;
+                    const int id = lane < kBlocks && tile < b && j < used ? table[j] : -1;
+                    return id >= 0 && id < p.num_blocks ? id : p.num_blocks;
                 };
+                const int kv_head = __shfl_sync(0xffffffffu, rows.kv, 0);
                 int id = id_of(a);
                 for (int tile = a; tile < b && ok; ++tile) {
-                    const int here = id;
+                    int ids[kBlocks];
+#pragma unroll
+                    for (int i = 0; i < kBlocks; ++i)
+                        ids[i] = __shfl_sync(0xffffffffu, id, i);
                     id = id_of(tile + 1);
-                    const int full = min(max(used - tile * kBlocks, 0), kBlocks);  // blocks of this tile
-                    for (int kv = 0; kv < 2 && ok; ++kv) {
-                        const int stage = fills % S::kStages;
-                        ok = wait_all(smem + S::kEmpty + 8 * stage, ((fills / S::kStages) & 1) ^ 1, PA_DEVERR_TIMEOUT_EMPTY);
+                    const int keys = __shfl_sync(0xffffffffu, min(it.seen - tile * kKeys, kKeys), 0);  // of this tile
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const uint32_t at = smem + S::kRing + stage * S::kTileBytes, bar = smem + S::kFull + 8 * stage;
+                        ok = wait_all(smem + S::kEmpty + 8 * stage, round ^ 1, PA_DEVERR_TIMEOUT_EMPTY);
                         if (!ok)
                             break;
-                        ++fills;
-                        const uint32_t at = smem + S::kRing + stage * S::kTileBytes, bar = smem + S::kFull + 8 * stage;
                         // V's rows behind the last key: the block that holds it by plain copies, zeros after it
-                        int copies = full;
-                        const int rest = it.seen - tile * kKeys;  // keys of this tile
-                        if (kv == 1 && rest < kKeys) {
-                            copies = rest / B;
-                            const int last = __shfl_sync(0xffffffffu, here, copies % 32);
+                        const int copies = kv == 0 ? (keys + B - 1) / B : keys / B;
+                        if (kv == 1 && keys < kKeys) {
+                            const int last = table[tile * kBlocks + min(copies, used - 1 - tile * kBlocks)];
+                            const bool there = last >= 0 && last < p.num_blocks;
                             const int first = copies * B;
                             for (int i = lane; i < (kKeys - first) * (D / 8); i += 32) {
                                 const int r = first + i / (D / 8), x = i % (D / 8);
                                 uint4 val = make_uint4(0, 0, 0, 0);
-                                if (r < rest && last < p.num_blocks)
+                                if (r < keys && there)
                                     val = *reinterpret_cast<const uint4 *>(
                                         static_cast<const T *>(p.v_cache) +
                                         (((size_t)last * B + (r - first)) * p.num_kv_heads + rows.kv) * D + x * 8);
-                                *reinterpret_cast<uint4 *>(smem_ptr + (at - smem) + (x / 8) * kChunkBytes + r * 128 +
+                                *reinterpret_cast<uint4 *>(smem_ptr + (at - smem) + (r / B) * (B * 128 * kChunks) +
+                                                           (x / 8) * (B * 128) + (r % B) * 128 +
                                                            (((x % 8) ^ (r & 7)) << 4)) = val;
                             }
                             fence_async_proxy();
                             __syncwarp();
                         }
-                        if (lane == 0)
+                        if (elect_one()) {
                             dev::mbar_arrive_expect_tx(bar, (uint32_t)(copies * B) * 128u * kChunks);
+#pragma unroll
+                            for (int i = 0; i < kBlocks; ++i) {
+                                if (i >= copies)
+                                    break;
+                                if (kv == 1) {
+                                    dev::tma_load_4d(at + i * (B * 128 * kChunks), &map_v, 0, ids[i] * B, 0, kv_head, bar);
+                                } else {
+#pragma unroll
+                                    for (int c = 0; c < kChunks; ++c)
+                                        dev::tma_load_4d(at + c * kChunkBytes + i * (B * 128), &map_k, 0, ids[i] * B, c,
+                                                         kv_head, bar);
+                                }
+                            }
+                        }
                         __syncwarp();
-                        if (chunk < kChunks && blk < copies)
-                            dev::tma_load_4d(at + chunk * kChunkBytes + blk * B * 128, kv == 0 ? &map_k : &map_v, 0,
-                                             here * B, chunk, rows.kv, bar);
-                        __syncwarp();
+                        ++fills;
+                        if (++stage == S::kStages) {
+                            stage = 0;
+                            round ^= 1;
+                        }
                     }
                 }
             } while (ok && walk.next() && walk.inside());
@@ -320,8 +348,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     dev::mbar_wait(smem + S::kFull + 8 * (f % S::kStages), (f / S::kStages) & 1, kWaitTimeoutNs);
                 }
                 for (int t = 0; t < 2; ++t)
-                    if (q_fills[t])
-                        dev::mbar_wait(smem + S::kQFull + 8 * t, (q_fills[t] - 1) & 1, kWaitTimeoutNs);
+                    if (q_used >> t & 1)
+                        dev::mbar_wait(smem + S::kQFull + 8 * t, (q_round >> t & 1) ^ 1, kWaitTimeoutNs);
             }
         } else if (warp == kMmaWarp) {
             // The whole warp goes through the loop, so that addresses and descriptors stay in uniform
@@ -329,69 +357,92 @@ __global__ void __launch_bounds__(kThreads, 1)
             // cycles to issue, more than the 64 it takes to run.)
             constexpr uint32_t kScores = instruction(kFormat, kKeys, false);
             constexpr uint32_t kOutput = instruction(kFormat, D, true);
-            uint32_t fills = 0, q_fills[2] = {0, 0}, steps[2] = {0, 0};
+            // (Scalars only: an array indexed by the row tile would live in local memory, and each wait
+            // would cost hundreds of cycles more.)
+            uint32_t q_round = 0, p_round = 0;  // bit t: parity of row tile t
+            uint32_t stage = 0, round = 0;      // of the ring
             bool ok = true;
             const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
-            auto stage_at = [&](uint32_t f) { return smem + S::kRing + (f % S::kStages) * S::kTileBytes; };
-            auto full = [&](uint32_t f) {
-                return wait_all(smem + S::kFull + 8 * (f % S::kStages), (f / S::kStages) & 1, PA_DEVERR_TIMEOUT_FULL);
+            auto advance = [&]() {
+                if (++stage == S::kStages) {
+                    stage = 0;
+                    round ^= 1;
+                }
             };
-            auto release = [&](uint32_t f) { return smem + S::kEmpty + 8 * (f % S::kStages); };
+            auto scores = [&](int t, uint32_t k_stage, bool last_keys, bool release) {
+                if (elect_one()) {
+                    const uint64_t q = operand(smem + t * S::kTileBytes, 16, 1024);
+                    const uint64_t k0 = operand(smem + S::kRing + k_stage * S::kTileBytes, 16, 1024);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t off = ((k / 4) * kChunkBytes + (k % 4) * 32) >> 4;
+                        mma_ss(base + t * kKeys, q + off, k0 + off, kScores, k > 0);
+                    }
+                    commit(smem + S::kSFull + 8 * t);
+                    if (last_keys)
+                        commit(smem + S::kQEmpty + 8 * t);
+                    if (release)
+                        commit(smem + S::kEmpty + 8 * k_stage);
+                }
+                __syncwarp();
+            };
             do {
                 int a, b;
                 if (!walk.part(a, b) || b == a)
                     continue;
                 const auto rows = Walk::rows_of(p, walk.it);
-                const int tiles_q = __shfl_sync(0xffffffffu, rows.tokens > half_tokens ? 2 : 1, 0);
+                const bool two = __shfl_sync(0xffffffffu, rows.tokens > half_tokens ? 1 : 0, 0) != 0;
                 const int n = __shfl_sync(0xffffffffu, b - a, 0);
-                for (int j = -1; j < n && ok; ++j) {
-                    const uint32_t fv = fills + 2 * j + 1, fk = fv + 1;  // V of tile j, K of tile j + 1
-                    const bool more = j + 1 < n;
-                    ok = (j < 0 || full(fv)) && (!more || full(fk));
-                    for (int t = 0; t < tiles_q && ok; ++t) {
-                        const bool last = t == tiles_q - 1;
-                        if (j < 0) {
-                            ok = wait_all(smem + S::kQFull + 8 * t, q_fills[t] & 1, PA_DEVERR_TIMEOUT_FULL);
-                            ++q_fills[t];
-                        } else {
-                            ok = wait_all(smem + S::kPFull + 8 * t, steps[t] & 1, PA_DEVERR_TIMEOUT_FULL);
-                            ++steps[t];
-                        }
+                ok = wait_all(smem + S::kFull + 8 * stage, round, PA_DEVERR_TIMEOUT_FULL);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (!ok || (t == 1 && !two))
+                        break;
+                    ok = wait_all(smem + S::kQFull + 8 * t, q_round >> t & 1, PA_DEVERR_TIMEOUT_FULL);
+                    if (!ok)
+                        break;
+                    q_round ^= 1u << t;
+                    scores(t, stage, n == 1, t == 1 || !two);
+                }
+                advance();
+                for (int j = 0; j < n && ok; ++j) {
+                    const uint32_t v_stage = stage;
+                    ok = wait_all(smem + S::kFull + 8 * stage, round, PA_DEVERR_TIMEOUT_FULL);
+                    advance();
+                    const bool more = j + 1 < n;  // `stage`: the next tile's K
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (!ok || (t == 1 && !two))
+                            break;
+                        ok = wait_all(smem + S::kPFull + 8 * t, p_round >> t & 1, PA_DEVERR_TIMEOUT_FULL);
                         if (!ok)
                             break;
+                        p_round ^= 1u << t;
                         fence_after();
                         if (elect_one()) {
-                            if (j >= 0) {
-                                const uint64_t v = operand(stage_at(fv), kChunkBytes, 1024);
-                                mma_ts(base + kColO + t * D, base + t * kKeys, v, kOutput, j > 0);
+                            const uint64_t v = operand(smem + S::kRing + v_stage * S::kTileBytes, B * 128, 1024);
+                            mma_ts(base + kColO + t * D, base + t * kKeys, v, kOutput, j > 0);
 #pragma unroll
-                                for (int k = 1; k < kKeys / 16; ++k)
-                                    mma_ts(base + kColO + t * D, base + t * kKeys + 8 * k, v + k * (2048 >> 4), kOutput,
-                                           true);
-                                if (!more)
-                                    commit(smem + S::kODone + 8 * t);
-                                if (last)
-                                    commit(release(fv));
+                            for (int k = 1; k < kKeys / 16; ++k) {
+                                const uint32_t off = (k * 16 / B * (B * 128 * kChunks) + k * 16 % B * 128) >> 4;
+                                mma_ts(base + kColO + t * D, base + t * kKeys + 8 * k, v + off, kOutput, true);
                             }
-                            if (more) {
-                                const uint64_t q = operand(smem + t * S::kTileBytes, 16, 1024);
-                                const uint64_t k0 = operand(stage_at(fk), 16, 1024);
-#pragma unroll
-                                for (int k = 0; k < D / 16; ++k) {
-                                    const uint32_t off = ((k / 4) * kChunkBytes + (k % 4) * 32) >> 4;
-                                    mma_ss(base + t * kKeys, q + off, k0 + off, kScores, k > 0);
-                                }
-                                commit(smem + S::kSFull + 8 * t);
-                                if (j + 2 == n)
-                                    commit(smem + S::kQEmpty + 8 * t);
-                                if (last)
-                                    commit(release(fk));
-                            }
+                            if (!more)
+                                commit(smem + S::kODone + 8 * t);
+                            if (t == 1 || !two)
+                                commit(smem + S::kEmpty + 8 * v_stage);
                         }
                         __syncwarp();
+                        if (!more)
+                            continue;
+                        if (t == 0)
+                            ok = wait_all(smem + S::kFull + 8 * stage, round, PA_DEVERR_TIMEOUT_FULL);
+                        if (ok)
+                            scores(t, stage, j + 2 == n, t == 1 || !two);
                     }
+                    if (more)
+                        advance();
                 }
-                fills += 2 * n;
             } while (ok && walk.next() && walk.inside());
             // every product has completed before the CTA gives its memory back
             if (elect_one())
