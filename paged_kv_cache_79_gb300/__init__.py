@@ -989,9 +989,10 @@ def pa_attend(out, q, k_cache, v_cache, block_tables, context_lens, query_start,
     include/pagedkv.h).  q's rows may be strided; lse: float32 [N, Hq] for the rows'
     log-sum-exp, or None; workspace: uint8 CUDA tensor or None (allocated here)."""
     T = _torch()
+    _want(q.dim() == 3 and q.shape[1:] == (num_q_heads, head_dim) and out.shape == q.shape,
+          "q and out must be [N, Hq, d]")
     n = q.shape[0]
-    q_stride = _rows(q, "q", n, head_dim)
-    _want(q.shape[1] == num_q_heads and out.shape == q.shape, "q and out must be [N, Hq, d]")
+    q_stride = _row_stride(q, "q")
     _want(k_cache.dim() == 4 and k_cache.shape == v_cache.shape and
           k_cache.shape[1:] == (block_size, num_kv_heads, head_dim), "the caches must be [num_blocks, B, Hkv, d]")
     if not out.dtype == q.dtype == k_cache.dtype == v_cache.dtype:
@@ -1048,48 +1049,48 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "non
     return freqs, amplitude.value
 
 
-def _rows(t, name: str, n: int, d: int):
-    """Stride between the rows of a [N, H, d] tensor whose rows are dense (in elements)."""
-    if t.dim() != 3 or t.shape[0] != n or t.shape[2] != d or not t.shape[1]:
-        raise ValueError(f"{name} must be [{n}, heads, {d}]")
-    h = t.shape[1]
+def _row_stride(t, name: str) -> int:
+    """Elements between the rows of a [N, H, d] tensor, whose rows have to be dense."""
+    n, h, d = t.shape
+    if t.is_contiguous():
+        return h * d
     row, head, one = t.stride()
     if one != 1 or (head != d and h > 1):
         raise ValueError(f"{name} must have dense [heads, head_dim] rows")
     return row if n > 1 else h * d
 
 
-def _rope_args(dense, rows, positions, freqs):
-    """Checks that pa_rope and pa_rope_append share: (device index, device context, n, d, strides)."""
+def _rope_check(q, k, positions, freqs, others):
+    """Checks that pa_rope and pa_rope_append share; returns (device index, device context)."""
     T = _torch()
-    names, tensors = tuple(rows), tuple(rows.values())
-    q = rows["q"]
-    n, _, d = q.shape if q.dim() == 3 else (0, 0, 0)
-    strides = tuple(_rows(t, name, n, d) for name, t in rows.items())
-    for name, t in {**rows, **dense}.items():
-        if t.dtype != q.dtype:
-            raise TypeError(f"{name} and q must have one dtype")
+    _want(q.dim() == 3 and k.dim() == 3 and k.shape[0] == q.shape[0] and k.shape[2] == q.shape[2],
+          "q must be [N, Hq, d] and k [N, Hkv, d]")
+    _want(positions.shape == q.shape[:1] and freqs.dim() == 1, "positions must be [N] and freqs [rotary_dim / 2]")
     if positions.dtype != T.int32 or freqs.dtype != T.int64:
         raise TypeError("positions must be int32 and freqs int64")
-    _want(positions.shape == (n,) and freqs.dim() == 1, "positions must be [N] and freqs [rotary_dim / 2]")
-    _check_counts(n)
-    dev, device = _on_device(tuple(dense) + ("positions", "freqs"), tuple(dense.values()) + (positions, freqs))
-    for name, t in zip(names, tensors):
-        if t.get_device() != dev:
-            raise ValueError(f"{name} must be a CUDA tensor on the device of positions")
-    return dev, device, n, d, strides
+    dtype, at = q.dtype, q.get_device()
+    for t in others:
+        if t.dtype != dtype:
+            raise TypeError("q, k, v, their outputs and the caches must have one dtype")
+        if t.get_device() != at:
+            raise ValueError("all tensors must be on the device of q")
+    dev, device = _on_device(("positions", "freqs"), (positions, freqs))
+    _want(at == dev, "all tensors must be on the device of q")
+    _check_counts(q.shape[0])
+    return dev, device
 
 
 def pa_rope(q_out, q, k_out, k, positions, freqs, interleaved: bool = False, amplitude: float = 1.0, stream=None):
     """q_out, k_out [N, H, d] <- q, k turned by their positions (see pa_rope in
     include/pagedkv.h).  Rows may be strided (parts of a fused projection); q_out may be q
     and k_out k.  freqs int64 [rotary_dim / 2]: rope_frequencies's, on the device."""
-    dev, device, n, d, (qos, qs, kos, ks) = _rope_args(
-        {}, {"q_out": q_out, "q": q, "k_out": k_out, "k": k}, positions, freqs)
+    dev, device = _rope_check(q, k, positions, freqs, (q_out, k_out, k))
     _want(q_out.shape == q.shape and k_out.shape == k.shape, "q_out must be as q and k_out as k")
-    _call("pa_rope", device, q_out.data_ptr(), qos, q.data_ptr(), qs, k_out.data_ptr(), kos, k.data_ptr(), ks,
-          positions.data_ptr(), freqs.data_ptr(), n, q.shape[1], k.shape[1], d, 2 * freqs.shape[0],
-          int(interleaved), float(amplitude), _code(q), _raw_stream(stream, dev))
+    n, hq, d = q.shape
+    _call("pa_rope", device, q_out.data_ptr(), _row_stride(q_out, "q_out"), q.data_ptr(), _row_stride(q, "q"),
+          k_out.data_ptr(), _row_stride(k_out, "k_out"), k.data_ptr(), _row_stride(k, "k"), positions.data_ptr(),
+          freqs.data_ptr(), n, hq, k.shape[1], d, 2 * freqs.shape[0], int(interleaved), float(amplitude), _code(q),
+          _raw_stream(stream, dev))
 
 
 def pa_rope_append(q_out, q, k, v, k_cache, v_cache, positions, slot_mapping, freqs, interleaved: bool = False,
@@ -1098,20 +1099,22 @@ def pa_rope_append(q_out, q, k, v, k_cache, v_cache, positions, slot_mapping, fr
     slot_mapping (int64 [N], negative: skipped) into the caches [num_blocks, B, Hkv, d] (see
     pa_rope_append in include/pagedkv.h).  q, k and v may be strided rows of one fused
     projection; q_out may be q."""
-    dev, device, n, d, (qos, qs, ks, vs) = _rope_args(
-        {"k_cache": k_cache, "v_cache": v_cache, }, {"q_out": q_out, "q": q, "k": k, "v": v}, positions, freqs)
+    dev, device = _rope_check(q, k, positions, freqs, (q_out, k, v, k_cache, v_cache))
+    _want(q_out.shape == q.shape and v.shape == k.shape, "q_out must be as q and v as k")
+    n, hq, d = q.shape
+    hkv = k.shape[1]
+    _want(k_cache.dim() == 4 and k_cache.shape == v_cache.shape and k_cache.shape[2:] == (hkv, d),
+          "the caches must be [num_blocks, B, Hkv, d]")
     if slot_mapping.dtype != _torch().int64:
         raise TypeError("slot_mapping must be int64")
-    _want(q_out.shape == q.shape and v.shape == k.shape, "q_out must be as q and v as k")
-    _want(k_cache.dim() == 4 and k_cache.shape == v_cache.shape and k_cache.shape[2:] == k.shape[1:],
-          "the caches must be [num_blocks, B, Hkv, d]")
     _want(slot_mapping.shape == (n,), "slot_mapping must be [N]")
-    _on_device(("positions", "slot_mapping"), (positions, slot_mapping))
-    _check_counts(k_cache.shape[0] | k_cache.shape[1])
-    _call("pa_rope_append", device, q_out.data_ptr(), qos, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
-          k_cache.data_ptr(), v_cache.data_ptr(), positions.data_ptr(), slot_mapping.data_ptr(), freqs.data_ptr(), n,
-          q.shape[1], k.shape[1], d, 2 * freqs.shape[0], int(interleaved), float(amplitude), k_cache.shape[1],
-          k_cache.shape[0], _code(q), _raw_stream(stream, dev))
+    _on_device(("positions", "slot_mapping", "k_cache", "v_cache"), (positions, slot_mapping, k_cache, v_cache))
+    blocks, size = k_cache.shape[:2]
+    _check_counts(blocks | size)
+    _call("pa_rope_append", device, q_out.data_ptr(), _row_stride(q_out, "q_out"), q.data_ptr(), _row_stride(q, "q"),
+          k.data_ptr(), _row_stride(k, "k"), v.data_ptr(), _row_stride(v, "v"), k_cache.data_ptr(),
+          v_cache.data_ptr(), positions.data_ptr(), slot_mapping.data_ptr(), freqs.data_ptr(), n, hq, hkv, d,
+          2 * freqs.shape[0], int(interleaved), float(amplitude), size, blocks, _code(q), _raw_stream(stream, dev))
 
 
 def pa_kv_transfer_worthwhile(reusable_tokens: int, threshold_tokens: int = 64) -> bool:

@@ -20,7 +20,7 @@ namespace pagedkv {
 
 constexpr int kAttendRows = 256;     // rows of an item at most
 constexpr int kAttendCharge = 192;   // an item's fixed cost, in keys
-constexpr int kAttendMinShare = 768; // cost per CTA at least
+constexpr int kAttendMinShare = 192; // cost per CTA at least: no two short items on one CTA while others idle
 constexpr int kF32TileRows = 64;     // rows of an item of the fp32 kernel
 
 struct AttendItem {

@@ -260,7 +260,7 @@ cudaError_t launch_d(const AttendLaunch &L, cudaStream_t stream)
 }
 
 // ---- the merge of cut items --------------------------------------------------------
-constexpr int kMergeWarps = 4;
+constexpr int kMergeWarps = 8;
 constexpr int kMergeRows = 16;  // rows per CTA
 
 // CTA (c, y): rows [y kMergeRows, ..) of the item that CTA c + 1 of the attention cut first.
@@ -282,31 +282,40 @@ __global__ void __launch_bounds__(32 * kMergeWarps) attend_merge_kernel(const __
         auto row_of = [&](int part) {
             return part == 0 ? attend_part_row(p, cta - 1, 1) + r : attend_part_row(p, cta + part - 1, 0) + r;
         };
+        // Two passes: the maximum over the parts, then 32 parts at a time, their weights a lane each.
+        // (A row's parts follow one another, so 8 loads are put in flight at once.)
         float m = -INFINITY;
         for (int i = lane; i < c.parts; i += 32)
             m = fmaxf(m, p.part_ml[row_of(i)].x);
         m = dev::warp_max(m);
         const float base = m == -INFINITY ? 0.f : m;
         float l = 0.f, o[kE] = {};
-#pragma unroll 4
-        for (int i = 0; i < c.parts; ++i) {
-            const size_t row = row_of(i);
-            const float2 ml = p.part_ml[row];
-            const float w = exp2f(ml.x - base);
-            l += w * ml.y;
-            const float *src = p.part_o + row * D + lane * kE;
-            if constexpr (kE == 4) {
-                const float4 x = *reinterpret_cast<const float4 *>(src);
-                o[0] += w * x.x;
-                o[1] += w * x.y;
-                o[2] += w * x.z;
-                o[3] += w * x.w;
-            } else {
-                const float2 x = *reinterpret_cast<const float2 *>(src);
-                o[0] += w * x.x;
-                o[1] += w * x.y;
+        for (int i0 = 0; i0 < c.parts; i0 += 32) {
+            float weight = 0.f;
+            if (i0 + lane < c.parts) {
+                const float2 ml = p.part_ml[row_of(i0 + lane)];
+                weight = exp2f(ml.x - base);
+                l += weight * ml.y;
+            }
+            const int n = min(c.parts - i0, 32);
+#pragma unroll 8
+            for (int i = 0; i < n; ++i) {
+                const float w = __shfl_sync(0xffffffffu, weight, i);
+                const float *src = p.part_o + row_of(i0 + i) * D + lane * kE;
+                if constexpr (kE == 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(src);
+                    o[0] += w * x.x;
+                    o[1] += w * x.y;
+                    o[2] += w * x.z;
+                    o[3] += w * x.w;
+                } else {
+                    const float2 x = *reinterpret_cast<const float2 *>(src);
+                    o[0] += w * x.x;
+                    o[1] += w * x.y;
+                }
             }
         }
+        l = dev::warp_sum(l);
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const size_t row = (size_t)(c.token0 + tok) * p.num_q_heads + c.head0 + head;
         T *dst = static_cast<T *>(p.out) + row * D + lane * kE;

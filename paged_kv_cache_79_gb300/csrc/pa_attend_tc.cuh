@@ -299,20 +299,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // V's rows behind the last key: the block that holds it by plain copies, zeros after it
                         const int copies = kv == 0 ? (keys + B - 1) / B : keys / B;
                         if (kv == 1 && keys < kKeys) {
-                            const int last = table[tile * kBlocks + min(copies, used - 1 - tile * kBlocks)];
-                            const bool there = last >= 0 && last < p.num_blocks;
+                            constexpr int kVecs = D / 8, kBatch = 8;
+                            auto row_at = [&](int r, int x) {  // vector x of row r of the tile
+                                return reinterpret_cast<uint4 *>(smem_ptr + (at - smem) + r / B * (B * 128 * kChunks) +
+                                                                 x / 8 * (B * 128) + r % B * 128 +
+                                                                 (((x % 8) ^ (r & 7)) << 4));
+                            };
                             const int first = copies * B;
-                            for (int i = lane; i < (kKeys - first) * (D / 8); i += 32) {
-                                const int r = first + i / (D / 8), x = i % (D / 8);
-                                uint4 val = make_uint4(0, 0, 0, 0);
-                                if (r < keys && there)
-                                    val = *reinterpret_cast<const uint4 *>(
-                                        static_cast<const T *>(p.v_cache) +
-                                        (((size_t)last * B + (r - first)) * p.num_kv_heads + rows.kv) * D + x * 8);
-                                *reinterpret_cast<uint4 *>(smem_ptr + (at - smem) + (r / B) * (B * 128 * kChunks) +
-                                                           (x / 8) * (B * 128) + (r % B) * 128 +
-                                                           (((x % 8) ^ (r & 7)) << 4)) = val;
+                            const int last = first < keys ? table[tile * kBlocks + copies] : -1;
+                            const bool there = last >= 0 && last < p.num_blocks;
+                            const uint4 *src = reinterpret_cast<const uint4 *>(
+                                static_cast<const T *>(p.v_cache) +
+                                ((size_t)(there ? last : 0) * B * p.num_kv_heads + rows.kv) * D);
+                            const int vecs = (keys - first) * kVecs;
+                            for (int i0 = lane; i0 < vecs; i0 += 32 * kBatch) {
+                                uint4 val[kBatch];
+#pragma unroll
+                                for (int u = 0; u < kBatch; ++u) {
+                                    const int i = i0 + 32 * u;
+                                    val[u] = make_uint4(0, 0, 0, 0);
+                                    if (i < vecs && there)
+                                        val[u] = src[(size_t)(i / kVecs) * p.num_kv_heads * kVecs + i % kVecs];
+                                }
+#pragma unroll
+                                for (int u = 0; u < kBatch; ++u)
+                                    if (i0 + 32 * u < vecs)
+                                        *row_at(first + (i0 + 32 * u) / kVecs, i0 % kVecs) = val[u];
                             }
+                            for (int i = keys * kVecs + lane; i < kKeys * kVecs; i += 32)
+                                *row_at(i / kVecs, i % kVecs) = make_uint4(0, 0, 0, 0);
                             fence_async_proxy();
                             __syncwarp();
                         }

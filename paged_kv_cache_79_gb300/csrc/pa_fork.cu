@@ -72,26 +72,33 @@ __global__ void __launch_bounds__(kRowThreads) fork_rows_kernel(const __grid_con
         int32_t *dst = p.tables_out + (size_t)i * p.max_blocks;
         for (int j = j0 + tid; j < j1; j += kRowThreads)
             dst[j] = j < row.blocks ? src[j] : -1;
-        if (j0 == 0) {
-            // a child before this one keeps the half-filled block
-            bool later = false;
-            if (row.half)
-                for (int k = tid; k < i; k += kRowThreads)
-                    later |= p.parents[k] == parent;
-            later = __syncthreads_or(later);
-            if (tid == 0)
-                p.granted[i] = !real ? kEmpty : later ? kWantsCopy : kContinues;
-        }
     }
-    if (i < p.rows) {
+    // One look through the parents: whether a child before this one keeps the half-filled block,
+    // and how many children old row i has.
+    const int parent = i < p.children ? p.parents[i] : -1;
+    int kids = 0, earlier = 0;
+    if (j0 == 0 || i < p.rows)
+#pragma unroll 4
+        for (int k = tid; k < p.children; k += kRowThreads) {
+            const int x = p.parents[k];
+            kids += x == i ? 1 : 0;
+            earlier |= k < i && x == parent ? 1 : 0;
+        }
+    __shared__ int s_kids;
+    if (tid == 0)
+        s_kids = 0;
+    earlier = __syncthreads_or(earlier);
+    kids = __reduce_add_sync(0xffffffffu, kids);
+    if ((tid & 31) == 0 && kids)
+        atomicAdd(&s_kids, kids);
+    __syncthreads();
+    kids = s_kids;
+    if (tid == 0 && j0 == 0 && i < p.children) {
+        const bool real = parent >= 0 && parent < p.rows;
+        p.granted[i] = !real ? kEmpty : earlier && row_of(p, parent).half ? kWantsCopy : kContinues;
+    }
+    if (i < p.rows && kids != 1) {
         const Row row = row_of(p, i);
-        if (j0 >= row.blocks)
-            return;
-        int kids = 0;
-        for (int k0 = 0; k0 < p.children; k0 += kRowThreads)
-            kids += __syncthreads_count(k0 + tid < p.children && p.parents[k0 + tid] == i);
-        if (kids == 1)
-            return;
         const int32_t *src = p.tables_in + (size_t)i * p.max_blocks;
         const int full = row.blocks - (row.half ? 1 : 0);
         for (int j = j0 + tid; j < min(j1, row.blocks); j += kRowThreads)
@@ -100,32 +107,41 @@ __global__ void __launch_bounds__(kRowThreads) fork_rows_kernel(const __grid_con
     }
 }
 
-// Exclusive count of the flags before this thread's in the CTA; *total: all of them.
-__device__ __forceinline__ int count_before(bool flag, int *total, int (&part)[32])
+// Exclusive sums of x over the CTA's threads; *total: all of them.
+__device__ __forceinline__ int sum_before(int x, int *total, int (&part)[32])
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const unsigned int m = __ballot_sync(0xffffffffu, flag);
-    __syncthreads();  // the previous counts have been read
-    if (lane == 0)
-        part[warp] = __popc(m);
-    __syncthreads();
-    const int own = lane < kEndThreads / 32 ? part[lane] : 0;
-    int x = own;
+    int in = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        const int y = __shfl_up_sync(0xffffffffu, in, o);
         if (lane >= o)
-            x += y;
+            in += y;
     }
-    *total = __shfl_sync(0xffffffffu, x, 31);
-    return __shfl_sync(0xffffffffu, x - own, warp) + __popc(m & ((1u << lane) - 1u));
+    __syncthreads();  // the previous sums have been read
+    if (lane == 31)
+        part[warp] = in;
+    __syncthreads();
+    const int own = part[lane];
+    int w = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o)
+            w += y;
+    }
+    *total = __shfl_sync(0xffffffffu, w, 31);
+    return __shfl_sync(0xffffffffu, w - own, warp) + in - x;
 }
 
+// A thread goes through kOwn consecutive blocks at a time, so that the ascending order of the
+// blocks is the order of the threads and one sum over the CTA places them all.
+constexpr int kOwn = 32;
 __global__ void __launch_bounds__(kEndThreads) fork_end_kernel(const __grid_constant__ ForkParams p)
 {
     namespace cg = cooperative_groups;
     __shared__ int part[32];
-    __shared__ int freed, refusals;
+    __shared__ int freed, wanted_here;
     cg::cluster_group cluster = cg::this_cluster();
     dev::grid_dependency_wait();
     dev::grid_launch_dependents();
@@ -133,57 +149,105 @@ __global__ void __launch_bounds__(kEndThreads) fork_end_kernel(const __grid_cons
     const int rank = (int)cluster.block_rank();
     const int had = min(max(*p.num_free, 0), p.num_blocks);
 
-    // the blocks that lost their last reference, in ascending order; each CTA a range
-    const long long share = ((long long)p.num_blocks + kEndCtas - 1) / kEndCtas;
-    const int b0 = (int)min(rank * share, (long long)p.num_blocks);
-    const int b1 = (int)min((rank + 1) * share, (long long)p.num_blocks);
-    int mine = 0;
-    for (int b = b0 + tid; b < b1; b += kEndThreads)
-        mine += p.extra[b] < 0 ? 1 : 0;
+    // The blocks that lost their last reference, in ascending order; each CTA a range of blocks, a
+    // multiple of kOwn long, each thread kOwn of them as a mask of bits.
+    const long long share =
+        ((long long)p.num_blocks + kEndCtas * kOwn - 1) / (kEndCtas * kOwn) * kOwn;
+    const long long b0 = min(rank * share, (long long)p.num_blocks);
+    const long long b1 = min(b0 + share, (long long)p.num_blocks);
+    const bool vectors = (reinterpret_cast<uintptr_t>(p.extra) & 15) == 0;
+    auto gone_of = [&](long long b) {  // of blocks b .. b + kOwn - 1
+        unsigned int gone = 0;
+        if (b + kOwn <= b1 && vectors) {
+            int4 x[kOwn / 4];
+#pragma unroll
+            for (int i = 0; i < kOwn / 4; ++i)
+                x[i] = *reinterpret_cast<const int4 *>(p.extra + b + 4 * i);
+#pragma unroll
+            for (int i = 0; i < kOwn / 4; ++i)
+                gone |= ((unsigned int)x[i].x >> 31 | (unsigned int)x[i].y >> 31 << 1 | (unsigned int)x[i].z >> 31 << 2 |
+                         (unsigned int)x[i].w >> 31 << 3)
+                        << (4 * i);
+        } else {
+            for (int i = 0; i < kOwn && b + i < b1; ++i)
+                gone |= (p.extra[b + i] < 0 ? 1u : 0u) << i;
+        }
+        return gone;
+    };
+    const long long step = (long long)kEndThreads * kOwn;
+    const unsigned int first_gone = gone_of(b0 + (long long)tid * kOwn);
+    int mine = __popc(first_gone);
+    for (long long b = b0 + tid * kOwn + step; b < b1; b += step)
+        mine += __popc(gone_of(b));
+    // the children that want a copy, kEndThreads of them a CTA at a time
+    auto state_of = [&](int i) { return i < p.children ? p.granted[i] : (int)kEmpty; };
+    int state = state_of(rank * kEndThreads + tid);
     if (tid == 0)
         freed = 0;
+    wanted_here = 0;
     __syncthreads();
-    if (mine)
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    if ((tid & 31) == 0 && mine)
         atomicAdd(&freed, mine);
+    const unsigned int wants_mask = __ballot_sync(0xffffffffu, state == kWantsCopy);
+    if ((tid & 31) == 0 && wants_mask)
+        atomicAdd(&wanted_here, __popc(wants_mask));
     cluster.sync();
     long long before = 0, all = 0;
+    int wanted = 0, round_wants = 0;  // wanted: by the children before this CTA's
     for (int r = 0; r < kEndCtas; ++r) {
-        const int n = *cluster.map_shared_rank(&freed, r);
+        const int n = *cluster.map_shared_rank(&freed, r), w = *cluster.map_shared_rank(&wanted_here, r);
         before += r < rank ? n : 0;
         all += n;
+        wanted += r < rank ? w : 0;
+        round_wants += w;
     }
     if (freed > 0) {
         long long at = had + before;
-        for (int c = b0; c < b1; c += kEndThreads) {
-            const int b = c + tid;
-            const bool gone = b < b1 && p.extra[b] < 0;
-            if (!__syncthreads_or(gone))
-                continue;
+        for (long long b = b0; b < b1; b += step) {
+            const long long own = b + (long long)tid * kOwn;
+            unsigned int gone = b == b0 ? first_gone : gone_of(own);
             int total;
-            const int k = count_before(gone, &total, part);
-            if (gone) {
-                if (at + k < p.num_blocks)  // (past it: the list held blocks that were in use)
-                    p.free_list[at + k] = b;
-                p.extra[b] = 0;
+            long long k = at + sum_before(__popc(gone), &total, part);
+            while (gone) {
+                const long long id = own + __ffs(gone) - 1;
+                gone &= gone - 1;
+                if (k < p.num_blocks)  // (past it: the list held blocks that were in use)
+                    p.free_list[k] = (int)id;
+                p.extra[id] = 0;
+                ++k;
             }
             at += total;
         }
     }
-    cluster.sync();  // the free list is whole
+    cluster.sync();  // the free list is whole, num_free and the counts have been read
     const int have = (int)min(had + all, (long long)p.num_blocks);
 
-    // the first CTA hands out the copies, in the children's order
-    if (rank == 0) {
-        int wanted = 0, refused = 0;
-        for (int c = 0; c < p.children; c += kEndThreads) {
-            const int i = c + tid;
-            const int state = i < p.children ? p.granted[i] : kEmpty;
-            const bool wants = state == kWantsCopy;
+    // copies, in the children's order
+    int total_wants = 0;
+    for (int c = 0; c < p.children; c += kEndCtas * kEndThreads) {
+        const int i = c + rank * kEndThreads + tid;
+        if (c > 0) {  // (more than kEndCtas kEndThreads children: count the next ones)
+            state = state_of(i);
             int total;
-            const int k = wanted + count_before(wants, &total, part);
-            wanted += total;
-            if (i >= p.children)
-                continue;
+            sum_before(state == kWantsCopy ? 1 : 0, &total, part);
+            cluster.sync();
+            wanted_here = total;
+            cluster.sync();
+            wanted = total_wants;
+            round_wants = 0;
+            for (int r = 0; r < kEndCtas; ++r) {
+                const int w = *cluster.map_shared_rank(&wanted_here, r);
+                wanted += r < rank ? w : 0;
+                round_wants += w;
+            }
+        }
+        total_wants += round_wants;
+        const bool wants = state == kWantsCopy;
+        int total;
+        const int k = wanted + sum_before(wants ? 1 : 0, &total, part);
+        bool refused = false;
+        if (i < p.children) {
             int len = 0, src = -1, dst = -1, says = state;
             if (state != kEmpty) {
                 const int parent = p.parents[i];
@@ -198,6 +262,7 @@ __global__ void __launch_bounds__(kEndThreads) fork_end_kernel(const __grid_cons
                 } else if (wants) {
                     len = 0;
                     says = kRefused;
+                    refused = true;
                 }
             }
             p.context_lens_out[i] = len;
@@ -205,30 +270,24 @@ __global__ void __launch_bounds__(kEndThreads) fork_end_kernel(const __grid_cons
             p.pairs[2 * (size_t)i + 1] = dst;
             p.granted[i] = says;
         }
-        refused = max(wanted - have, 0);
-        if (tid == 0) {
-            refusals = refused;
-            *p.num_free_out = max(have - wanted, 0);
-        }
-    }
-    cluster.sync();  // what the first CTA wrote is seen by all; num_free was read by all
-    const int any = *cluster.map_shared_rank(&refusals, 0);
-    if (any > 0) {
-        // a refused child's row is empty and holds no references (its parent's first child
-        // holds the same full blocks, so none of them is freed here)
-        for (int i = rank; i < p.children; i += kEndCtas) {
-            if (p.granted[i] != kRefused)
-                continue;
-            const int parent = p.parents[i];
+        // A refused child's row is empty and holds no references (its parent's first child holds the
+        // same full blocks, so none of them is freed here).  A warp goes through its own.
+        unsigned int left = __ballot_sync(0xffffffffu, refused);
+        while (left) {
+            const int child = (i & ~31) + __ffs(left) - 1;
+            left &= left - 1;
+            const int parent = p.parents[child];
             const Row row = row_of(p, parent);
-            for (int j = tid; j < row.blocks; j += kEndThreads) {
+            for (int j = tid & 31; j < row.blocks; j += 32) {
                 if (j < row.blocks - 1)
                     add_refs(p, p.tables_in[(size_t)parent * p.max_blocks + j], -1);
-                p.tables_out[(size_t)i * p.max_blocks + j] = -1;
+                p.tables_out[(size_t)child * p.max_blocks + j] = -1;
             }
         }
     }
-    cluster.sync();  // the first CTA's shared memory is read before it ends
+    if (rank == 0 && tid == 0)
+        *p.num_free_out = max(have - total_wants, 0);
+    cluster.sync();  // nobody's shared memory is read any more
 }
 
 }  // namespace

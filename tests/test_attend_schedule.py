@@ -7,7 +7,7 @@ import random
 
 import pytest
 
-CHARGE, MIN_SHARE = 192, 768
+CHARGE, MIN_SHARE = 192, 192
 
 
 class Schedule:
