@@ -3,12 +3,14 @@
 // An item has two tiles of 128 rows (rows: query tokens times heads of a group) that step
 // through the same keys, 128 at a time.  Per CTA, one per SM:
 //   warp 8       loader: per tile of keys one TMA copy for each cache block and 128-byte
-//                column of K, then one for each block of V, into a ring; Q's rows with TMA too.  The rows
-//                behind the last key that an item sees are zeros in V (a weight of 0 times what
-//                a stale row holds would be NaN where that is NaN);
+//                column of K, then one for each block of V, into a ring; Q's rows with TMA too.
+//                Block ids are read a window of 32 ahead, the next item's first ones while this
+//                one's tiles are copied (a read takes longer than a tile when DRAM is busy);
+//   warp 10      makes the rows behind the last key that an item sees zeros in V (a weight of
+//                0 times what a stale row holds would be NaN where that is NaN);
 //   warp 9       products, issued by one thread: S = Q K^T into TMEM (operands in shared
 //                memory), O += P V with P read from TMEM;
-//   (warps 10 and 11 only fill up their warpgroup, which hands its registers on)
+//   (warp 11 only fills up its warpgroup, which hands its registers on)
 //   warps 0..3   softmax of the first row tile, warps 4..7 of the second: a thread has a row.
 //                It reads its 128 scores from TMEM, writes its probabilities over them as
 //                fp16/bf16, and keeps the row's maximum and sum.
@@ -31,6 +33,7 @@ namespace tc {
 constexpr int kThreads = 384;
 constexpr int kLoaderWarp = 8;
 constexpr int kMmaWarp = 9;
+constexpr int kTailWarp = 10;
 constexpr int kTileRows = 128;
 constexpr int kKeys = 128;
 constexpr int kChunkBytes = kKeys * 128;   // 128 rows of 128 bytes: one column of a tile
@@ -46,7 +49,8 @@ struct Smem {
     static constexpr int kStages = D == 128 ? 5 : 10;
     static constexpr int kRing = 2 * kTileBytes;              // behind the two tiles of Q
     static constexpr int kBars = kRing + kStages * kTileBytes;
-    static constexpr int kFull = kBars, kEmpty = kFull + 8 * kStages, kQFull = kEmpty + 8 * kStages,
+    static constexpr int kFull = kBars, kEmpty = kFull + 8 * kStages, kRaw = kEmpty + 8 * kStages,
+                         kQFull = kRaw + 8 * kStages,
                          kQEmpty = kQFull + 16, kSFull = kQEmpty + 16, kPFull = kSFull + 16, kODone = kPFull + 16,
                          kDrain = kODone + 16, kTmem = kDrain + 8, kAbort = kTmem + 4, kScratch = kAbort + 4,
                          kEnd = kScratch + 8 * (kThreads / 32 + 4);
@@ -199,6 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < S::kStages; ++i) {
             dev::mbar_init(smem + S::kFull + 8 * i, 1);
             dev::mbar_init(smem + S::kEmpty + 8 * i, 1);
+            dev::mbar_init(smem + S::kRaw + 8 * i, 1);
         }
         for (int t = 0; t < 2; ++t) {
             dev::mbar_init(smem + S::kQFull + 8 * t, 1);
@@ -239,19 +244,44 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     // The softmax warps hold 128 scores a thread: 168 registers each at launch (three warps per
-    // scheduler) become 2 x 208 and 88.
+    // scheduler) become 2 x 200 and 104.
     if (warp >= kLoaderWarp) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         if (warp == kLoaderWarp) {
-            uint32_t fills = 0, stage = 0, round = 0, q_round = 0, q_used = 0;  // (bits t: row tile t)
+            uint32_t stage = 0, round = 0, q_round = 0;  // parities of the ring, of Q (bit t: row tile t)
+            uint32_t filled = 0, raw = 0, raw_round = 0; // bits: stages filled, filled with a tail, its parity
+            uint32_t q_used = 0;
             bool ok = true;
             const uint32_t q_bytes = (uint32_t)(half_tokens * p.heads_per_item) * 128u * kChunks;
-            do {
-                int a, b;
-                if (!walk.part(a, b) || b == a)
-                    continue;
-                const AttendItem &it = walk.it;
+            // The blocks of 32 / kBlocks tiles from `tile` on, one per lane (past the last that is seen, or
+            // outside the pool: past the pool's end, where a copy brings zeros).
+            constexpr int kWindow = 32 / kBlocks;
+            auto window = [&](const AttendItem &it, int tile, int end) {
+                const int j = tile * kBlocks + lane;
+                int id = -1;
+                if (j < min((it.seen + B - 1) / B, end * kBlocks))
+                    id = p.block_tables[(size_t)it.s * p.max_blocks + j];
+                return id >= 0 && id < p.num_blocks ? id : p.num_blocks;
+            };
+            int a, b;
+            bool there = false;  // an item with tiles of this CTA
+            int ahead = 0;       // its first window
+            auto find = [&](bool more) {
+                for (there = false; more; more = walk.next() && walk.inside())
+                    if (walk.part(a, b) && b > a) {
+                        there = true;
+                        ahead = window(walk.it, a, b);
+                        return;
+                    }
+            };
+            find(true);
+            while (there && ok) {
+                const AttendItem it = walk.it;
                 const auto rows = Walk::rows_of(p, it);
+                const int from = a, end = b;
+                int id = ahead, id_next = window(it, from + kWindow, end);
+                // the next item's blocks are read while this one's are copied
+                find(walk.next() && walk.inside());
                 const bool two = rows.tokens > half_tokens;
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
@@ -272,65 +302,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                     q_round ^= 1u << t;
                     q_used |= 1u << t;
                 }
-                const int32_t *table = p.block_tables + (size_t)it.s * p.max_blocks;
-                const int used = (it.seen + B - 1) / B;  // blocks with a key that is seen
-                // lane i: block i of a tile (past the last, or outside the pool: past the pool's end,
-                // where a copy brings zeros)
-                auto id_of = [&](int tile) {
-                    const int j = tile * kBlocks + lane;
-                    const int id = lane < kBlocks && tile < b && j < used ? table[j] : -1;
-                    return id >= 0 && id < p.num_blocks ? id : p.num_blocks;
-                };
                 const int kv_head = __shfl_sync(0xffffffffu, rows.kv, 0);
-                int id = id_of(a);
-                for (int tile = a; tile < b && ok; ++tile) {
+                int slot = 0;  // of the window
+                for (int tile = from; tile < end && ok; ++tile) {
                     int ids[kBlocks];
 #pragma unroll
                     for (int i = 0; i < kBlocks; ++i)
-                        ids[i] = __shfl_sync(0xffffffffu, id, i);
-                    id = id_of(tile + 1);
+                        ids[i] = __shfl_sync(0xffffffffu, id, slot * kBlocks + i);
+                    if (++slot == kWindow) {
+                        slot = 0;
+                        id = id_next;
+                        id_next = window(it, tile + 1 + kWindow, end);
+                    }
                     const int keys = __shfl_sync(0xffffffffu, min(it.seen - tile * kKeys, kKeys), 0);  // of this tile
+                    const int copies = (keys + B - 1) / B;
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv) {
-                        const uint32_t at = smem + S::kRing + stage * S::kTileBytes, bar = smem + S::kFull + 8 * stage;
                         ok = wait_all(smem + S::kEmpty + 8 * stage, round ^ 1, PA_DEVERR_TIMEOUT_EMPTY);
                         if (!ok)
                             break;
-                        // V's rows behind the last key: the block that holds it by plain copies, zeros after it
-                        const int copies = kv == 0 ? (keys + B - 1) / B : keys / B;
-                        if (kv == 1 && keys < kKeys) {
-                            constexpr int kVecs = D / 8, kBatch = 8;
-                            auto row_at = [&](int r, int x) {  // vector x of row r of the tile
-                                return reinterpret_cast<uint4 *>(smem_ptr + (at - smem) + r / B * (B * 128 * kChunks) +
-                                                                 x / 8 * (B * 128) + r % B * 128 +
-                                                                 (((x % 8) ^ (r & 7)) << 4));
-                            };
-                            const int first = copies * B;
-                            const int last = first < keys ? table[tile * kBlocks + copies] : -1;
-                            const bool there = last >= 0 && last < p.num_blocks;
-                            const uint4 *src = reinterpret_cast<const uint4 *>(
-                                static_cast<const T *>(p.v_cache) +
-                                ((size_t)(there ? last : 0) * B * p.num_kv_heads + rows.kv) * D);
-                            const int vecs = (keys - first) * kVecs;
-                            for (int i0 = lane; i0 < vecs; i0 += 32 * kBatch) {
-                                uint4 val[kBatch];
-#pragma unroll
-                                for (int u = 0; u < kBatch; ++u) {
-                                    const int i = i0 + 32 * u;
-                                    val[u] = make_uint4(0, 0, 0, 0);
-                                    if (i < vecs && there)
-                                        val[u] = src[(size_t)(i / kVecs) * p.num_kv_heads * kVecs + i % kVecs];
-                                }
-#pragma unroll
-                                for (int u = 0; u < kBatch; ++u)
-                                    if (i0 + 32 * u < vecs)
-                                        *row_at(first + (i0 + 32 * u) / kVecs, i0 % kVecs) = val[u];
-                            }
-                            for (int i = keys * kVecs + lane; i < kKeys * kVecs; i += 32)
-                                *row_at(i / kVecs, i % kVecs) = make_uint4(0, 0, 0, 0);
-                            fence_async_proxy();
-                            __syncwarp();
-                        }
+                        // V with rows behind the last key goes to the tail warp first
+                        const bool tail = kv == 1 && keys < kKeys;
+                        const uint32_t at = smem + S::kRing + stage * S::kTileBytes;
+                        const uint32_t bar = smem + (tail ? S::kRaw : S::kFull) + 8 * stage;
                         if (elect_one()) {
                             dev::mbar_arrive_expect_tx(bar, (uint32_t)(copies * B) * 128u * kChunks);
 #pragma unroll
@@ -348,24 +342,61 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                         __syncwarp();
-                        ++fills;
+                        const uint32_t bit = 1u << stage;
+                        filled |= bit;
+                        raw = tail ? raw | bit : raw & ~bit;
+                        raw_round ^= tail ? bit : 0;
                         if (++stage == S::kStages) {
                             stage = 0;
                             round ^= 1;
                         }
                     }
                 }
-            } while (ok && walk.next() && walk.inside());
+            }
             // what is in flight lands before the CTA ends
             if (*abort) {
-                for (uint32_t i = 0; i < S::kStages && i < fills; ++i) {
-                    const uint32_t f = fills - 1 - i;
-                    dev::mbar_wait(smem + S::kFull + 8 * (f % S::kStages), (f / S::kStages) & 1, kWaitTimeoutNs);
+                for (uint32_t i = 0; i < S::kStages; ++i) {
+                    if (!(filled >> i & 1))
+                        continue;
+                    // (stages before `stage` were filled in this round, the others in the one before)
+                    const uint32_t parity = raw >> i & 1 ? (raw_round >> i & 1) ^ 1 : i < stage ? round : round ^ 1;
+                    dev::mbar_wait(smem + (raw >> i & 1 ? S::kRaw : S::kFull) + 8 * i, parity, kWaitTimeoutNs);
                 }
                 for (int t = 0; t < 2; ++t)
                     if (q_used >> t & 1)
                         dev::mbar_wait(smem + S::kQFull + 8 * t, (q_round >> t & 1) ^ 1, kWaitTimeoutNs);
             }
+        } else if (warp == kTailWarp) {
+            // V's rows behind the last key an item sees become zeros, once they have landed.
+            uint32_t stage = 0, raw_round = 0;
+            bool ok = true;
+            do {
+                int a, b;
+                if (!walk.part(a, b) || b == a)
+                    continue;
+                const int keys = walk.it.seen - (b - 1) * kKeys;  // of the last tile
+                stage = (stage + 2 * (uint32_t)(b - a) - 1) % S::kStages;  // its V
+                if (keys < kKeys) {
+                    ok = wait_all(smem + S::kRaw + 8 * stage, raw_round >> stage & 1, PA_DEVERR_TIMEOUT_FULL);
+                    if (!ok)
+                        break;
+                    raw_round ^= 1u << stage;
+                    constexpr int kVecs = D / 8;
+                    for (int i = keys * kVecs + lane; i < kKeys * kVecs; i += 32) {
+                        const int r = i / kVecs, x = i % kVecs;
+                        *reinterpret_cast<uint4 *>(smem_ptr + S::kRing + stage * S::kTileBytes + r / B * (B * 128 * kChunks) +
+                                                   x / 8 * (B * 128) + r % B * 128 + (((x % 8) ^ (r & 7)) << 4)) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+                    fence_async_proxy();
+                    __syncwarp();
+                    if (lane == 0)
+                        dev::mbar_arrive(smem + S::kFull + 8 * stage);
+                    __syncwarp();
+                }
+                if (++stage == S::kStages)
+                    stage = 0;
+            } while (ok && walk.next() && walk.inside());
         } else if (warp == kMmaWarp) {
             // The whole warp goes through the loop, so that addresses and descriptors stay in uniform
             // registers; one lane issues.  (With one thread alone in the loop each product took 75
@@ -467,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         const int t = warp >> 2;              // row tile
         const int r = tid & (kTileRows - 1);  // row of it: this thread's
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
