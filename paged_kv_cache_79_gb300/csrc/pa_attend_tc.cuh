@@ -3,14 +3,14 @@
 // An item has two tiles of 128 rows (rows: query tokens times heads of a group) that step
 // through the same keys, 128 at a time.  Per CTA, one per SM:
 //   warp 8       loader: per tile of keys one TMA copy for each cache block and 128-byte
-//                column of K, then one for each block of V, into a ring; Q's rows with TMA too.
-//                Block ids are read a window of 32 ahead, the next item's first ones while this
+//                column of K, then one for each block of V, into a ring.  Block ids are read a window of 32 ahead, the next item's first ones while this
 //                one's tiles are copied (a read takes longer than a tile when DRAM is busy);
 //   warp 10      makes the rows behind the last key that an item sees zeros in V (a weight of
 //                0 times what a stale row holds would be NaN where that is NaN);
 //   warp 9       products, issued by one thread: S = Q K^T into TMEM (operands in shared
 //                memory), O += P V with P read from TMEM;
-//   (warp 11 only fills up its warpgroup, which hands its registers on)
+//   warp 11      walks through the CTA's share, hands the items on to the others and copies
+//                Q's rows with TMA;
 //   warps 0..3   softmax of the first row tile, warps 4..7 of the second: a thread has a row.
 //                It reads its 128 scores from TMEM, writes its probabilities over them as
 //                fp16/bf16, and keeps the row's maximum and sum.
@@ -34,6 +34,7 @@ constexpr int kThreads = 384;
 constexpr int kLoaderWarp = 8;
 constexpr int kMmaWarp = 9;
 constexpr int kTailWarp = 10;
+constexpr int kQueryWarp = 11;
 constexpr int kTileRows = 128;
 constexpr int kKeys = 128;
 constexpr int kChunkBytes = kKeys * 128;   // 128 rows of 128 bytes: one column of a tile
@@ -41,6 +42,25 @@ constexpr float kRescale = 8.0f;           // growth of a maximum (log2) that th
 constexpr float kFar = 1048576.0f;         // bases (log2) from which on products are rounded first
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;            // O of the row tiles, behind their S (128 columns each)
+
+// An item, or a part of one, as the warps need it.  One warp walks through the stream and hands
+// the items on through shared memory: each step takes thousands of cycles (64-bit divisions, the
+// lengths of the next sequence), which every role would else wait for at every item.
+struct alignas(16) Item {
+    int s;                // sequence
+    int seen;             // keys that the last token sees
+    int a, b;             // tiles of keys
+    int token0, tokens;   // query tokens (rows of q)
+    int head0, heads;     // query heads
+    int kv;               // kv head
+    int T;                // keys of the sequence
+    int own;              // causal: keys that the first token sees (may be below 0)
+    int whole;            // all of the item's tiles; 0: partial rows
+    int valid;            // 0: no more
+    int unused[3];
+};
+constexpr int kItems = 4;                             // handed on ahead
+constexpr int kItemReaders = 8 + 3;                   // warps that read them
 
 template <int D>
 struct Smem {
@@ -52,8 +72,10 @@ struct Smem {
     static constexpr int kFull = kBars, kEmpty = kFull + 8 * kStages, kRaw = kEmpty + 8 * kStages,
                          kQFull = kRaw + 8 * kStages,
                          kQEmpty = kQFull + 16, kSFull = kQEmpty + 16, kPFull = kSFull + 16, kODone = kPFull + 16,
-                         kDrain = kODone + 16, kTmem = kDrain + 8, kAbort = kTmem + 4, kScratch = kAbort + 4,
-                         kEnd = kScratch + 8 * (kThreads / 32 + 4);
+                         kItemFull = kODone + 16, kItemEmpty = kItemFull + 8 * kItems,
+                         kDrain = kItemEmpty + 8 * kItems, kTmem = kDrain + 8, kAbort = kTmem + 4, kScratch = kAbort + 4,
+                         kSlots = (kScratch + 8 * (kThreads / 32 + 4) + 15) / 16 * 16,
+                         kEnd = kSlots + kItems * (int)sizeof(Item);
     static constexpr int kBytes = kEnd + 1024;                // slack to align the base
     static_assert(kBytes <= 232448, "one CTA's shared memory");
 };
@@ -128,6 +150,25 @@ __device__ __forceinline__ void wait_ld(uint32_t (&r)[32])
                    "+r"(r[30]), "+r"(r[31])::"memory");
 }
 
+// N consecutive words of a row, 32 bytes (whole sectors) at a time where the address allows it.
+template <int N>
+__device__ __forceinline__ void store_words(void *dst, const uint32_t (&w)[N], bool wide)
+{
+    if (wide) {
+#pragma unroll
+        for (int i = 0; i < N; i += 8)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                             static_cast<uint32_t *>(dst) + i),
+                         "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]), "r"(w[i + 5]),
+                         "r"(w[i + 6]), "r"(w[i + 7])
+                         : "memory");
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+            static_cast<uint4 *>(dst)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    }
+}
+
 // Two fp32 operations at a time, and the larger of three.
 __device__ __forceinline__ unsigned long long bits(float2 x)
 {
@@ -200,6 +241,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     if (tid == 0) {
+        dev::tma_prefetch_desc(&map_q);
+        dev::tma_prefetch_desc(&map_k);
+        dev::tma_prefetch_desc(&map_v);
         for (int i = 0; i < S::kStages; ++i) {
             dev::mbar_init(smem + S::kFull + 8 * i, 1);
             dev::mbar_init(smem + S::kEmpty + 8 * i, 1);
@@ -211,6 +255,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             dev::mbar_init(smem + S::kSFull + 8 * t, 1);
             dev::mbar_init(smem + S::kPFull + 8 * t, kTileRows / 32);  // a warp each
             dev::mbar_init(smem + S::kODone + 8 * t, 1);
+        }
+        for (int i = 0; i < kItems; ++i) {
+            dev::mbar_init(smem + S::kItemFull + 8 * i, 1);
+            dev::mbar_init(smem + S::kItemEmpty + 8 * i, kItemReaders);
         }
         dev::mbar_init(smem + S::kDrain, 1);
         *abort = 0;
@@ -243,68 +291,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         return __all_sync(0xffffffffu, wait(bar, parity, flag)) != 0;
     };
 
+    // The next item for a warp that reads them in turn (`turn`: how many it has read).
+    Item *const slots = reinterpret_cast<Item *>(smem_ptr + S::kSlots);
+    auto next_item = [&](Item &it, uint32_t &turn) {
+        const uint32_t i = turn % kItems;
+        if (!wait_all(smem + S::kItemFull + 8 * i, turn / kItems & 1, PA_DEVERR_TIMEOUT_FULL))
+            return false;
+        it = slots[i];
+        __syncwarp();
+        if (lane == 0)
+            dev::mbar_arrive(smem + S::kItemEmpty + 8 * i);
+        ++turn;
+        return it.valid != 0;
+    };
+
     // The softmax warps hold 128 scores a thread: 168 registers each at launch (three warps per
     // scheduler) become 2 x 200 and 104.
     if (warp >= kLoaderWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         if (warp == kLoaderWarp) {
-            uint32_t stage = 0, round = 0, q_round = 0;  // parities of the ring, of Q (bit t: row tile t)
-            uint32_t filled = 0, raw = 0, raw_round = 0; // bits: stages filled, filled with a tail, its parity
-            uint32_t q_used = 0;
+            uint32_t stage = 0, round = 0;                // of the ring
+            uint32_t filled = 0, raw = 0, raw_round = 0;  // bits: stages filled, filled with a tail, its parity
             bool ok = true;
-            const uint32_t q_bytes = (uint32_t)(half_tokens * p.heads_per_item) * 128u * kChunks;
             // The blocks of 32 / kBlocks tiles from `tile` on, one per lane (past the last that is seen, or
             // outside the pool: past the pool's end, where a copy brings zeros).
             constexpr int kWindow = 32 / kBlocks;
-            auto window = [&](const AttendItem &it, int tile, int end) {
+            auto window = [&](const Item &it, int tile) {
                 const int j = tile * kBlocks + lane;
                 int id = -1;
-                if (j < min((it.seen + B - 1) / B, end * kBlocks))
+                if (j < min((it.seen + B - 1) / B, it.b * kBlocks))
                     id = p.block_tables[(size_t)it.s * p.max_blocks + j];
                 return id >= 0 && id < p.num_blocks ? id : p.num_blocks;
             };
-            int a, b;
-            bool there = false;  // an item with tiles of this CTA
-            int ahead = 0;       // its first window
-            auto find = [&](bool more) {
-                for (there = false; more; more = walk.next() && walk.inside())
-                    if (walk.part(a, b) && b > a) {
-                        there = true;
-                        ahead = window(walk.it, a, b);
-                        return;
-                    }
-            };
-            find(true);
-            while (there && ok) {
-                const AttendItem it = walk.it;
-                const auto rows = Walk::rows_of(p, it);
-                const int from = a, end = b;
-                int id = ahead, id_next = window(it, from + kWindow, end);
-                // the next item's blocks are read while this one's are copied
-                find(walk.next() && walk.inside());
-                const bool two = rows.tokens > half_tokens;
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (!ok || (t == 1 && !two))
-                        break;
-                    ok = wait_all(smem + S::kQEmpty + 8 * t, (q_round >> t & 1) ^ 1, PA_DEVERR_TIMEOUT_EMPTY);
-                    if (!ok)
-                        break;
-                    if (elect_one()) {
-                        const uint32_t bar = smem + S::kQFull + 8 * t;
-                        dev::mbar_arrive_expect_tx(bar, q_bytes);
-#pragma unroll
-                        for (int c = 0; c < kChunks; ++c)
-                            dev::tma_load_4d(smem + t * S::kTileBytes + c * kChunkBytes, &map_q, 0, rows.head0,
-                                             rows.token0 + t * half_tokens, c, bar);
-                    }
-                    __syncwarp();
-                    q_round ^= 1u << t;
-                    q_used |= 1u << t;
-                }
-                const int kv_head = __shfl_sync(0xffffffffu, rows.kv, 0);
+            Item it;
+            uint32_t turn = 0;
+            while (ok && next_item(it, turn)) {
+                if (it.a == it.b)
+                    continue;
+                int id = window(it, it.a), id_next = window(it, it.a + kWindow);
+                const int kv_head = __shfl_sync(0xffffffffu, it.kv, 0);
                 int slot = 0;  // of the window
-                for (int tile = from; tile < end && ok; ++tile) {
+                for (int tile = it.a; tile < it.b && ok; ++tile) {
                     int ids[kBlocks];
 #pragma unroll
                     for (int i = 0; i < kBlocks; ++i)
@@ -312,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (++slot == kWindow) {
                         slot = 0;
                         id = id_next;
-                        id_next = window(it, tile + 1 + kWindow, end);
+                        id_next = window(it, tile + 1 + kWindow);
                     }
                     const int keys = __shfl_sync(0xffffffffu, min(it.seen - tile * kKeys, kKeys), 0);  // of this tile
                     const int copies = (keys + B - 1) / B;
@@ -362,20 +389,80 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t parity = raw >> i & 1 ? (raw_round >> i & 1) ^ 1 : i < stage ? round : round ^ 1;
                     dev::mbar_wait(smem + (raw >> i & 1 ? S::kRaw : S::kFull) + 8 * i, parity, kWaitTimeoutNs);
                 }
+            }
+        } else if (warp == kQueryWarp) {
+            uint32_t q_round = 0, q_used = 0;  // bit t: row tile t
+            uint32_t turn = 0;
+            bool ok = true;
+            const uint32_t q_bytes = (uint32_t)(half_tokens * p.heads_per_item) * 128u * kChunks;
+            auto hand_on = [&](const Item &it) {
+                const uint32_t i = turn % kItems;
+                ok = wait_all(smem + S::kItemEmpty + 8 * i, (turn / kItems & 1) ^ 1, PA_DEVERR_TIMEOUT_EMPTY);
+                if (ok && lane == 0) {
+                    slots[i] = it;
+                    dev::mbar_arrive(smem + S::kItemFull + 8 * i);
+                }
+                __syncwarp();
+                ++turn;
+            };
+            do {
+                Item it;
+                if (!walk.part(it.a, it.b))
+                    continue;
+                const auto rows = Walk::rows_of(p, walk.it);
+                it.s = walk.it.s;
+                it.seen = walk.it.seen;
+                it.token0 = rows.token0;
+                it.tokens = rows.tokens;
+                it.head0 = rows.head0;
+                it.heads = rows.heads;
+                it.kv = rows.kv;
+                it.T = walk.it.T;
+                it.own = walk.it.T - walk.it.n + walk.it.j * p.tokens_per_item + 1;
+                it.whole = it.a == 0 && it.b == walk.it.tiles;
+                it.valid = 1;
+                hand_on(it);
+                if (it.a == it.b)
+                    continue;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (!ok || (t == 1 && rows.tokens <= half_tokens))
+                        break;
+                    ok = wait_all(smem + S::kQEmpty + 8 * t, (q_round >> t & 1) ^ 1, PA_DEVERR_TIMEOUT_EMPTY);
+                    if (!ok)
+                        break;
+                    if (elect_one()) {
+                        const uint32_t bar = smem + S::kQFull + 8 * t;
+                        dev::mbar_arrive_expect_tx(bar, q_bytes);
+#pragma unroll
+                        for (int c = 0; c < kChunks; ++c)
+                            dev::tma_load_4d(smem + t * S::kTileBytes + c * kChunkBytes, &map_q, 0, rows.head0,
+                                             rows.token0 + t * half_tokens, c, bar);
+                    }
+                    __syncwarp();
+                    q_round ^= 1u << t;
+                    q_used |= 1u << t;
+                }
+            } while (ok && walk.next() && walk.inside());
+            if (ok) {
+                Item none = {};
+                hand_on(none);
+            }
+            if (*abort) {
                 for (int t = 0; t < 2; ++t)
                     if (q_used >> t & 1)
                         dev::mbar_wait(smem + S::kQFull + 8 * t, (q_round >> t & 1) ^ 1, kWaitTimeoutNs);
             }
         } else if (warp == kTailWarp) {
             // V's rows behind the last key an item sees become zeros, once they have landed.
-            uint32_t stage = 0, raw_round = 0;
+            uint32_t stage = 0, raw_round = 0, turn = 0;
             bool ok = true;
-            do {
-                int a, b;
-                if (!walk.part(a, b) || b == a)
+            Item it;
+            while (ok && next_item(it, turn)) {
+                if (it.a == it.b)
                     continue;
-                const int keys = walk.it.seen - (b - 1) * kKeys;  // of the last tile
-                stage = (stage + 2 * (uint32_t)(b - a) - 1) % S::kStages;  // its V
+                const int keys = it.seen - (it.b - 1) * kKeys;  // of the last tile
+                stage = (stage + 2 * (uint32_t)(it.b - it.a) - 1) % S::kStages;  // its V
                 if (keys < kKeys) {
                     ok = wait_all(smem + S::kRaw + 8 * stage, raw_round >> stage & 1, PA_DEVERR_TIMEOUT_FULL);
                     if (!ok)
@@ -396,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (++stage == S::kStages)
                     stage = 0;
-            } while (ok && walk.next() && walk.inside());
+            }
         } else if (warp == kMmaWarp) {
             // The whole warp goes through the loop, so that addresses and descriptors stay in uniform
             // registers; one lane issues.  (With one thread alone in the loop each product took 75
@@ -432,13 +519,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
             };
-            do {
-                int a, b;
-                if (!walk.part(a, b) || b == a)
+            Item it;
+            uint32_t turn = 0;
+            while (ok && next_item(it, turn)) {
+                const bool two = __shfl_sync(0xffffffffu, it.tokens > half_tokens ? 1 : 0, 0) != 0;
+                const int n = __shfl_sync(0xffffffffu, it.b - it.a, 0);
+                if (n == 0)
                     continue;
-                const auto rows = Walk::rows_of(p, walk.it);
-                const bool two = __shfl_sync(0xffffffffu, rows.tokens > half_tokens ? 1 : 0, 0) != 0;
-                const int n = __shfl_sync(0xffffffffu, b - a, 0);
                 ok = wait_all(smem + S::kFull + 8 * stage, round, PA_DEVERR_TIMEOUT_FULL);
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
@@ -489,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (more)
                         advance();
                 }
-            } while (ok && walk.next() && walk.inside());
+            }
             // every product has completed before the CTA gives its memory back
             if (elect_one())
                 commit(smem + S::kDrain);
@@ -506,23 +593,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t steps = 0, parts = 0;
         bool ok = true;
         const int tok = r / p.heads_per_item, head = r - tok * p.heads_per_item;
-        do {
-            int a, b;
-            if (!walk.part(a, b))
+        const bool wide = ((reinterpret_cast<uintptr_t>(p.out) | reinterpret_cast<uintptr_t>(p.part_o)) & 31) == 0;
+        Item it;
+        uint32_t turn = 0;
+        while (ok && next_item(it, turn)) {
+            if (t * half_tokens >= it.tokens)
                 continue;
-            const AttendItem &it = walk.it;
-            const auto rows = Walk::rows_of(p, it);
-            if (t * half_tokens >= rows.tokens)
-                continue;
+            const int a = it.a, b = it.b;
             const int my_tok = t * half_tokens + tok;  // of the item
-            const bool mine = tok < half_tokens && my_tok < rows.tokens && head < rows.heads;
-            const size_t row = (size_t)(rows.token0 + my_tok) * p.num_q_heads + rows.head0 + head;
+            const bool mine = tok < half_tokens && my_tok < it.tokens && head < it.heads;
+            const size_t row = (size_t)(it.token0 + my_tok) * p.num_q_heads + it.head0 + head;
             // keys that this row sees, and that every row of the tile sees
             int limit = it.T, common = it.T;
             if (p.causal) {
-                const long long own = (long long)it.T - it.n + it.j * (long long)p.tokens_per_item + 1;
-                limit = (int)min(max(own + my_tok, 0ll), (long long)it.T);
-                common = (int)min(max(own + t * half_tokens, 0ll), (long long)it.T);
+                limit = min(max(it.own + my_tok, 0), it.T);
+                common = min(max(it.own + t * half_tokens, 0), it.T);
             }
             float m = -INFINITY, l = 0.f;  // the base in use, the sum
             bool far = false;
@@ -644,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok)
                 break;
-            const bool whole = a == 0 && b == it.tiles;
+            const bool whole = it.whole != 0;
             if (b > a) {
                 ok = wait_all(smem + S::kODone + 8 * t, parts & 1, PA_DEVERR_TIMEOUT_FULL);
                 if (!ok)
@@ -662,22 +747,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     wait_ld(o);
                 }
                 if (mine && whole) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + row * D + c);
+                    uint32_t w[16];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            w[e] = b > a ? dev::Mma<T>::pack(__uint_as_float(o[8 * k + 2 * e]) * inv,
-                                                             __uint_as_float(o[8 * k + 2 * e + 1]) * inv)
-                                         : 0u;
-                        dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
+                    for (int k = 0; k < 16; ++k)
+                        w[k] = b > a ? dev::Mma<T>::pack(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv)
+                                     : 0u;
+                    store_words(static_cast<T *>(p.out) + row * D + c, w, wide);
                 } else if (mine) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.part_o + part * D + c);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                    store_words(p.part_o + part * D + c, o, wide);
                 }
                 __syncwarp();
             }
@@ -686,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
             if (mine && !whole)
                 p.part_ml[part] = make_float2(m, l);
-        } while (walk.next() && walk.inside());
+        }
     }
     fence_before();
     __syncthreads();
