@@ -19,8 +19,13 @@
 namespace pagedkv {
 
 constexpr int kAttendRows = 256;     // rows of an item at most
-constexpr int kAttendCharge = 192;   // an item's fixed cost, in keys
-constexpr int kAttendMinShare = 192; // cost per CTA at least: no two short items on one CTA while others idle
+// An item's fixed cost, in keys: a tile of 128 takes 1.4 us, an item 2.4 to 3.8 us more.
+constexpr int kAttendCharge = 320;
+// A share's cost at least.  It is at least a tile of any item that can be cut (two tiles or more:
+// charge + 2 * 128 <= 2 * 320), so two cuts of an item never fall on the same tile and every CTA
+// between them has a part.
+constexpr int kAttendMinShare = 320;
+static_assert(kAttendCharge + 2 * 128 <= 2 * kAttendMinShare, "a part for every CTA");
 constexpr int kF32TileRows = 64;     // rows of an item of the fp32 kernel
 
 struct AttendItem {
@@ -62,18 +67,25 @@ struct AttendWalk {
         const long long last = min((long long)n, (long long)(j + 1) * p.tokens_per_item);
         return (int)max((long long)T - n + last, 0ll);
     }
-    // Cost of runs 0 .. j - 1 of one unit of the sequence.
+    // Cost of run j, which sees `seen` keys; one of few tokens goes through its keys twice as fast.
+    static __device__ __forceinline__ long long cost_of(const AttendParams &p, int n, int j, int seen)
+    {
+        const bool few = n - (long long)j * p.tokens_per_item <= p.few_tokens;
+        return kAttendCharge + (few ? ((long long)seen + 1) / 2 : (long long)seen);
+    }
+    // Cost of runs 0 .. j - 1 of one unit of the sequence.  (All but the last are whole.)
     static __device__ __forceinline__ long long before(const AttendParams &p, int n, int T, int j)
     {
-        const long long fixed = (long long)j * kAttendCharge;
+        const long long t = p.tokens_per_item;
+        const bool all = j > 0 && (long long)j * t >= n;  // the last run is among them
+        const int full = all ? j - 1 : j;
+        long long sum = (long long)full * kAttendCharge + (all ? cost_of(p, n, j - 1, T) : 0);
         if (!p.causal)
-            return fixed + (long long)j * T;
-        const long long t = p.tokens_per_item, over = (long long)T - n;
-        const bool all = j > 0 && (long long)j * t >= n;  // the last run may be short
-        const long long full = all ? j - 1 : j;
-        const long long i0 = over >= 0 ? 0 : min(-over / t, full);
+            return sum + (long long)full * T;
+        const long long over = (long long)T - n;
+        const long long i0 = over >= 0 ? 0 : min(-over / t, (long long)full);
         const long long m = full - i0;
-        return fixed + m * over + t * ((i0 + 1 + full) * m / 2) + (all ? T : 0);
+        return sum + m * over + t * ((i0 + 1 + full) * m / 2);
     }
 
     __device__ __forceinline__ void set(int s, int u, int j, int q0, int n, int T, long long at)
@@ -87,7 +99,7 @@ struct AttendWalk {
         it.at = at;
         it.seen = seen_by(p, n, T, j);
         it.tiles = (it.seen + kKeys - 1) / kKeys;
-        it.cost = (long long)it.seen + kAttendCharge;
+        it.cost = cost_of(p, n, j, it.seen);
     }
     // The next item of the stream; false behind the last.
     __device__ __forceinline__ bool next()

@@ -159,6 +159,7 @@ pa_status pa_attend(void *out, float *lse, const void *q, long long q_stride, co
     p.head_chunks = (p.group + p.heads_per_item - 1) / p.heads_per_item;
     p.units = num_kv_heads * p.head_chunks;
     p.tokens_per_item = tile / p.heads_per_item * (f32 ? 1 : 2);
+    p.few_tokens = f32 ? 0 : p.tokens_per_item / 2;
     p.part_rows = f32 ? kF32TileRows : kAttendRows;
     L.ctas = f32 ? 2 * sms : sms;
     if (!f32 &&

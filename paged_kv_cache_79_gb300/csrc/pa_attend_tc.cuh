@@ -56,8 +56,9 @@ struct alignas(16) Item {
     int T;                // keys of the sequence
     int own;              // causal: keys that the first token sees (may be below 0)
     int whole;            // all of the item's tiles; 0: partial rows
+    int dual;             // one row tile: both softmax groups take its tiles of keys in turn
     int valid;            // 0: no more
-    int unused[3];
+    int unused[2];
 };
 constexpr int kItems = 4;                             // handed on ahead
 constexpr int kItemReaders = 8 + 3;                   // warps that read them
@@ -72,10 +73,11 @@ struct Smem {
     static constexpr int kFull = kBars, kEmpty = kFull + 8 * kStages, kRaw = kEmpty + 8 * kStages,
                          kQFull = kRaw + 8 * kStages,
                          kQEmpty = kQFull + 16, kSFull = kQEmpty + 16, kPFull = kSFull + 16, kODone = kPFull + 16,
-                         kItemFull = kODone + 16, kItemEmpty = kItemFull + 8 * kItems,
+                         kPair = kODone + 16, kPairFree = kPair + 8, kItemFull = kPairFree + 8, kItemEmpty = kItemFull + 8 * kItems,
                          kDrain = kItemEmpty + 8 * kItems, kTmem = kDrain + 8, kAbort = kTmem + 4, kScratch = kAbort + 4,
                          kSlots = (kScratch + 8 * (kThreads / 32 + 4) + 15) / 16 * 16,
-                         kEnd = kSlots + kItems * (int)sizeof(Item);
+                         kPairRows = kSlots + kItems * (int)sizeof(Item),
+                         kEnd = kPairRows + kTileRows * 8;
     static constexpr int kBytes = kEnd + 1024;                // slack to align the base
     static_assert(kBytes <= 232448, "one CTA's shared memory");
 };
@@ -256,6 +258,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             dev::mbar_init(smem + S::kPFull + 8 * t, kTileRows / 32);  // a warp each
             dev::mbar_init(smem + S::kODone + 8 * t, 1);
         }
+        dev::mbar_init(smem + S::kPair, kTileRows / 32);
+        dev::mbar_init(smem + S::kPairFree, kTileRows / 32);
         for (int i = 0; i < kItems; ++i) {
             dev::mbar_init(smem + S::kItemFull + 8 * i, 1);
             dev::mbar_init(smem + S::kItemEmpty + 8 * i, kItemReaders);
@@ -420,13 +424,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 it.T = walk.it.T;
                 it.own = walk.it.T - walk.it.n + walk.it.j * p.tokens_per_item + 1;
                 it.whole = it.a == 0 && it.b == walk.it.tiles;
+                it.dual = rows.tokens <= half_tokens && it.b - it.a > 1;
                 it.valid = 1;
                 hand_on(it);
                 if (it.a == it.b)
                     continue;
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    if (!ok || (t == 1 && rows.tokens <= half_tokens))
+                    if (!ok || (t == 1 && rows.tokens <= half_tokens && !it.dual))
                         break;
                     ok = wait_all(smem + S::kQEmpty + 8 * t, (q_round >> t & 1) ^ 1, PA_DEVERR_TIMEOUT_EMPTY);
                     if (!ok)
@@ -437,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int c = 0; c < kChunks; ++c)
                             dev::tma_load_4d(smem + t * S::kTileBytes + c * kChunkBytes, &map_q, 0, rows.head0,
-                                             rows.token0 + t * half_tokens, c, bar);
+                                             rows.token0 + (it.dual ? 0 : t * half_tokens), c, bar);
                     }
                     __syncwarp();
                     q_round ^= 1u << t;
@@ -493,19 +498,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             // (Scalars only: an array indexed by the row tile would live in local memory, and each wait
             // would cost hundreds of cycles more.)
             uint32_t q_round = 0, p_round = 0;  // bit t: parity of row tile t
-            uint32_t stage = 0, round = 0;      // of the ring
+            uint32_t fills = 0;                 // of the ring, before this item: its K and V in turn
             bool ok = true;
             const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
-            auto advance = [&]() {
-                if (++stage == S::kStages) {
-                    stage = 0;
-                    round ^= 1;
-                }
+            auto full = [&](uint32_t f) {
+                return wait_all(smem + S::kFull + 8 * (f % S::kStages), f / S::kStages & 1, PA_DEVERR_TIMEOUT_FULL);
             };
-            auto scores = [&](int t, uint32_t k_stage, bool last_keys, bool release) {
+            // S of row tile t from fill f
+            auto scores = [&](int t, uint32_t f, bool last_keys, bool release) {
+                const uint32_t stage = f % S::kStages;
                 if (elect_one()) {
                     const uint64_t q = operand(smem + t * S::kTileBytes, 16, 1024);
-                    const uint64_t k0 = operand(smem + S::kRing + k_stage * S::kTileBytes, 16, 1024);
+                    const uint64_t k0 = operand(smem + S::kRing + stage * S::kTileBytes, 16, 1024);
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         const uint32_t off = ((k / 4) * kChunkBytes + (k % 4) * 32) >> 4;
@@ -515,67 +519,98 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (last_keys)
                         commit(smem + S::kQEmpty + 8 * t);
                     if (release)
-                        commit(smem + S::kEmpty + 8 * k_stage);
+                        commit(smem + S::kEmpty + 8 * stage);
                 }
                 __syncwarp();
+            };
+            // O of row tile t, once its probabilities are there, from fill f
+            auto output = [&](int t, uint32_t f, bool first, bool last_keys, bool release) {
+                if (!wait_all(smem + S::kPFull + 8 * t, p_round >> t & 1, PA_DEVERR_TIMEOUT_FULL))
+                    return false;
+                p_round ^= 1u << t;
+                fence_after();
+                const uint32_t stage = f % S::kStages;
+                if (elect_one()) {
+                    const uint64_t v = operand(smem + S::kRing + stage * S::kTileBytes, B * 128, 1024);
+                    mma_ts(base + kColO + t * D, base + t * kKeys, v, kOutput, !first);
+#pragma unroll
+                    for (int k = 1; k < kKeys / 16; ++k) {
+                        const uint32_t off = (k * 16 / B * (B * 128 * kChunks) + k * 16 % B * 128) >> 4;
+                        mma_ts(base + kColO + t * D, base + t * kKeys + 8 * k, v + off, kOutput, true);
+                    }
+                    if (last_keys)
+                        commit(smem + S::kODone + 8 * t);
+                    if (release)
+                        commit(smem + S::kEmpty + 8 * stage);
+                }
+                __syncwarp();
+                return true;
+            };
+            auto queries = [&](int t) {
+                const bool r = wait_all(smem + S::kQFull + 8 * t, q_round >> t & 1, PA_DEVERR_TIMEOUT_FULL);
+                q_round ^= 1u << t;
+                return r;
             };
             Item it;
             uint32_t turn = 0;
             while (ok && next_item(it, turn)) {
                 const bool two = __shfl_sync(0xffffffffu, it.tokens > half_tokens ? 1 : 0, 0) != 0;
+                const bool dual = __shfl_sync(0xffffffffu, it.dual, 0) != 0;
                 const int n = __shfl_sync(0xffffffffu, it.b - it.a, 0);
                 if (n == 0)
                     continue;
-                ok = wait_all(smem + S::kFull + 8 * stage, round, PA_DEVERR_TIMEOUT_FULL);
+                if (dual) {
+                    // tile j is row tile j % 2's; K of tile j is fill 2 j, V fill 2 j + 1
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (!ok || (t == 1 && !two))
-                        break;
-                    ok = wait_all(smem + S::kQFull + 8 * t, q_round >> t & 1, PA_DEVERR_TIMEOUT_FULL);
-                    if (!ok)
-                        break;
-                    q_round ^= 1u << t;
-                    scores(t, stage, n == 1, t == 1 || !two);
-                }
-                advance();
-                for (int j = 0; j < n && ok; ++j) {
-                    const uint32_t v_stage = stage;
-                    ok = wait_all(smem + S::kFull + 8 * stage, round, PA_DEVERR_TIMEOUT_FULL);
-                    advance();
-                    const bool more = j + 1 < n;  // `stage`: the next tile's K
+                    for (int t = 0; t < 2; ++t) {
+                        ok = ok && full(fills + 2 * t) && queries(t);
+                        if (ok)
+                            scores(t, fills + 2 * t, t + 2 >= n, true);
+                    }
+                    for (int j = 0; j < n && ok; j += 2) {
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            if (!ok || j + t >= n)
+                                break;
+                            const uint32_t f = fills + 2 * (j + t);
+                            const bool more = j + t + 2 < n;
+                            ok = full(f + 1) && output(t, f + 1, j == 0, !more, true);
+                            if (ok && more) {
+                                ok = full(f + 4);
+                                if (ok)
+                                    scores(t, f + 4, j + t + 4 >= n, true);
+                            }
+                        }
+                    }
+                } else {
+                    ok = full(fills);
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         if (!ok || (t == 1 && !two))
                             break;
-                        ok = wait_all(smem + S::kPFull + 8 * t, p_round >> t & 1, PA_DEVERR_TIMEOUT_FULL);
-                        if (!ok)
-                            break;
-                        p_round ^= 1u << t;
-                        fence_after();
-                        if (elect_one()) {
-                            const uint64_t v = operand(smem + S::kRing + v_stage * S::kTileBytes, B * 128, 1024);
-                            mma_ts(base + kColO + t * D, base + t * kKeys, v, kOutput, j > 0);
-#pragma unroll
-                            for (int k = 1; k < kKeys / 16; ++k) {
-                                const uint32_t off = (k * 16 / B * (B * 128 * kChunks) + k * 16 % B * 128) >> 4;
-                                mma_ts(base + kColO + t * D, base + t * kKeys + 8 * k, v + off, kOutput, true);
-                            }
-                            if (!more)
-                                commit(smem + S::kODone + 8 * t);
-                            if (t == 1 || !two)
-                                commit(smem + S::kEmpty + 8 * v_stage);
-                        }
-                        __syncwarp();
-                        if (!more)
-                            continue;
-                        if (t == 0)
-                            ok = wait_all(smem + S::kFull + 8 * stage, round, PA_DEVERR_TIMEOUT_FULL);
+                        ok = queries(t);
                         if (ok)
-                            scores(t, stage, j + 2 == n, t == 1 || !two);
+                            scores(t, fills, n == 1, t == 1 || !two);
                     }
-                    if (more)
-                        advance();
+                    for (int j = 0; j < n && ok; ++j) {
+                        const uint32_t f = fills + 2 * j;
+                        const bool more = j + 1 < n;
+                        ok = full(f + 1);
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            if (!ok || (t == 1 && !two))
+                                break;
+                            ok = output(t, f + 1, j == 0, !more, t == 1 || !two);
+                            if (!ok || !more)
+                                continue;
+                            if (t == 0)
+                                ok = full(f + 2);
+                            if (ok)
+                                scores(t, f + 2, j + 2 == n, t == 1 || !two);
+                        }
+                    }
                 }
+                fills += 2 * n;
             }
             // every product has completed before the CTA gives its memory back
             if (elect_one())
@@ -591,27 +626,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         const uint32_t s_at = tmem + lanes + t * kKeys, o_at = tmem + lanes + kColO + t * D;
         uint32_t steps = 0, parts = 0;
+        uint32_t o1_round = 0, pair_round = 0, free_round = 0;
+        bool lent = false;
+        float2 *const pair_rows = reinterpret_cast<float2 *>(smem_ptr + S::kPairRows);
         bool ok = true;
         const int tok = r / p.heads_per_item, head = r - tok * p.heads_per_item;
         const bool wide = ((reinterpret_cast<uintptr_t>(p.out) | reinterpret_cast<uintptr_t>(p.part_o)) & 31) == 0;
         Item it;
         uint32_t turn = 0;
         while (ok && next_item(it, turn)) {
-            if (t * half_tokens >= it.tokens)
+            const bool any = it.b > it.a, dual = it.dual != 0;
+            const uint32_t o1_now = o1_round;  // parity of the second row tile's output
+            if (any && (dual || it.tokens > half_tokens))
+                o1_round ^= 1;
+            if (!dual && t * half_tokens >= it.tokens)
                 continue;
-            const int a = it.a, b = it.b;
-            const int my_tok = t * half_tokens + tok;  // of the item
+            if (lent) {  // the other group has read the output that this one left it
+                ok = wait_all(smem + S::kPairFree, free_round, PA_DEVERR_TIMEOUT_FULL);
+                if (!ok)
+                    break;
+                free_round ^= 1;
+                lent = false;
+            }
+            const int row0 = dual ? 0 : t * half_tokens;  // first token of the row tile
+            const int step = dual ? 2 : 1, a = it.a + (dual ? t : 0), b = it.b;
+            const int my_tok = row0 + tok;  // of the item
             const bool mine = tok < half_tokens && my_tok < it.tokens && head < it.heads;
             const size_t row = (size_t)(it.token0 + my_tok) * p.num_q_heads + it.head0 + head;
             // keys that this row sees, and that every row of the tile sees
             int limit = it.T, common = it.T;
             if (p.causal) {
                 limit = min(max(it.own + my_tok, 0), it.T);
-                common = min(max(it.own + t * half_tokens, 0), it.T);
+                common = min(max(it.own + row0, 0), it.T);
             }
             float m = -INFINITY, l = 0.f;  // the base in use, the sum
             bool far = false;
-            for (int tile = a; tile < b; ++tile) {
+            for (int tile = a; tile < b; tile += step) {
                 ok = wait_all(smem + S::kSFull + 8 * t, steps & 1, PA_DEVERR_TIMEOUT_FULL);
                 if (!ok)
                     break;
@@ -730,28 +780,59 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok)
                 break;
             const bool whole = it.whole != 0;
-            if (b > a) {
+            if (dual && t == 1) {
+                // the first group joins the two: it has the same rows, and reads this one's output
+                ++parts;
+                pair_rows[r] = make_float2(m, l);
+                __syncwarp();
+                if (lane == 0)
+                    dev::mbar_arrive(smem + S::kPair);
+                lent = true;
+                continue;
+            }
+            float f0 = 1.f, f1 = 0.f;
+            if (any) {
                 ok = wait_all(smem + S::kODone + 8 * t, parts & 1, PA_DEVERR_TIMEOUT_FULL);
+                if (ok && dual)
+                    ok = wait_all(smem + S::kODone + 8, o1_now, PA_DEVERR_TIMEOUT_FULL) &&
+                         wait_all(smem + S::kPair, pair_round, PA_DEVERR_TIMEOUT_FULL);
                 if (!ok)
                     break;
                 ++parts;
                 fence_after();
+                if (dual) {
+                    pair_round ^= 1;
+                    const float2 other = pair_rows[r];
+                    const float top = fmaxf(m, other.x), ref = top == -INFINITY ? 0.f : top;
+                    f0 = exp2f(m - ref);
+                    f1 = exp2f(other.x - ref);
+                    m = top;
+                    l = l * f0 + other.y * f1;
+                }
             }
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            const size_t part = attend_part_row(p, blockIdx.x, a > 0 ? 0 : 1) + my_tok * p.heads_per_item + head;
-#pragma unroll
+            const size_t part = attend_part_row(p, blockIdx.x, it.a > 0 ? 0 : 1) + my_tok * p.heads_per_item + head;
+#pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
-                if (b > a) {
+                if (any) {
                     tmem_ld32(o, o_at + c);
                     wait_ld(o);
+                    if (dual) {
+                        uint32_t o1[32];
+                        tmem_ld32(o1, o_at + D + c);
+                        wait_ld(o1);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            o[k] = __float_as_uint(__uint_as_float(o[k]) * f0 + __uint_as_float(o1[k]) * f1);
+                    }
                 }
                 if (mine && whole) {
                     uint32_t w[16];
 #pragma unroll
                     for (int k = 0; k < 16; ++k)
-                        w[k] = b > a ? dev::Mma<T>::pack(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv)
-                                     : 0u;
+                        w[k] = any ? dev::Mma<T>::pack(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv)
+                                   : 0u;
                     store_words(static_cast<T *>(p.out) + row * D + c, w, wide);
                 } else if (mine) {
                     store_words(p.part_o + part * D + c, o, wide);
@@ -759,6 +840,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
             }
             fence_before();  // O has been read before the next item's first probabilities are announced
+            if (dual) {
+                __syncwarp();
+                if (lane == 0)
+                    dev::mbar_arrive(smem + S::kPairFree);
+            }
             if (mine && whole && p.lse)
                 p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
             if (mine && !whole)

@@ -262,6 +262,7 @@ struct AttendParams {
     int num_q_heads, num_kv_heads, group;
     int heads_per_item, head_chunks, units;  // units: kv heads * chunks of their groups
     int tokens_per_item;
+    int few_tokens;               // items of up to this many go through their keys at twice the rate
     int part_rows;
     int causal;
 };

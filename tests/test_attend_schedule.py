@@ -7,19 +7,19 @@ import random
 
 import pytest
 
-CHARGE, MIN_SHARE = 192, 192
+CHARGE, MIN_SHARE = 320, 320
 
 
 class Schedule:
-    def __init__(self, lens, units, tokens, keys, causal, grid):
-        self.units, self.t, self.keys, self.causal = units, tokens, keys, causal
+    def __init__(self, lens, units, tokens, keys, causal, grid, few=0):
+        self.units, self.t, self.keys, self.causal, self.few = units, tokens, keys, causal, few
         self.seqs = [(n, T) for n, T in lens]
         self.items, at = [], 0
         for s, (n, T) in enumerate(self.seqs):
             for u in range(units if n else 0):
                 for j in range(self.runs(n)):
                     seen = self.seen(n, T, j)
-                    cost = seen + CHARGE
+                    cost = self.cost_of(n, j, seen)
                     self.items.append((s, u, j, -(-seen // keys), at, cost))
                     at += cost
         self.total = at
@@ -32,16 +32,19 @@ class Schedule:
     def seen(self, n, T, j):
         return max(T - n + min(n, (j + 1) * self.t), 0) if self.causal else T
 
+    def cost_of(self, n, j, seen):
+        return CHARGE + ((seen + 1) // 2 if n - j * self.t <= self.few else seen)
+
     def before(self, n, T, j):
-        fixed = j * CHARGE
-        if not self.causal:
-            return fixed + j * T
-        over = T - n
         every = j > 0 and j * self.t >= n
         full = j - 1 if every else j
+        total = full * CHARGE + (self.cost_of(n, j - 1, T) if every else 0)
+        if not self.causal:
+            return total + full * T
+        over = T - n
         i0 = 0 if over >= 0 else min(-over // self.t, full)
         m = full - i0
-        return fixed + m * over + self.t * ((i0 + 1 + full) * m // 2) + (T if every else 0)
+        return total + m * over + self.t * ((i0 + 1 + full) * m // 2)
 
     def start(self, c):
         q, r = divmod(self.total, self.ctas)
@@ -70,15 +73,16 @@ def random_lens(rng):
     return out
 
 
-@pytest.mark.parametrize("seed", range(60))
+@pytest.mark.parametrize("seed", range(150))
 def test_every_tile_once(seed):
     rng = random.Random(seed)
     lens = random_lens(rng)
-    sch = Schedule(lens, rng.choice([1, 3, 8]), rng.choice([1, 2, 7, 16, 64, 256]), rng.choice([32, 128]),
-                   rng.choice([False, True]), rng.choice([1, 152, 304]))
+    tokens = rng.choice([1, 2, 7, 16, 64, 256])
+    sch = Schedule(lens, rng.choice([1, 3, 8]), tokens, rng.choice([32, 128]), rng.choice([False, True]),
+                   rng.choice([1, 152, 304]), few=rng.choice([0, tokens // 2]))
     for n, T in lens:
         for j in range(sch.runs(n) + 1):
-            assert sch.before(n, T, j) == sum(sch.seen(n, T, i) + CHARGE for i in range(j))
+            assert sch.before(n, T, j) == sum(sch.cost_of(n, i, sch.seen(n, T, i)) for i in range(j))
     shares = [(sch.start(c), sch.start(c + 1)) for c in range(sch.ctas)]
     assert shares[0][0] == 0 and shares[-1][1] == sch.total
     for item in sch.items:
