@@ -368,8 +368,8 @@ pa_status pa_decode_noalloc(void *out, const void *q, const void *k_cache, const
  * bf16: rounded to 2^-12 and 2^-9 of themselves; fp32: two tf32 terms, about 21 bits).  Keys
  * past T are never counted, whatever their rows hold; a table entry outside [0, num_blocks)
  * reads zeros.  A NaN or infinity among the values of a sequence's context can make NaN also
- * of its query tokens that do not see it.  One query token of every sequence is
- * pa_decode's case, which takes half the time; here it may stand among longer ones.
+ * of its query tokens that do not see it.  (One query token of every sequence, all of its keys
+ * seen, is pa_decode's case; here such tokens may stand among longer runs.)
  *
  *   out            device [num_tokens][Hq][d]; rows of q and out from query_start[num_seqs] on
  *                  are padding: not read, and left as they were

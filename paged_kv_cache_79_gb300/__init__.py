@@ -686,7 +686,7 @@ class _Torch:
         import torch
         self.int32, self.int64, self.uint8, self.float32 = torch.int32, torch.int64, torch.uint8, torch.float32
         self.codes = {torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16}
-        self.device = torch.cuda.device
+        self.device, self.empty = torch.cuda.device, torch.empty
         self.current_device = torch._C._cuda_getDevice
         self.current_stream = torch._C._cuda_getCurrentRawStream
 
@@ -977,6 +977,11 @@ def pa_attend_workspace_size(num_q_heads: int, num_kv_heads: int, head_dim: int)
     return n
 
 
+@functools.lru_cache(maxsize=None)
+def _attend_workspace_bytes(dev: int, num_q_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    return pa_attend_workspace_size(num_q_heads, num_kv_heads, head_dim)
+
+
 _ATTEND_NAMES = ("out", "k_cache", "v_cache", "block_tables", "context_lens", "query_start", "lse")
 
 
@@ -1014,8 +1019,9 @@ def pa_attend(out, q, k_cache, v_cache, block_tables, context_lens, query_start,
     _want(q.get_device() == dev, "q must be on the device of out")
     if workspace is None:
         with device or contextlib.nullcontext():
-            workspace = _launch_scratch(pa_attend_workspace_size(num_q_heads, num_kv_heads, head_dim), q.device,
-                                        stream)
+            size = _attend_workspace_bytes(dev, num_q_heads, num_kv_heads, head_dim)
+            workspace = T.empty(size, dtype=T.uint8, device=q.device) if stream is None else _launch_scratch(
+                size, q.device, stream)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous and on the device of q")
     _call("pa_attend", device, out.data_ptr(), None if lse is None else lse.data_ptr(), q.data_ptr(), q_stride,

@@ -1,7 +1,7 @@
 // pa_attend for fp32: mma.sync with each operand in two tf32 terms.
 //
-// Tensor cores take fp32 operands as tf32 (11 significant bits).  x = hi + lo, both rounded to
-// that, leaves a product as hi hi' + hi lo' + lo hi', off by 2^-22 of itself at most,
+// Tensor cores take fp32 operands as tf32 (11 significant bits).  x = hi + lo, hi
+// rounded to that, leaves a product as hi hi' + hi lo' + lo hi', off by 2^-22 of itself at most,
 // accumulated in fp32: three instructions per product.  (tcgen05 takes both operands from shared memory or TMEM as
 // they are, so the split would have to be written there first, four tiles for each one.)
 //
@@ -19,17 +19,12 @@ constexpr int kF32Threads = 128;
 constexpr int kF32Rows = kF32TileRows;
 constexpr int kF32Keys = 32;
 
+// hi: x rounded to tf32's 11 bits; lo: the rest (the tensor core cuts its last bit, 2^-23 of x).
+// Infinities and NaN have no rest.
 __device__ __forceinline__ void split(float x, uint32_t &hi, uint32_t &lo)
 {
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
-    const float d = x - __uint_as_float(hi);
-    // (infinities and NaN have no rest, and values at the type's end may round to infinity)
-    if ((hi & 0x7f800000u) == 0x7f800000u) {
-        hi = __float_as_uint(x);
-        lo = 0u;
-    } else {
-        asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(d));
-    }
+    hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+    lo = fabsf(x) < INFINITY ? __float_as_uint(x - __uint_as_float(hi)) : 0u;
 }
 
 __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)

@@ -181,6 +181,22 @@ def test_placements_strides_and_workspace(dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+def test_outputs_and_workspace_at_any_16_bytes(dtype):
+    """out and workspace 16 bytes past a 32-byte boundary: whole items, cut ones, empty rows."""
+    c = Case([300, 5, 9], [900, 6000, 3], 4, 1, 64, 16, dtype, seed=17)
+    want, want_lse = c.run(True)
+    n = c.n * 4 * 64
+    off = 16 // c.q.element_size()
+    buf = torch.full((n + 2 * off,), 7.0, device=DEV, dtype=c.dt)
+    out = buf[off:off + n].view(c.n, 4, 64)
+    ws = torch.empty(P.pa_attend_workspace_size(4, 1, 64) + 16, dtype=torch.uint8, device=DEV)[16:]
+    assert out.data_ptr() % 32 == 16 and ws.data_ptr() % 32 == 16
+    out, lse = c.run(True, out=out, workspace=ws)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    assert (buf[:off] == 7.0).all() and (buf[off + n:] == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_entries_outside_the_pool_read_zeros(dtype):
     c = Case([20], [100], 2, 2, 64, 16, dtype, seed=7)
     zero = c.bt[0, 3].item()
