@@ -92,6 +92,25 @@ def test_random(rows, children, pool, width, hi, stays):
 
 
 @pytest.mark.parametrize("num_free", [0, 1, 2, 5, -3, 1 << 30])
+def test_counts_at_any_4_bytes(num_free):
+    """extra_refs that does not begin at 16 bytes, as a slice of a larger buffer may."""
+    rng = np.random.default_rng(11)
+    b = Batch(rng.integers(0, 200, size=50), 16, 1500, 14, rng, share=[(0, 1, 1)])
+    parents = rng.integers(-1, 50, size=60)
+    want = F.fork(b.tables, b.lens, parents, b.extra, b.free, num_free, 16)
+    buf = torch.full((1503,), 9, dtype=torch.int32, device=DEV)
+    extra = buf[1:1501]
+    extra.copy_(dev(b.extra))
+    i32 = dict(dtype=torch.int32, device=DEV)
+    out, lens, pairs, granted = torch.empty(60, 14, **i32), torch.empty(60, **i32), torch.empty(60, 2, **i32), torch.empty(60, **i32)
+    free, nf = dev(b.free), dev([num_free])
+    P.pa_fork_tables(out, lens, dev(b.tables), dev(b.lens), dev(parents), extra, free, nf, 16, pairs, granted)
+    got = {"tables": out, "lens": lens, "pairs": pairs, "granted": granted, "extra": extra, "free": free, "num_free": nf}
+    same({k: v.cpu().numpy() for k, v in got.items()}, want)
+    assert buf[0] == 9 and (buf[1501:] == 9).all()
+
+
+@pytest.mark.parametrize("num_free", [0, 1, 2, 5, -3, 1 << 30])
 def test_short_pool(num_free):
     """Refused rows are empty, hold nothing, and the ones that need no block go on."""
     rng = np.random.default_rng(5)
