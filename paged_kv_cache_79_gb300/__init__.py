@@ -979,7 +979,8 @@ def pa_attend_workspace_size(num_q_heads: int, num_kv_heads: int, head_dim: int)
 
 @functools.lru_cache(maxsize=None)
 def _attend_workspace_bytes(dev: int, num_q_heads: int, num_kv_heads: int, head_dim: int) -> int:
-    return pa_attend_workspace_size(num_q_heads, num_kv_heads, head_dim)
+    with _torch().device(dev):
+        return pa_attend_workspace_size(num_q_heads, num_kv_heads, head_dim)
 
 
 _ATTEND_NAMES = ("out", "k_cache", "v_cache", "block_tables", "context_lens", "query_start", "lse")
@@ -994,39 +995,42 @@ def pa_attend(out, q, k_cache, v_cache, block_tables, context_lens, query_start,
     include/pagedkv.h).  q's rows may be strided; lse: float32 [N, Hq] for the rows'
     log-sum-exp, or None; workspace: uint8 CUDA tensor or None (allocated here)."""
     T = _torch()
-    _want(q.dim() == 3 and q.shape[1:] == (num_q_heads, head_dim) and out.shape == q.shape,
-          "q and out must be [N, Hq, d]")
-    n = q.shape[0]
-    q_stride = _row_stride(q, "q")
-    _want(k_cache.dim() == 4 and k_cache.shape == v_cache.shape and
-          k_cache.shape[1:] == (block_size, num_kv_heads, head_dim), "the caches must be [num_blocks, B, Hkv, d]")
-    if not out.dtype == q.dtype == k_cache.dtype == v_cache.dtype:
+    qshape = q.shape
+    n = qshape[0] if qshape else 0
+    _want(qshape == (n, num_q_heads, head_dim) and out.shape == qshape, "q and out must be [N, Hq, d]")
+    q_stride = _row_stride(q, "q", n, num_q_heads * head_dim, head_dim)
+    cache = k_cache.shape
+    blocks = cache[0] if cache else 0
+    _want(cache == (blocks, block_size, num_kv_heads, head_dim) and v_cache.shape == cache,
+          "the caches must be [num_blocks, B, Hkv, d]")
+    if not out.dtype is q.dtype is k_cache.dtype is v_cache.dtype:
         raise TypeError("out, q, k_cache and v_cache must have one dtype")
-    if not block_tables.dtype == context_lens.dtype == query_start.dtype == T.int32:
+    if not block_tables.dtype is context_lens.dtype is query_start.dtype is T.int32:
         raise TypeError("block_tables, context_lens and query_start must be int32")
     _want(block_tables.dim() == 2, "block_tables must be [S, W]")
     S, W = block_tables.shape
     _want(context_lens.shape == (S,) and query_start.shape == (S + 1,),
           "context_lens must be [S] and query_start [S + 1]")
-    _check_counts(n | S | W | k_cache.shape[0])
+    _check_counts(n | S | W | blocks)
     tensors = (out, k_cache, v_cache, block_tables, context_lens, query_start)
+    lse_ptr = None
     if lse is not None:
-        if lse.dtype != T.float32:
+        if lse.dtype is not T.float32:
             raise TypeError("lse must be float32")
         _want(lse.shape == (n, num_q_heads), "lse must be [N, Hq]")
         tensors += (lse,)
+        lse_ptr = lse.data_ptr()
     dev, device = _on_device(_ATTEND_NAMES, tensors)
     _want(q.get_device() == dev, "q must be on the device of out")
     if workspace is None:
-        with device or contextlib.nullcontext():
-            size = _attend_workspace_bytes(dev, num_q_heads, num_kv_heads, head_dim)
-            workspace = T.empty(size, dtype=T.uint8, device=q.device) if stream is None else _launch_scratch(
-                size, q.device, stream)
+        size = _attend_workspace_bytes(dev, num_q_heads, num_kv_heads, head_dim)
+        workspace = T.empty(size, dtype=T.uint8, device=q.device) if stream is None else _launch_scratch(
+            size, q.device, stream)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous and on the device of q")
-    _call("pa_attend", device, out.data_ptr(), None if lse is None else lse.data_ptr(), q.data_ptr(), q_stride,
+    _call("pa_attend", device, out.data_ptr(), lse_ptr, q.data_ptr(), q_stride,
           k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), W, context_lens.data_ptr(),
-          query_start.data_ptr(), S, n, k_cache.shape[0], float(scale), int(causal), num_q_heads, num_kv_heads,
+          query_start.data_ptr(), S, n, blocks, float(scale), int(causal), num_q_heads, num_kv_heads,
           head_dim, block_size, _code(q), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
           _raw_stream(stream, dev))
     return out
@@ -1055,48 +1059,57 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "non
     return freqs, amplitude.value
 
 
-def _row_stride(t, name: str) -> int:
-    """Elements between the rows of a [N, H, d] tensor, whose rows have to be dense."""
-    n, h, d = t.shape
+def _row_stride(t, name: str, n: int, dense: int, d: int) -> int:
+    """Elements between the rows of a [n, H, d] tensor, whose rows (`dense` elements) have to be dense."""
     if t.is_contiguous():
-        return h * d
+        return dense
     row, head, one = t.stride()
-    if one != 1 or (head != d and h > 1):
+    if one != 1 or (head != d and dense > d):
         raise ValueError(f"{name} must have dense [heads, head_dim] rows")
-    return row if n > 1 else h * d
+    return row if n > 1 else dense
 
 
-def _rope_check(q, k, positions, freqs, others):
-    """Checks that pa_rope and pa_rope_append share; returns (device index, device context)."""
+def _rope_error(names, tensors, positions, freqs):
+    """What is wrong with the types and places of a rotary call's tensors."""
     T = _torch()
-    _want(q.dim() == 3 and k.dim() == 3 and k.shape[0] == q.shape[0] and k.shape[2] == q.shape[2],
-          "q must be [N, Hq, d] and k [N, Hkv, d]")
-    _want(positions.shape == q.shape[:1] and freqs.dim() == 1, "positions must be [N] and freqs [rotary_dim / 2]")
+    for name, t in zip(names, tensors):
+        if t.dtype != tensors[0].dtype:
+            raise TypeError(f"{name} and {names[0]} must have one dtype")
     if positions.dtype != T.int32 or freqs.dtype != T.int64:
         raise TypeError("positions must be int32 and freqs int64")
-    dtype, at = q.dtype, q.get_device()
-    for t in others:
-        if t.dtype != dtype:
-            raise TypeError("q, k, v, their outputs and the caches must have one dtype")
-        if t.get_device() != at:
-            raise ValueError("all tensors must be on the device of q")
-    dev, device = _on_device(("positions", "freqs"), (positions, freqs))
-    _want(at == dev, "all tensors must be on the device of q")
-    _check_counts(q.shape[0])
-    return dev, device
+    dev = tensors[0].get_device()
+    for name, t in zip(names + ("positions", "freqs"), tensors + (positions, freqs)):
+        if t.get_device() != dev or dev < 0:
+            raise ValueError(f"{name} must be a CUDA tensor on the device of {names[0]}")
+    _on_device(("positions", "freqs"), (positions, freqs))
+    raise ValueError("positions must be [N] and freqs [rotary_dim / 2]")
 
 
 def pa_rope(q_out, q, k_out, k, positions, freqs, interleaved: bool = False, amplitude: float = 1.0, stream=None):
     """q_out, k_out [N, H, d] <- q, k turned by their positions (see pa_rope in
     include/pagedkv.h).  Rows may be strided (parts of a fused projection); q_out may be q
     and k_out k.  freqs int64 [rotary_dim / 2]: rope_frequencies's, on the device."""
-    dev, device = _rope_check(q, k, positions, freqs, (q_out, k_out, k))
-    _want(q_out.shape == q.shape and k_out.shape == k.shape, "q_out must be as q and k_out as k")
+    T = _torch()
+    _want(q.dim() == 3 and k.dim() == 3, "q must be [N, Hq, d] and k [N, Hkv, d]")
     n, hq, d = q.shape
-    _call("pa_rope", device, q_out.data_ptr(), _row_stride(q_out, "q_out"), q.data_ptr(), _row_stride(q, "q"),
-          k_out.data_ptr(), _row_stride(k_out, "k_out"), k.data_ptr(), _row_stride(k, "k"), positions.data_ptr(),
-          freqs.data_ptr(), n, hq, k.shape[1], d, 2 * freqs.shape[0], int(interleaved), float(amplitude), _code(q),
-          _raw_stream(stream, dev))
+    kshape = k.shape
+    hkv = kshape[1]
+    _want(kshape == (n, hkv, d), "q must be [N, Hq, d] and k [N, Hkv, d]")
+    _want(q_out.shape == (n, hq, d) and k_out.shape == kshape, "q_out must be as q and k_out as k")
+    dtype, dev = q.dtype, q.get_device()
+    for t in (q_out, k_out, k):
+        if t.dtype is not dtype or t.get_device() != dev:
+            _rope_error(("q", "q_out", "k_out", "k"), (q, q_out, k_out, k), positions, freqs)
+    if (positions.dtype is not T.int32 or freqs.dtype is not T.int64 or positions.shape != (n,) or freqs.dim() != 1 or
+            positions.get_device() != dev or freqs.get_device() != dev or dev < 0 or
+            not positions.is_contiguous() or not freqs.is_contiguous()):
+        _rope_error(("q",), (q,), positions, freqs)
+    _check_counts(n)
+    _call("pa_rope", None if dev == T.current_device() else T.device(dev), q_out.data_ptr(),
+          _row_stride(q_out, "q_out", n, hq * d, d), q.data_ptr(), _row_stride(q, "q", n, hq * d, d), k_out.data_ptr(),
+          _row_stride(k_out, "k_out", n, hkv * d, d), k.data_ptr(), _row_stride(k, "k", n, hkv * d, d),
+          positions.data_ptr(), freqs.data_ptr(), n, hq, hkv, d, 2 * freqs.shape[0], int(interleaved), amplitude,
+          _code(q), _raw_stream(stream, dev))
 
 
 def pa_rope_append(q_out, q, k, v, k_cache, v_cache, positions, slot_mapping, freqs, interleaved: bool = False,
@@ -1105,22 +1118,35 @@ def pa_rope_append(q_out, q, k, v, k_cache, v_cache, positions, slot_mapping, fr
     slot_mapping (int64 [N], negative: skipped) into the caches [num_blocks, B, Hkv, d] (see
     pa_rope_append in include/pagedkv.h).  q, k and v may be strided rows of one fused
     projection; q_out may be q."""
-    dev, device = _rope_check(q, k, positions, freqs, (q_out, k, v, k_cache, v_cache))
-    _want(q_out.shape == q.shape and v.shape == k.shape, "q_out must be as q and v as k")
+    T = _torch()
+    _want(q.dim() == 3 and k_cache.dim() == 4, "q must be [N, Hq, d] and the caches [num_blocks, B, Hkv, d]")
     n, hq, d = q.shape
-    hkv = k.shape[1]
-    _want(k_cache.dim() == 4 and k_cache.shape == v_cache.shape and k_cache.shape[2:] == (hkv, d),
-          "the caches must be [num_blocks, B, Hkv, d]")
-    if slot_mapping.dtype != _torch().int64:
+    cache = k_cache.shape
+    blocks, size, hkv, _ = cache
+    _want(cache == (blocks, size, hkv, d) and v_cache.shape == cache, "the caches must be [num_blocks, B, Hkv, d]")
+    _want(k.shape == (n, hkv, d) and v.shape == (n, hkv, d), "k and v must be [N, Hkv, d]")
+    _want(q_out.shape == (n, hq, d), "q_out must be as q")
+    dtype, dev = q.dtype, q.get_device()
+    for t in (q_out, k, v, k_cache, v_cache):
+        if t.dtype is not dtype or t.get_device() != dev:
+            _rope_error(("q", "q_out", "k", "v", "k_cache", "v_cache"), (q, q_out, k, v, k_cache, v_cache), positions,
+                        freqs)
+    if (positions.dtype is not T.int32 or freqs.dtype is not T.int64 or positions.shape != (n,) or freqs.dim() != 1 or
+            positions.get_device() != dev or freqs.get_device() != dev or dev < 0 or
+            not positions.is_contiguous() or not freqs.is_contiguous()):
+        _rope_error(("q",), (q,), positions, freqs)
+    if slot_mapping.dtype is not T.int64:
         raise TypeError("slot_mapping must be int64")
     _want(slot_mapping.shape == (n,), "slot_mapping must be [N]")
-    _on_device(("positions", "slot_mapping", "k_cache", "v_cache"), (positions, slot_mapping, k_cache, v_cache))
-    blocks, size = k_cache.shape[:2]
-    _check_counts(blocks | size)
-    _call("pa_rope_append", device, q_out.data_ptr(), _row_stride(q_out, "q_out"), q.data_ptr(), _row_stride(q, "q"),
-          k.data_ptr(), _row_stride(k, "k"), v.data_ptr(), _row_stride(v, "v"), k_cache.data_ptr(),
+    for name, t in (("slot_mapping", slot_mapping), ("k_cache", k_cache), ("v_cache", v_cache)):
+        if t.get_device() != dev or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous and on the device of q")
+    _check_counts(n | blocks | size)
+    _call("pa_rope_append", None if dev == T.current_device() else T.device(dev), q_out.data_ptr(),
+          _row_stride(q_out, "q_out", n, hq * d, d), q.data_ptr(), _row_stride(q, "q", n, hq * d, d), k.data_ptr(),
+          _row_stride(k, "k", n, hkv * d, d), v.data_ptr(), _row_stride(v, "v", n, hkv * d, d), k_cache.data_ptr(),
           v_cache.data_ptr(), positions.data_ptr(), slot_mapping.data_ptr(), freqs.data_ptr(), n, hq, hkv, d,
-          2 * freqs.shape[0], int(interleaved), float(amplitude), size, blocks, _code(q), _raw_stream(stream, dev))
+          2 * freqs.shape[0], int(interleaved), amplitude, size, blocks, _code(q), _raw_stream(stream, dev))
 
 
 def pa_kv_transfer_worthwhile(reusable_tokens: int, threshold_tokens: int = 64) -> bool:
