@@ -9,6 +9,10 @@
 // in two buffers, the next one's copies in flight while this one is multiplied.  Scores
 // stay in registers: the fragment that Q K^T leaves becomes P's when a step of 8 keys is taken
 // in the order 0 2 4 6 1 3 5 7, which only means reading V's rows in that order.
+//
+// Measured: 7 ragged chunks of up to 700 tokens on up to 1003 keys, 39 / 3 heads of 64 dims: 227 us,
+// 27 TFLOP/s.  Bound by the splitting (every warp splits the K and V that it reads; with
+// conversion instructions instead of integer ones 462 us) and by reads of shared memory.
 #include "pa_attend.cuh"
 
 namespace pagedkv {

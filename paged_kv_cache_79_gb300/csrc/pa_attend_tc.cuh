@@ -7,7 +7,7 @@
 //                one's tiles are copied (a read takes longer than a tile when DRAM is busy);
 //   warp 10      makes the rows behind the last key that an item sees zeros in V (a weight of
 //                0 times what a stale row holds would be NaN where that is NaN);
-//   warp 9       products, issued by one thread: S = Q K^T into TMEM (operands in shared
+//   warp 9       products, issued by one lane: S = Q K^T into TMEM (operands in shared
 //                memory), O += P V with P read from TMEM;
 //   warp 11      walks through the CTA's share, hands the items on to the others and copies
 //                Q's rows with TMA;
@@ -21,6 +21,15 @@
 // tile's maximum is still being found, and only where a row's maximum has grown by more than
 // 2^8 over its base, O (in TMEM) is rescaled and the tile's probabilities are taken again.
 // They stay below 2^8, far from fp16's end.
+//
+// Where an item has one row tile (few query tokens), its tiles of keys go to the two softmax groups
+// in turn, each with an output of its own over the same rows, and the first joins them.
+//
+// Measured (32 / 8 heads of 128, bf16, causal): two prompts of 8192 tokens 725 us, 1350 TFLOP/s,
+// 69% of the measured bf16 rate; 1000 tokens behind 95,000 1156 us, 1360 TFLOP/s.  64 sequences of
+// 1 to 8 tokens over 500 to 8192 keys, 64 / 8 heads: 136 us, 5360 GB/s, 79% of the measured copy.
+// Bound by the products (the tensor pipe is busy 70% of the time) and the hand-overs between
+// them and the softmax, of which the other row tile covers a part; with few tokens by DRAM.
 #pragma once
 
 #include <type_traits>
@@ -67,7 +76,7 @@ template <int D>
 struct Smem {
     static constexpr int kChunks = D / 64;
     static constexpr int kTileBytes = kChunks * kChunkBytes;  // 128 rows of Q, K or V
-    static constexpr int kStages = D == 128 ? 5 : 10;
+    static constexpr int kStages = D == 128 ? 5 : 10;         // what shared memory holds
     static constexpr int kRing = 2 * kTileBytes;              // behind the two tiles of Q
     static constexpr int kBars = kRing + kStages * kTileBytes;
     static constexpr int kFull = kBars, kEmpty = kFull + 8 * kStages, kRaw = kEmpty + 8 * kStages,
