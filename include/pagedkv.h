@@ -372,7 +372,8 @@ pa_status pa_decode_noalloc(void *out, const void *q, const void *k_cache, const
  * seen, is pa_decode's case; here such tokens may stand among longer runs.)
  *
  *   out            device [num_tokens][Hq][d]; rows of q and out from query_start[num_seqs] on
- *                  are padding: not read, and left as they were
+ *                  are padding: q's may hold anything and change no result, out's are left as
+ *                  they were
  *   lse            device fp32 [num_tokens][Hq], or NULL
  *   q              device rows of [Hq][d], q_stride elements from one token's to the next (a
  *                  multiple of 16 bytes, at least Hq * d: q may be part of a fused projection)

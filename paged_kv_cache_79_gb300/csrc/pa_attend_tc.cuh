@@ -724,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const float f = top == -INFINITY ? 1.f : exp2f(m - top);
                     m = top;
-                    far = __any_sync(0xffffffffu, fabsf(m) > kFar && m != -INFINITY);
+                    far = __any_sync(0xffffffffu, mine && fabsf(m) > kFar && m != -INFINITY);
                     return f;
                 };
                 if (tile == a)
@@ -760,7 +760,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 // By the base at hand; where that has fallen behind, once more by the maximum.
                 const float top = masked || far ? probabilities(std::false_type()) : probabilities(std::true_type());
-                if (__any_sync(0xffffffffu, top > (m == -INFINITY ? -INFINITY : kRescale))) {
+                // (Rows that are not the item's have no vote: they hold other queries or what an earlier
+                // kernel left, and a new base rounds every row of the warp differently.)
+                if (__any_sync(0xffffffffu, mine && top > (m == -INFINITY ? -INFINITY : kRescale))) {
                     // O is at rest: the scores of this tile came after the product before it
                     const float f = raise();
                     l *= f;
