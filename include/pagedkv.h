@@ -364,8 +364,9 @@ pa_status pa_decode_noalloc(void *out, const void *q, const void *k_cache, const
  * and   out[r][h] = sum_t exp(s_t - max) V_t / sum_t exp(s_t - max),   s_t = scale q[r][h] . K_t
  *       lse[r][h] = log sum_t exp(s_t)          (natural logarithm; to merge with other keys)
  * A row that sees no key (T = 0, or n_s > T with causal) yields zeros and lse -inf.  Scores,
- * statistics and sums are fp32; probabilities enter the second product in `dtype` (fp16 and
- * bf16: rounded to 2^-12 and 2^-9 of themselves; fp32: two tf32 terms, about 21 bits).  Keys
+ * statistics and sums are fp32; probabilities enter the second product in `dtype`: rounded by
+ * half a step, 2^-11 (fp16) and 2^-8 (bf16) of themselves, in fp16 those below 2^-25 of the
+ * row's largest by up to 2^-36 of that one; in fp32 as two tf32 terms, about 21 bits.  Keys
  * past T are never counted, whatever their rows hold; a table entry outside [0, num_blocks)
  * reads zeros.  A NaN or infinity among the values of a sequence's context can make NaN also
  * of its query tokens that do not see it.  (One query token of every sequence, all of its keys

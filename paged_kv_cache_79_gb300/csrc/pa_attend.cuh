@@ -13,6 +13,8 @@
 // that has to be cleared.
 #pragma once
 
+#include <type_traits>
+
 #include "pa_device.cuh"
 #include "pa_internal.h"
 
@@ -272,6 +274,20 @@ struct AttendWalk {
         return r;
     }
 };
+
+// Exponents (log2) that a row's base lies below the maximum that it was taken from.
+template <typename T>
+constexpr float kAttendBelow = std::is_same<T, __half>::value ? 11.0f : 0.0f;
+
+// A row's log sum exp from its base m (log2 units) and its sum l over exp2(score - m).  (The
+// base's distance is taken out of both first, so that neither is rounded at a larger size.)
+template <typename T>
+__device__ __forceinline__ float attend_lse(float m, float l)
+{
+    constexpr float kBelow = kAttendBelow<T>;
+    const float scale = kBelow == 0.f ? 1.f : 1.f / (float)(1 << (int)kBelow);
+    return l == 0.f ? -INFINITY : ((m + kBelow) + log2f(l * scale)) * 0.6931471805599453f;
+}
 
 // Partial rows of CTA c: slot 0 holds the item that its start cuts, slot 1 an item that
 // begins in its share and is cut by its end; kAttendRows rows each, or fewer (max_rows).

@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kF32Threads) attend_f32_kernel(const __grid_co
                 for (int d = 0; d < D / 8; ++d)
                     *reinterpret_cast<float2 *>(dst + 8 * d) = make_float2(o[d][2 * h] * inv, o[d][2 * h + 1] * inv);
                 if (p.lse && c4 == 0)
-                    p.lse[row] = l[h] == 0.f ? -INFINITY : (m[h] + log2f(l[h])) * 0.6931471805599453f;
+                    p.lse[row] = attend_lse<float>(m[h], l[h]);
             } else {
                 const size_t row = attend_part_row(p, blockIdx.x, a > 0 ? 0 : 1) + r;
                 if (c4 == 0)
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) attend_merge_kernel(const __
         else
             *reinterpret_cast<uint32_t *>(dst) = *reinterpret_cast<const uint32_t *>(x);
         if (p.lse && lane == 0)
-            p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+            p.lse[row] = attend_lse<T>(m, l);
     }
 }
 

@@ -18,9 +18,13 @@
 //
 // The running maximum need not be the true one: any base with exponents that stay in range
 // gives the same quotient.  So a tile's probabilities are taken by the base at hand while the
-// tile's maximum is still being found, and only where a row's maximum has grown by more than
-// 2^8 over its base, O (in TMEM) is rescaled and the tile's probabilities are taken again.
-// They stay below 2^8, far from fp16's end.
+// tile's maximum is still being found, and only where a row's maximum has outgrown its base by
+// too much (bf16: 2^8), O (in TMEM) is rescaled and the tile's probabilities are taken again.
+//
+// fp16 has no room below: weights under 2^-14 would lose bits and those under 2^-25 vanish, which
+// over a long context adds up.  There the base lies 2^11 below the maximum and may lag by 2^4
+// more: weights reach 2^15 (fp16 ends at 2^16), and only those under 2^-25 of the largest lose
+// bits, 2^-36 of it at most.
 //
 // Where an item has one row tile (few query tokens), its tiles of keys go to the two softmax groups
 // in turn, each with an output of its own over the same rows, and the first joins them.
@@ -31,8 +35,6 @@
 // Bound by the products (the tensor pipe is busy 70% of the time) and the hand-overs between
 // them and the softmax, of which the other row tile covers a part; with few tokens by DRAM.
 #pragma once
-
-#include <type_traits>
 
 #include "pa_attend.cuh"
 
@@ -47,7 +49,10 @@ constexpr int kQueryWarp = 11;
 constexpr int kTileRows = 128;
 constexpr int kKeys = 128;
 constexpr int kChunkBytes = kKeys * 128;   // 128 rows of 128 bytes: one column of a tile
-constexpr float kRescale = 8.0f;           // growth of a maximum (log2) that the base may lag by
+// Exponents (log2) that a row's scores may reach over its base before it is taken anew.  (It lies
+// kAttendBelow below the maximum; from 2^24 on it rounds to a multiple of up to 8, so by at most 8.)
+template <typename T>
+constexpr float kRescale = std::is_same<T, __half>::value ? 15.0f : 8.0f;
 constexpr float kFar = 1048576.0f;         // bases (log2) from which on products are rounded first
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;            // O of the row tiles, behind their S (128 columns each)
@@ -711,9 +716,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     return fmaxf(top, top2);
                 };
-                // The base becomes the row's maximum, this tile's included.
+                // The base follows the row's maximum, this tile's included.
                 auto raise = [&]() {
-                    float top = m;
+                    const float had = m + kAttendBelow<T>;
+                    float top = had;
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
                         uint32_t s[32];
@@ -722,6 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         wait_ld(s);
                         top = exponents(std::false_type(), s, c, 0.f, true, x, top);
                     }
+                    top = top > had ? top - kAttendBelow<T> : m;
                     const float f = top == -INFINITY ? 1.f : exp2f(m - top);
                     m = top;
                     far = __any_sync(0xffffffffu, mine && fabsf(m) > kFar && m != -INFINITY);
@@ -762,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float top = masked || far ? probabilities(std::false_type()) : probabilities(std::true_type());
                 // (Rows that are not the item's have no vote: they hold other queries or what an earlier
                 // kernel left, and a new base rounds every row of the warp differently.)
-                if (__any_sync(0xffffffffu, mine && top > (m == -INFINITY ? -INFINITY : kRescale))) {
+                if (__any_sync(0xffffffffu, mine && top > (m == -INFINITY ? -INFINITY : kRescale<T>))) {
                     // O is at rest: the scores of this tile came after the product before it
                     const float f = raise();
                     l *= f;
@@ -857,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     dev::mbar_arrive(smem + S::kPairFree);
             }
             if (mine && whole && p.lse)
-                p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+                p.lse[row] = attend_lse<T>(m, l);
             if (mine && !whole)
                 p.part_ml[part] = make_float2(m, l);
         }
