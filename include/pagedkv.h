@@ -368,9 +368,11 @@ pa_status pa_decode_noalloc(void *out, const void *q, const void *k_cache, const
  * half a step, 2^-11 (fp16) and 2^-8 (bf16) of themselves, in fp16 those below 2^-25 of the
  * row's largest by up to 2^-36 of that one; in fp32 as two tf32 terms, about 21 bits.  Keys
  * past T are never counted, whatever their rows hold; a table entry outside [0, num_blocks)
- * reads zeros.  A NaN or infinity among the values of a sequence's context can make NaN also
- * of its query tokens that do not see it.  (One query token of every sequence, all of its keys
- * seen, is pa_decode's case; here such tokens may stand among longer runs.)
+ * reads zeros.  A NaN reaches every row that sees it; in fp16 and bf16 a NaN or infinity among
+ * the values of a sequence's context can make NaN also of its query tokens that do not see it
+ * (0 times it, in a product over a tile of keys), in fp32 it cannot.  (One query token of every
+ * sequence, all of its keys seen, is pa_decode's case; here such tokens may stand among longer
+ * runs.)
  *
  *   out            device [num_tokens][Hq][d]; rows of q and out from query_start[num_seqs] on
  *                  are padding: q's may hold anything and change no result, out's are left as

@@ -10,9 +10,14 @@
 // stay in registers: the fragment that Q K^T leaves becomes P's when a step of 8 keys is taken
 // in the order 0 2 4 6 1 3 5 7, which only means reading V's rows in that order.
 //
-// Measured: 7 ragged chunks of up to 700 tokens on up to 1003 keys, 39 / 3 heads of 64 dims: 227 us,
-// 27 TFLOP/s.  Bound by the splitting (every warp splits the K and V that it reads; with
-// conversion instructions instead of integer ones 462 us) and by reads of shared memory.
+// Tiles with values that two terms do not stand for (NaN, infinities, numbers next to the largest)
+// are multiplied by fp32 FMAs: V's are looked for as a tile arrives, in the scores what is not
+// finite gives them away.
+//
+// Measured: 7 ragged chunks of up to 700 tokens on up to 1003 keys, 39 / 3 heads of 64 dims: 212 us,
+// 29 TFLOP/s (220 with every term guarded).  Bound by the splitting (every warp splits the K and V
+// that it reads; with conversion instructions instead of integer ones 462 us) and by reads of
+// shared memory.
 #include "pa_attend.cuh"
 
 namespace pagedkv {
@@ -24,11 +29,14 @@ constexpr int kF32Rows = kF32TileRows;
 constexpr int kF32Keys = 32;
 
 // hi: x rounded to tf32's 11 bits; lo: the rest (the tensor core cuts its last bit, 2^-23 of x).
-// Infinities and NaN have no rest.
+// Of NaN, an infinity or a number that rounds to one (kSplitEnd on), at least one term is NaN or
+// infinite, so sums that it is in are neither right nor finite: such tiles are multiplied by FMAs
+// instead.
+constexpr uint32_t kSplitEnd = 0x7f7ff000u;  // bits of |x|
 __device__ __forceinline__ void split(float x, uint32_t &hi, uint32_t &lo)
 {
     hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
-    lo = fabsf(x) < INFINITY ? __float_as_uint(x - __uint_as_float(hi)) : 0u;
+    lo = __float_as_uint(x - __uint_as_float(hi));
 }
 
 __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
@@ -61,9 +69,11 @@ __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src
 template <int D>
 struct SmemF32 {
     static constexpr int kStride = D + 4;  // floats; rows 4 banks apart
+    static constexpr int kPStride = kF32Keys + 1;
     float q[kF32Rows * kStride];
     float k[2][kF32Keys * kStride];
     float v[2][kF32Keys * kStride];
+    float p[kF32Rows * kPStride];  // a tile's probabilities, for products by FMAs
     long long scratch[kF32Threads / 32 + 4];
 };
 
@@ -131,7 +141,14 @@ __global__ void __launch_bounds__(kF32Threads) attend_f32_kernel(const __grid_co
         for (int tile = a; tile < b; ++tile) {
             const int buf = (tile - a) & 1;
             dev::cp_async_wait_all();
-            __syncthreads();  // this tile's copies are there, the other buffer has been read
+            // values that no two terms stand for: each thread looks at what it copied itself
+            uint32_t largest = 0;
+            for (int i = tid; i < kF32Keys * kVecs; i += kF32Threads) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(&sm.v[buf][i / kVecs * kStride + i % kVecs * 4]);
+                largest = max(max(largest, max(x.x << 1, x.y << 1)), max(x.z << 1, x.w << 1));
+            }
+            // this tile's copies are there, the other buffer has been read
+            const bool by_fma = __syncthreads_or(largest >= kSplitEnd << 1);
             if (tile + 1 < b)
                 load_kv(tile + 1, buf ^ 1);
             dev::cp_async_commit();
@@ -150,6 +167,34 @@ __global__ void __launch_bounds__(kF32Threads) attend_f32_kernel(const __grid_co
                     mma_3(s[n], ah, al, kr[0], kr[4]);
                 }
             }
+            // NaN, infinities and numbers next to them in q or K, or a sum past fp32's range
+            bool finite = true;
+#pragma unroll
+            for (int n = 0; n < kF32Keys / 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    finite = finite && fabsf(s[n][e]) < INFINITY;
+            if (!finite) {
+#pragma unroll
+                for (int n = 0; n < kF32Keys / 8; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        s[n][e] = 0.f;
+#pragma unroll 1
+                for (int k = 0; k < D; ++k) {
+                    const float *qr = &sm.q[(16 * warp + g) * kStride + k], *kr = &sm.k[buf][2 * c4 * kStride + k];
+                    const float q0 = qr[0], q1 = qr[8 * kStride];
+#pragma unroll
+                    for (int n = 0; n < kF32Keys / 8; ++n) {
+                        const float k0 = kr[8 * n * kStride], k1 = kr[(8 * n + 1) * kStride];
+                        s[n][0] = fmaf(q0, k0, s[n][0]);
+                        s[n][1] = fmaf(q0, k1, s[n][1]);
+                        s[n][2] = fmaf(q1, k0, s[n][2]);
+                        s[n][3] = fmaf(q1, k1, s[n][3]);
+                    }
+                }
+            }
+            __syncwarp();
             const int key0 = tile * kF32Keys + 2 * c4;
             float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
@@ -186,6 +231,40 @@ __global__ void __launch_bounds__(kF32Threads) attend_f32_kernel(const __grid_co
                 split(e[2], ah[n][1], al[n][1]);
                 split(e[1], ah[n][2], al[n][2]);
                 split(e[3], ah[n][3], al[n][3]);
+            }
+            if (by_fma) {
+                float *const pr = &sm.p[16 * warp * SmemF32<D>::kPStride];
+#pragma unroll
+                for (int n = 0; n < kF32Keys / 8; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int i = e == 0 ? 0 : e == 1 ? 2 : e == 2 ? 1 : 3;  // (the order of the splits)
+                        pr[(g + 8 * (e >> 1)) * SmemF32<D>::kPStride + 8 * n + 2 * c4 + (e & 1)] =
+                            __uint_as_float(ah[n][i]) + __uint_as_float(al[n][i]);
+                    }
+                __syncwarp();
+#pragma unroll
+                for (int d = 0; d < D / 8; ++d) {
+                    float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                    for (int k = 0; k < kF32Keys; ++k) {
+                        const float *vr = &sm.v[buf][k * kStride + 8 * d + 2 * c4];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            // (a hidden key's value may be anything)
+                            if (tile * kF32Keys + k >= limit[h])
+                                continue;
+                            const float w = pr[(g + 8 * h) * SmemF32<D>::kPStride + k];
+                            c[2 * h] = fmaf(w, vr[0], c[2 * h]);
+                            c[2 * h + 1] = fmaf(w, vr[1], c[2 * h + 1]);
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        o[d][e] = fmaf(o[d][e], scale[e >> 1], c[e]);
+                }
+                __syncwarp();  // the probabilities have been read
+                continue;
             }
             // The tile's share of the output is summed by itself: the tensor core's additions cut
             // low bits off, which over a long context leans one way; the addition here rounds.

@@ -59,3 +59,106 @@ def test_many_small_weights_under_a_dominant_one(dtype, at, below, new):
     assert (err <= tol).all(), (float((err / tol).max()), float((err / size).max()))
     z = score + math.log(total)
     assert ((lse.double() - z).abs() <= t * 2.0 ** -24 + 2.0 ** -20 + z * 2.0 ** -21).all()
+
+
+def definition(c, causal):
+    """(out, lse) in 64 bits of a case with values that are not finite: hidden keys are left out."""
+    out = torch.zeros(c.n, c.hq, c.d, device=DEV, dtype=torch.float64)
+    lse = torch.full((c.n, c.hq), -math.inf, device=DEV, dtype=torch.float64)
+    at = 0
+    for s, (n, t) in enumerate(zip(c.new, c.lens)):
+        slots = rows_of(c, s)
+        for i in range(n):
+            seen = t - n + i + 1 if causal else t
+            for h in range(c.hq):
+                kv = h * c.hkv // c.hq
+                k, v = (x.view(-1, c.hkv, c.d)[slots[:seen], kv].double() for x in (c.k, c.v))
+                sc = (k * c.q[at + i, h].double()).sum(-1) * c.scale
+                z = torch.logsumexp(sc, 0)
+                p = torch.exp(sc - z)
+                out[at + i, h] = (torch.where(p[:, None] == 0, 0.0, p[:, None] * v)).sum(0)
+                lse[at + i, h] = z
+        at += n
+    return out, lse
+
+
+NANS = [0x7fffffff, -1, 0x7f800001, 0x7fc00000, -0x400000]     # bit patterns of fp32 NaN
+
+
+def same_kind(got, want, tol):
+    """NaN and infinities where the definition has them, the others within tol."""
+    assert torch.equal(got.isnan(), want.isnan())
+    inf = want.isinf()
+    assert torch.equal(got[inf].double(), want[inf])
+    fin = want.isfinite()
+    assert (got.double() - want)[fin].abs().le((tol * torch.ones_like(want))[fin]).all()
+
+
+def nan_of(bits):
+    return torch.tensor(bits, dtype=torch.int32, device=DEV).view(torch.float32)
+
+
+@pytest.mark.parametrize("bits", NANS)
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("where", ["q", "k", "v"])
+def test_nan_of_any_bits_fp32(bits, causal, d, where):
+    """One NaN in a query, a key or a value: it reaches the rows that see it, and no other.
+
+    Tolerance: scale * sum |q k| <= 12 in two tf32 terms (2^-21) and 132 roundings of 2^-24, twice
+    that for a weight, times |v| <= 5: below 2^-9."""
+    c = Case([33, 5], [70, 40], 4, 2, d, 16, "f32", seed=3, pad=0)
+    flat = (c.q if where == "q" else c.k if where == "k" else c.v).view(-1, c.hq if where == "q" else c.hkv, d)
+    row = 20 if where == "q" else int(rows_of(c, 0)[55])
+    flat.view(torch.int32)[row, 1, 7] = bits
+    want, want_lse = definition(c, causal)
+    assert want.isnan().any() and not want.isnan().all()
+    out, lse = c.run(causal)
+    same_kind(out, want, 2.0 ** -9)
+    assert torch.equal(lse.isnan(), want_lse.isnan())
+
+
+@pytest.mark.parametrize("value", [math.inf, -math.inf])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("where", ["k", "v"])
+def test_infinities_fp32(value, causal, where):
+    """An infinite value makes its column infinite for the rows that see it; an infinite key gives a
+    weight of 0 where its score is -inf, NaN where it is +inf."""
+    c = Case([33, 5], [70, 40], 4, 2, 64, 16, "f32", seed=4, pad=0)
+    (c.k if where == "k" else c.v).view(-1, 2, 64)[int(rows_of(c, 0)[55]), 1, 7] = value
+    want, _ = definition(c, causal)
+    out, _ = c.run(causal)
+    same_kind(out, want, 2.0 ** -9)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+def test_values_that_every_row_sees(dtype, value):
+    """Without a mask every row of the sequence sees the value, and no other column changes.
+    Tolerance: as above, and half a step of the type twice for a weight, once for the output."""
+    c = Case([33, 5], [70, 40], 4, 2, 128, 16, dtype, seed=5, pad=0)
+    c.v.view(-1, 2, 128)[int(rows_of(c, 0)[55]), 1, 7] = value
+    want, _ = definition(c, False)
+    out, _ = c.run(False)
+    same_kind(out, want, {"f32": 2.0 ** -9, "f16": 2.0 ** -6, "bf16": 2.0 ** -3}[dtype])
+
+
+@pytest.mark.parametrize("big", [3.4028234663852886e38, 3.4024e38, 3.3e38, -3.4028234663852886e38])
+def test_values_next_to_the_largest_fp32(big):
+    """A key and a value next to the largest number: score and output stay finite, to 2^-20."""
+    c = Case([3], [40], 1, 1, 64, 16, "f32", seed=6, pad=0)
+    slots = rows_of(c, 0)
+    k, v = c.k.view(-1, 64), c.v.view(-1, 64)
+    c.scale = 2.0 ** -117
+    k[slots] = 0.0
+    k[slots[11], 5] = big
+    c.q[...] = 0.0
+    c.q[..., 5] = math.copysign(0.25, big)       # score: 2^-119 of |big|, about 512; the others 0
+    v[slots[11], 9] = big
+    v[slots[12], 9] = 1.0
+    v[slots[11], 10] = 2.5
+    out, lse = c.run(False)
+    score = abs(float(k[slots[11], 5].double())) * 2.0 ** -119
+    assert ((lse.double() - score).abs() <= score * 2.0 ** -20).all()
+    assert (out[:, 0, 9].double() - float(v[slots[11], 9])).abs().le(abs(big) * 2.0 ** -20).all()
+    assert (out[:, 0, 10].double() - 2.5).abs().le(2.0 ** -19).all()
