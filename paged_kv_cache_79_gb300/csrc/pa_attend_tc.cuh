@@ -398,15 +398,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            // what is in flight lands before the CTA ends
-            if (*abort) {
-                for (uint32_t i = 0; i < S::kStages; ++i) {
-                    if (!(filled >> i & 1))
-                        continue;
-                    // (stages before `stage` were filled in this round, the others in the one before)
-                    const uint32_t parity = raw >> i & 1 ? (raw_round >> i & 1) ^ 1 : i < stage ? round : round ^ 1;
-                    dev::mbar_wait(smem + (raw >> i & 1 ? S::kRaw : S::kFull) + 8 * i, parity, kWaitTimeoutNs);
-                }
+            // What is in flight lands before the CTA ends.  (Always waited for: whether another warp will
+            // have given up, and so not have waited for it, is not known here.)
+            for (uint32_t i = 0; i < S::kStages; ++i) {
+                if (!(filled >> i & 1))
+                    continue;
+                // (stages before `stage` were filled in this round, the others in the one before)
+                const uint32_t parity = raw >> i & 1 ? (raw_round >> i & 1) ^ 1 : i < stage ? round : round ^ 1;
+                dev::mbar_wait(smem + (raw >> i & 1 ? S::kRaw : S::kFull) + 8 * i, parity, kWaitTimeoutNs);
             }
         } else if (warp == kQueryWarp) {
             uint32_t q_round = 0, q_used = 0;  // bit t: row tile t
@@ -467,11 +466,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 Item none = {};
                 hand_on(none);
             }
-            if (*abort) {
-                for (int t = 0; t < 2; ++t)
-                    if (q_used >> t & 1)
-                        dev::mbar_wait(smem + S::kQFull + 8 * t, (q_round >> t & 1) ^ 1, kWaitTimeoutNs);
-            }
+            for (int t = 0; t < 2; ++t)  // (as the loader)
+                if (q_used >> t & 1)
+                    dev::mbar_wait(smem + S::kQFull + 8 * t, (q_round >> t & 1) ^ 1, kWaitTimeoutNs);
         } else if (warp == kTailWarp) {
             // V's rows behind the last key an item sees become zeros, once they have landed.
             uint32_t stage = 0, raw_round = 0, turn = 0;
