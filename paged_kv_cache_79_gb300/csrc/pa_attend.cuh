@@ -100,7 +100,7 @@ struct AttendWalk {
         it.T = T;
         it.at = at;
         it.seen = seen_by(p, n, T, j);
-        it.tiles = (it.seen + kKeys - 1) / kKeys;
+        it.tiles = (int)(((unsigned int)it.seen + (kKeys - 1)) / kKeys);  // (seen may be next to 2^31)
         it.cost = cost_of(p, n, j, it.seen);
     }
     // The next item of the stream; false behind the last.

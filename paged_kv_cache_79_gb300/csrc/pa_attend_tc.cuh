@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto window = [&](const Item &it, int tile) {
                 const int j = tile * kBlocks + lane;
                 int id = -1;
-                if (j < min((it.seen + B - 1) / B, it.b * kBlocks))
+                if (j < min((int)(((unsigned int)it.seen + (B - 1)) / B), it.b * kBlocks))
                     id = p.block_tables[(size_t)it.s * p.max_blocks + j];
                 return id >= 0 && id < p.num_blocks ? id : p.num_blocks;
             };
@@ -666,9 +666,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const size_t row = (size_t)(it.token0 + my_tok) * p.num_q_heads + it.head0 + head;
             // keys that this row sees, and that every row of the tile sees
             int limit = it.T, common = it.T;
-            if (p.causal) {
-                limit = min(max(it.own + my_tok, 0), it.T);
-                common = min(max(it.own + row0, 0), it.T);
+            if (p.causal) {  // (rows behind the item's tokens may pass 2^31)
+                limit = (int)min(max((long long)it.own + my_tok, 0ll), (long long)it.T);
+                common = (int)min(max((long long)it.own + row0, 0ll), (long long)it.T);
             }
             float m = -INFINITY, l = 0.f;  // the base in use, the sum
             bool far = false;
@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++steps;
                 fence_after();
                 const int key0 = tile * kKeys;
-                const bool masked = key0 + kKeys > common;
+                const bool masked = common - key0 < kKeys;
                 // Exponents of 32 columns: x = s * scale - base, -inf where the key is hidden; their
                 // maximum.  `far`: the product is rounded first.  Behind a large base the exact one
                 // would differ from it by the product's rounding error, which may be large itself.
