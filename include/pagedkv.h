@@ -508,7 +508,7 @@ pa_status pa_scatter_blocks(const void *staging_k, const void *staging_v, void *
  *
  *   q, q_out        device rows of [Hq][d]; strides in elements from one token's row to the
  *                   next, multiples of 16 bytes and at least a row (so q may be part of a
- *                   fused projection's rows).  q_out may be q, with the same stride; it must
+ *                   fused projection's rows); not looked at for one token.  q_out may be q, with the same stride; it must
  *                   not overlap it otherwise.
  *   k, v            device rows of [Hkv][d], likewise with strides
  *   k_out           (pa_rope) rows of [Hkv][d]; may be k with the same stride

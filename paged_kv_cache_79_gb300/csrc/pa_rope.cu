@@ -208,13 +208,15 @@ pa_status rope_impl(RopeParams &p, int block_size, int num_blocks, int dtype, vo
     if (q_row + 2 * k_row > (1ll << 24))
         return PA_ERR_UNSUPPORTED;
     const int per_vec = dtype == PA_F32 ? 4 : 8;
-    // one token has no next row, so its strides may be anything
-    for (const long long s : {p.q_stride, p.q_out_stride, p.k_stride, p.k_out_stride, p.v ? p.v_stride : 0})
-        if (s % per_vec != 0)
+    // (one token has no next row, so its strides may be anything)
+    if (p.num_tokens > 1) {
+        for (const long long s : {p.q_stride, p.q_out_stride, p.k_stride, p.k_out_stride, p.v ? p.v_stride : 0})
+            if (s % per_vec != 0)
+                return PA_ERR_INVALID;
+        if (p.q_stride < q_row || p.q_out_stride < q_row || p.k_stride < k_row || p.k_out_stride < k_row ||
+            (p.v && p.v_stride < k_row))
             return PA_ERR_INVALID;
-    if (p.num_tokens > 1 && (p.q_stride < q_row || p.q_out_stride < q_row || p.k_stride < k_row ||
-                             p.k_out_stride < k_row || (p.v && p.v_stride < k_row)))
-        return PA_ERR_INVALID;
+    }
     for (const void *ptr : {(const void *)p.q, (const void *)p.q_out, (const void *)p.k, (const void *)p.k_out,
                             p.v, (const void *)p.v_out})
         if (!aligned(ptr, 16))
