@@ -379,7 +379,8 @@ pa_status pa_decode_noalloc(void *out, const void *q, const void *k_cache, const
  *                  they were
  *   lse            device fp32 [num_tokens][Hq], or NULL
  *   q              device rows of [Hq][d], q_stride elements from one token's to the next (a
- *                  multiple of 16 bytes, at least Hq * d: q may be part of a fused projection)
+ *                  multiple of 16 bytes, at least Hq * d: q may be part of a fused projection;
+ *                  not looked at for one token)
  *   query_start    device int32 [num_seqs + 1], non-decreasing from 0 to at most num_tokens
  *   others         as pa_decode's; num_q_heads / num_kv_heads may be any size
  *   workspace      device, 16-byte aligned, pa_attend_workspace_size bytes; no initialisation.
@@ -514,7 +515,9 @@ pa_status pa_scatter_blocks(const void *staging_k, const void *staging_v, void *
  *   k_out           (pa_rope) rows of [Hkv][d]; may be k with the same stride
  *   k_cache, v_cache, slot_mapping  (pa_rope_append) as pa_reshape_and_cache's; a slot outside
  *                   [0, num_blocks * block_size) skips the cache, the token's queries are
- *                   turned all the same.  Two tokens with one slot: either's row may land.
+ *                   turned all the same.  Two tokens with one slot: what lands there is
+ *                   undefined, pieces of 32 bytes of either's rows (K's of one, V's of the
+ *                   other among them).
  *   positions       device int32 [num_tokens];  freqs device int64 [rotary_dim / 2]
  *   rotary_dim      a multiple of 16, at most head_dim;  head_dim 64 or 128
  * Errors: PA_ERR_INVALID (null or misaligned pointer, bad size or stride, amplitude not
@@ -740,7 +743,8 @@ pa_status pa_build_tables(int32_t *block_tables, int max_blocks_per_seq, int32_t
  * Deterministic.  Lengths are clamped to [0, max_blocks_per_seq * block_size], *num_free to
  * [0, num_blocks]; table entries outside [0, num_blocks) are copied and counted nowhere; a
  * free-list entry outside is handed out as it is; pushes past num_blocks are dropped.  Nothing
- * is accessed outside the arguments.
+ * is accessed outside the arguments.  Made for batches of up to a few thousand rows: every row
+ * looks through all the parents, once per 1024 entries of its width.
  * Errors: PA_ERR_INVALID (null or misaligned pointer, negative count, non-positive size,
  *   block_tables_out = block_tables, context_lens_out = context_lens, num_blocks or
  *   max_blocks_per_seq * block_size >= 2^31), PA_ERR_UNSUPPORTED (more than 65536 rows or

@@ -150,7 +150,6 @@ pa_status pa_attend(void *out, float *lse, const void *q, long long q_stride, co
         return cuda_fail(e);
     p.wait_ns = wait_limit_ns();
     L.head_dim = head_dim;
-    L.sms = sms;
     // fp32: items of kF32TileRows rows, two CTAs per SM; fp16 and bf16: two tiles of 128 rows, one
     // CTA per SM.  Either way at most two slots of kAttendRows rows per SM.
     const bool f32 = dtype == PA_F32;

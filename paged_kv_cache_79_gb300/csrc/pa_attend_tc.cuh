@@ -3,8 +3,9 @@
 // An item has two tiles of 128 rows (rows: query tokens times heads of a group) that step
 // through the same keys, 128 at a time.  Per CTA, one per SM:
 //   warp 8       loader: per tile of keys one TMA copy for each cache block and 128-byte
-//                column of K, then one for each block of V, into a ring.  Block ids are read a window of 32 ahead, the next item's first ones while this
-//                one's tiles are copied (a read takes longer than a tile when DRAM is busy);
+//                column of K, then one for each block of V, into a ring.  Block ids are read a
+//                window of 32 ahead (a read takes longer than a tile when DRAM is busy), an
+//                item's first ones when the loader comes to it;
 //   warp 10      makes the rows behind the last key that an item sees zeros in V (a weight of
 //                0 times what a stale row holds would be NaN where that is NaN);
 //   warp 9       products, issued by one lane: S = Q K^T into TMEM (operands in shared

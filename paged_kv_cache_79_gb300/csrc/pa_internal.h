@@ -269,7 +269,7 @@ struct AttendParams {
 struct AttendLaunch {
     AttendParams p;
     CUtensorMap map_q, map_k, map_v;
-    int head_dim, sms, ctas;      // ctas: the grid
+    int head_dim, ctas;           // ctas: the grid
 };
 
 // ---- forked tables ---------------------------------------------------------------
