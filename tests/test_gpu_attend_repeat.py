@@ -1,4 +1,4 @@
-"""pa_attend in fp16 and bf16: a row's bits depend on its own query and its sequence's keys alone.
+"""pa_attend: a row's bits depend on its own sequence's queries and keys alone (and on the lengths).
 
 Groups that do not divide a row tile leave rows of it that no query fills; runs shorter than a
 tile leave rows that hold the next sequence's queries or the padding of q.  None of them may
